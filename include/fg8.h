@@ -339,6 +339,166 @@ fg8_status moe_contiguous_layout_fp8(const void* x, int32_t x_is_bf16, int64_t t
  * expert, rounded up to whole 128-row blocks (0 for arguments out of range). */
 int64_t fg8_moe_capacity(int64_t tokens, int32_t topk, int32_t num_experts);
 
+/* ------------------------------------------------------------------------
+ * BF16 products, layer norm and the MoE combine: what an MoE layer computes
+ * around its FP8 products, forward and backward.  bfloat16 values are uint16_t
+ * bit patterns.  ld arguments count elements between rows and let a row be
+ * part of a wider one; pointers are 16-byte aligned as everywhere, and ld of
+ * an operand that a product reads is a multiple of 8 and at most 2^22 (a
+ * larger one is FG8_EUNSUPPORTED).  All sums are FP32, rounded once where the
+ * output is BF16.  Sums run in a fixed order: the same call gives the same
+ * bits.  m, rows or tokens of 0 are valid where a call takes them: nothing is
+ * read, and gradients summed over them are zeros.
+ */
+
+/*
+ * grouped_gemm_bf16: expert products over ragged row runs.  Rows
+ * row_offsets[e] .. row_offsets[e + 1] - 1 of x belong to expert e; runs may
+ * have any length, empty ones included (expert_offsets of
+ * moe_contiguous_layout_fp8 serve, and so do the prefix sums of plain counts).
+ *   y[r][j] = sum_i x[r][i] w[e][j][i]
+ *   x            bf16 [rows][ldx]            w  bf16 [num_experts][n][k]
+ *   row_offsets  int32 [num_experts + 1], device memory, non-decreasing in
+ *                [0, rows]; the kernels clamp each to that range
+ *   y            [rows][ldy] float or bf16; rows before the first and after
+ *                the last run are written as zeros
+ *   k % 8 == 0 (else FG8_EUNSUPPORTED), any n, 0 <= rows < 2^31,
+ *   1 <= num_experts <= 1024.
+ */
+fg8_status grouped_gemm_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w,
+                             const int32_t* row_offsets, void* y, int64_t ldy, fg8_out out,
+                             int64_t rows, int64_t n, int64_t k, int32_t num_experts,
+                             hipStream_t stream);
+
+/*
+ * grouped_gemm_bf16_dgrad: its input gradient, dx[r][i] = sum_j dy[r][j]
+ * w[e][j][i], with the forward pass's weights as they lie.
+ *   dy bf16 [rows][lddy]   dx [rows][lddx] float or bf16 (zeros outside the
+ *   runs)   n % 8 == 0 and k % 8 == 0; the rest as grouped_gemm_bf16.
+ */
+fg8_status grouped_gemm_bf16_dgrad(const uint16_t* dy, int64_t lddy, const uint16_t* w,
+                                   const int32_t* row_offsets, void* dx, int64_t lddx, fg8_out out,
+                                   int64_t rows, int64_t n, int64_t k, int32_t num_experts,
+                                   hipStream_t stream);
+
+/*
+ * grouped_gemm_bf16_wgrad: its weight gradient, dw[e][j][i] = the sum over
+ * expert e's rows of dy[r][j] x[r][i].  Rows of no run (whatever they hold)
+ * and other experts' rows take no part; an empty run's dw is zeros.
+ *   dw [num_experts][n][k] float or bf16, all of it written.
+ *   n % 8 == 0 and k % 8 == 0; the rest as grouped_gemm_bf16.
+ */
+fg8_status grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                                   const int32_t* row_offsets, void* dw, fg8_out out, int64_t rows,
+                                   int64_t n, int64_t k, int32_t num_experts, hipStream_t stream);
+
+typedef enum {
+  FG8_ACT_NONE = 0,
+  FG8_ACT_RELU = 1,
+  FG8_ACT_SILU = 2,   /* z / (1 + e^-z) */
+  FG8_ACT_GELU = 3    /* z (1 + erf(z / sqrt 2)) / 2 */
+} fg8_activation;
+
+/*
+ * gemm_bf16_epilogue: y = act(x w^T + bias) + residual in one kernel.
+ *   x bf16 [m][ldx]   w bf16 [n][k]
+ *   bias      NULL, or [n] float (bias_is_bf16 = 0) or bf16 (1)
+ *   residual  NULL, or bf16 [m][ldr]
+ *   z         NULL, or bf16 [m][n] (output): x w^T + bias, what the backward
+ *             pass takes the activation's slope at
+ *   y         [m][ldy] float or bf16; it may be the residual's memory
+ *   k % 8 == 0 (else FG8_EUNSUPPORTED), any n >= 1, 0 <= m < 2^31.
+ *   workspace: fg8_gemm_bf16_workspace_bytes(m, n, k) bytes (NULL allowed when
+ *   that is 0), under gemm_fp8_blockscaled's rules: zero-filled before its
+ *   first use, not shared by calls that can overlap; one workspace serves both.
+ */
+fg8_status gemm_bf16_epilogue(const uint16_t* x, int64_t ldx, const uint16_t* w, const void* bias,
+                              int32_t bias_is_bf16, fg8_activation activation,
+                              const uint16_t* residual, int64_t ldr, uint16_t* z, void* y,
+                              int64_t ldy, fg8_out out, int64_t m, int64_t n, int64_t k,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t fg8_gemm_bf16_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/*
+ * gemm_bf16_epilogue_backward: the gradients of act(x w^T + bias), from dy (the
+ * residual's gradient is dy itself):
+ *   dz = dy act'(z),  dx = dz w,  dw = dz^T x,  dbias = column sums of dz
+ *   dy bf16 [m][lddy] (any lddy >= n)   z bf16 [m][n] (NULL without activation)
+ *   dx bf16 [m][k], dw [n][k] float or bf16, dbias float [n]: each may be NULL
+ *   and is then not computed (w is needed for dx, x for dw).
+ *   dz is rounded to BF16 for the two products (the matrix units' operand
+ *   type); dbias sums it before that rounding.  relu' (0) = 0.
+ *   k % 8 == 0 (else FG8_EUNSUPPORTED), any n, m >= 1.
+ *   workspace: fg8_gemm_bf16_backward_workspace_bytes(m, n, k) bytes, under
+ *   gemm_bf16_epilogue's rules (it holds dz and partial sums besides).
+ */
+fg8_status gemm_bf16_epilogue_backward(const uint16_t* dy, int64_t lddy, const uint16_t* x,
+                                       int64_t ldx, const uint16_t* w, const uint16_t* z,
+                                       fg8_activation activation, uint16_t* dx, void* dw,
+                                       fg8_out dw_out, float* dbias, int64_t m, int64_t n,
+                                       int64_t k, void* workspace, size_t workspace_bytes,
+                                       hipStream_t stream);
+size_t fg8_gemm_bf16_backward_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/*
+ * layer_norm: y = (x - mean) rstd weight + bias over the last axis, with
+ * rstd = 1 / sqrt(variance + eps) and the variance taken around the mean.
+ *   x [rows][ldx] bf16 (x_is_bf16 = 1) or float (0), any cols and ldx
+ *   weight, bias [cols] bf16 (w_is_bf16 = 1) or float; bias may be NULL
+ *   y [rows][cols] of x's type; mean, rstd float [rows]
+ *   1 <= cols <= 32768 (more is FG8_EUNSUPPORTED), 0 <= rows < 2^31.
+ */
+fg8_status layer_norm(const void* x, int64_t ldx, int32_t x_is_bf16, const void* weight,
+                      const void* bias, int32_t w_is_bf16, float eps, int64_t rows, int64_t cols,
+                      void* y, float* mean, float* rstd, hipStream_t stream);
+
+/*
+ * layer_norm_backward: with g = dy weight and h = (x - mean) rstd,
+ *   dx = rstd (g - mean(g) - h mean(g h)),  dweight = the sum over rows of
+ *   dy h,  dbias = the sum over rows of dy.
+ *   dy [rows][lddy] of x's type; dx [rows][cols] of x's type; dweight, dbias
+ *   float [cols].
+ *   workspace: fg8_layer_norm_backward_workspace_bytes(...) bytes, of any
+ *   contents, not shared by calls that can overlap.
+ */
+fg8_status layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                               int32_t x_is_bf16, const void* weight, int32_t w_is_bf16,
+                               const float* mean, const float* rstd, int64_t rows, int64_t cols,
+                               void* dx, float* dweight, float* dbias, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+size_t fg8_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols, int32_t x_is_bf16);
+
+/*
+ * moe_combine: the step after the second expert product, each token's rows
+ * weighted and summed:
+ *   out[t] = sum_j weights[t][j] y[token_row[t][j]]  (+ residual[t])
+ *   y          [rows][hidden] bf16 (is_bf16 = 1) or float (0)
+ *   token_row  int32 [tokens][topk] as moe_contiguous_layout_fp8 gives it; a
+ *              position outside [0, rows) adds nothing
+ *   weights    float [tokens][topk]
+ *   residual   NULL, or [tokens][hidden] of y's type; out [tokens][hidden] of
+ *              y's type
+ *   hidden % 8 == 0 (else FG8_EUNSUPPORTED), rows >= 1, 1 <= topk <= 256.
+ */
+fg8_status moe_combine(const void* y, int32_t is_bf16, int64_t rows, const int32_t* token_row,
+                       const float* weights, const void* residual, int64_t tokens, int32_t topk,
+                       int64_t hidden, void* out, hipStream_t stream);
+
+/*
+ * moe_combine_backward: its gradients (the residual's is dout itself):
+ *   dy[token_row[t][j]] = weights[t][j] dout[t],  dweights[t][j] = dout[t] .
+ *   y[token_row[t][j]] (0 where token_row lies outside [0, rows)).
+ *   row_token  int32 [rows], token_row's inverse as moe_contiguous_layout_fp8
+ *              gives it: a row whose value lies outside [0, tokens) holds no
+ *              token, and its dy is written as zeros
+ *   dout, dy   of y's type; dy [rows][hidden]; dweights float [tokens][topk].
+ *   A row belongs to one position at most.
+ */
+fg8_status moe_combine_backward(const void* dout, const void* y, int32_t is_bf16, int64_t rows,
+                                const int32_t* token_row, const int32_t* row_token,
+                                const float* weights, int64_t tokens, int32_t topk, int64_t hidden,
+                                void* dy, float* dweights, hipStream_t stream);
+
 /* Diagnostic, host only (no GPU call): the tiling the library picks for a
  * GEMM of this shape on a device with num_cus compute units.  mode: 0 dense
  * (gemm_fp8_blockscaled; m, n, k as there), 1 contiguous (m = m_total),

@@ -7,16 +7,25 @@ has not been built.
 from ._lib import (  # noqa: F401
     Fg8Error,
     fp8_quantize,
+    gemm_bf16_epilogue,
+    gemm_bf16_epilogue_backward,
     gemm_fp8_blockscaled,
     gemm_fp8_blockscaled_noalloc,
     gemm_mxfp8,
     gemm_workspace_bytes,
+    grouped_gemm_bf16,
+    grouped_gemm_bf16_dgrad,
+    grouped_gemm_bf16_wgrad,
     grouped_gemm_fp8_contiguous,
     grouped_gemm_fp8_contiguous_swiglu,
     grouped_gemm_fp8_kgrouped,
     grouped_gemm_fp8_masked,
     grouped_gemm_mxfp8_contiguous,
+    layer_norm,
+    layer_norm_backward,
     moe_capacity,
+    moe_combine,
+    moe_combine_backward,
     moe_contiguous_layout_fp8,
     tile_choice,
     version,

@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_PKG, "libfg8.so")
 FG8_OK, FG8_EINVAL, FG8_EUNSUPPORTED, FG8_EHIP = 0, 1, 2, 3
 OUT_F32, OUT_BF16 = 0, 1
 SCALE_KINDS = {"1x128": 0, "128x128": 1, "mx": 2, "1x128_t": 3}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 _c_i64 = ctypes.c_int64
 _c_i32 = ctypes.c_int32
@@ -45,13 +46,40 @@ _SIGNATURES = {
     "moe_contiguous_layout_fp8": [_c_ptr, _c_i32, _c_i64, _c_i64, _c_ptr, _c_i32, _c_i32, _c_i64,
                                   _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr],
     "fg8_moe_capacity": [_c_i64, _c_i32, _c_i32],
+    "grouped_gemm_bf16": [_c_ptr, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64, ctypes.c_int, _c_i64,
+                          _c_i64, _c_i64, _c_i32, _c_ptr],
+    "grouped_gemm_bf16_dgrad": [_c_ptr, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64, ctypes.c_int,
+                                _c_i64, _c_i64, _c_i64, _c_i32, _c_ptr],
+    "grouped_gemm_bf16_wgrad": [_c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_ptr, ctypes.c_int,
+                                _c_i64, _c_i64, _c_i64, _c_i32, _c_ptr],
+    "gemm_bf16_epilogue": [_c_ptr, _c_i64, _c_ptr, _c_ptr, _c_i32, ctypes.c_int, _c_ptr, _c_i64,
+                           _c_ptr, _c_ptr, _c_i64, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_ptr,
+                           ctypes.c_size_t, _c_ptr],
+    "gemm_bf16_epilogue_backward": [_c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_ptr, ctypes.c_int,
+                                    _c_ptr, _c_ptr, ctypes.c_int, _c_ptr, _c_i64, _c_i64, _c_i64,
+                                    _c_ptr, ctypes.c_size_t, _c_ptr],
+    "fg8_gemm_bf16_workspace_bytes": [_c_i64, _c_i64, _c_i64],
+    "fg8_gemm_bf16_backward_workspace_bytes": [_c_i64, _c_i64, _c_i64],
+    "layer_norm": [_c_ptr, _c_i64, _c_i32, _c_ptr, _c_ptr, _c_i32, ctypes.c_float, _c_i64, _c_i64,
+                   _c_ptr, _c_ptr, _c_ptr, _c_ptr],
+    "layer_norm_backward": [_c_ptr, _c_i64, _c_ptr, _c_i64, _c_i32, _c_ptr, _c_i32, _c_ptr, _c_ptr,
+                            _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, ctypes.c_size_t,
+                            _c_ptr],
+    "fg8_layer_norm_backward_workspace_bytes": [_c_i64, _c_i64, _c_i32],
+    "moe_combine": [_c_ptr, _c_i32, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i32, _c_i64, _c_ptr,
+                    _c_ptr],
+    "moe_combine_backward": [_c_ptr, _c_ptr, _c_i32, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_i32,
+                             _c_i64, _c_ptr, _c_ptr, _c_ptr],
     "fg8_gemm_workspace_bytes": [_c_i64, _c_i64, _c_i64],
     "fg8_tile_choice": [_c_i32, _c_i64, _c_i64, _c_i64, _c_i32, _c_i32, _c_ptr],
     "fg8_last_error": [],
     "fg8_version": [],
 }
 _RESTYPES = {"fg8_gemm_workspace_bytes": ctypes.c_size_t, "fg8_last_error": ctypes.c_char_p,
-             "fg8_moe_capacity": ctypes.c_int64}
+             "fg8_moe_capacity": ctypes.c_int64,
+             "fg8_gemm_bf16_workspace_bytes": ctypes.c_size_t,
+             "fg8_gemm_bf16_backward_workspace_bytes": ctypes.c_size_t,
+             "fg8_layer_norm_backward_workspace_bytes": ctypes.c_size_t}
 
 _lib = None
 _lock = threading.Lock()
@@ -399,3 +427,286 @@ def moe_contiguous_layout_fp8(x, topk_ids, num_experts, m_cap=None, out=None):
         _ptr(out["token_row"]), _ptr(out["expert_offsets"]), _ptr(out["expert_counts"]),
         _stream()))
     return out
+
+
+# ------------------------------------------- BF16 products over ragged runs
+def _rows(t, dtype, name):
+    """Row stride of a 2-D tensor whose rows are contiguous but may be part of
+    wider ones."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    rows, cols = t.shape
+    if rows <= 1:   # (a single row's stride means nothing)
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}'s rows must be contiguous")
+        return -(-cols // 8) * 8
+    ld = t.stride(0)
+    if ld < cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}'s rows must be contiguous and apart")
+    return ld
+
+
+def _out_rows(out, shape, dtype, device, name="out"):
+    """(tensor, row stride, dtype code) of a given or new 2-D output."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device), shape[1], _out_code(dtype)
+    code = _out_code(out.dtype)
+    ld = _rows(out, out.dtype, name)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return out, (ld if out.shape[0] > 1 else shape[1]), code
+
+
+def _experts(w, row_offsets):
+    _dev(w, torch.bfloat16, "w")
+    _dev(row_offsets, torch.int32, "row_offsets")
+    if w.dim() != 3 or row_offsets.shape != (w.shape[0] + 1,):
+        raise ValueError("w must be [E, n, k] and row_offsets [E + 1]")
+    return w.shape
+
+
+def grouped_gemm_bf16(x, w, row_offsets, out_dtype=torch.bfloat16, out=None):
+    """Expert products over ragged row runs: x bf16 [rows, k] (rows may be
+    strided), w bf16 [E, n, k], row_offsets int32 [E + 1] (device), rows
+    row_offsets[e] .. row_offsets[e + 1] - 1 belonging to expert e -> y
+    [rows, n] with y[r] = x[r] w[e]^T; rows of no run are zeros."""
+    E, n, k = _experts(w, row_offsets)
+    ldx = _rows(x, torch.bfloat16, "x")
+    rows = x.shape[0]
+    if x.shape[1] != k:
+        raise ValueError("operand shapes disagree")
+    out, ldy, code = _out_rows(out, (rows, n), out_dtype, x.device)
+    _check(lib().grouped_gemm_bf16(x.data_ptr(), ldx, w.data_ptr(), row_offsets.data_ptr(),
+                                   out.data_ptr(), ldy, code, rows, n, k, E, _stream()))
+    return out
+
+
+def grouped_gemm_bf16_dgrad(dy, w, row_offsets, out_dtype=torch.bfloat16, out=None):
+    """Input gradient of grouped_gemm_bf16: dy bf16 [rows, n], w bf16 [E, n, k]
+    -> dx [rows, k] with dx[r] = dy[r] w[e]; rows of no run are zeros."""
+    E, n, k = _experts(w, row_offsets)
+    lddy = _rows(dy, torch.bfloat16, "dy")
+    rows = dy.shape[0]
+    if dy.shape[1] != n:
+        raise ValueError("operand shapes disagree")
+    out, ldx, code = _out_rows(out, (rows, k), out_dtype, dy.device)
+    _check(lib().grouped_gemm_bf16_dgrad(dy.data_ptr(), lddy, w.data_ptr(), row_offsets.data_ptr(),
+                                         out.data_ptr(), ldx, code, rows, n, k, E, _stream()))
+    return out
+
+
+def grouped_gemm_bf16_wgrad(dy, x, row_offsets, out_dtype=torch.float32, out=None):
+    """Weight gradient of grouped_gemm_bf16: dy bf16 [rows, n], x bf16
+    [rows, k], row_offsets int32 [E + 1] (device) -> dw [E, n, k] with dw[e] =
+    the sum of dy[r]^T x[r] over expert e's rows (zeros for an empty run)."""
+    _dev(row_offsets, torch.int32, "row_offsets")
+    lddy, ldx = _rows(dy, torch.bfloat16, "dy"), _rows(x, torch.bfloat16, "x")
+    rows, n = dy.shape
+    k = x.shape[1]
+    E = row_offsets.numel() - 1
+    if x.shape[0] != rows or row_offsets.dim() != 1 or E < 1:
+        raise ValueError("operand shapes disagree")
+    if out is None:
+        out = torch.empty((E, n, k), dtype=out_dtype, device=dy.device)
+    _dev(out, out.dtype, "out")
+    if out.shape != (E, n, k):
+        raise ValueError("output shape disagrees")
+    _check(lib().grouped_gemm_bf16_wgrad(dy.data_ptr(), lddy, x.data_ptr(), ldx,
+                                         row_offsets.data_ptr(), out.data_ptr(),
+                                         _out_code(out.dtype), rows, n, k, E, _stream()))
+    return out
+
+
+# ------------------------------------------- BF16 product with an epilogue
+def _param(t, cols, name):
+    """(pointer, is bf16) of an optional FP32 or BF16 vector."""
+    if t is None:
+        return None, 0
+    bf16 = t.dtype == torch.bfloat16
+    _dev(t, torch.bfloat16 if bf16 else torch.float32, name)
+    if t.shape != (cols,):
+        raise ValueError(f"{name} must have shape ({cols},)")
+    return t.data_ptr(), int(bf16)
+
+
+def gemm_bf16_epilogue(x, w, bias=None, residual=None, activation="none", save_z=False,
+                       out_dtype=torch.bfloat16, out=None, workspace=None):
+    """y = act(x w^T + bias) + residual in one kernel: x bf16 [m, k], w bf16
+    [n, k], bias float32 or bfloat16 [n], residual bf16 [m, n], activation
+    "none", "relu", "silu" or "gelu" (the erf form).  Returns y, or (y, z) with
+    save_z, z = x w^T + bias in bf16 for the backward pass.  x, residual and
+    out may have strided rows; out may be the residual."""
+    act = ACTIVATIONS[activation]
+    _dev(w, torch.bfloat16, "w")
+    ldx = _rows(x, torch.bfloat16, "x")
+    m, k = x.shape
+    if w.dim() != 2 or w.shape[1] != k:
+        raise ValueError("operand shapes disagree")
+    n = w.shape[0]
+    bias_ptr, bias_bf16 = _param(bias, n, "bias")
+    res_ptr, ldr = None, n
+    if residual is not None:
+        ldr = _rows(residual, torch.bfloat16, "residual")
+        if residual.shape != (m, n):
+            raise ValueError("residual must have the output's shape")
+        res_ptr = residual.data_ptr()
+        if m == 1:
+            ldr = n
+    out, ldy, code = _out_rows(out, (m, n), out_dtype, x.device)
+    z = torch.empty((m, n), dtype=torch.bfloat16, device=x.device) if save_z else None
+    L = lib()
+    ws = workspace
+    if ws is None:
+        ws = _workspace(L.fg8_gemm_bf16_workspace_bytes(m, n, k), x.device)
+    _check(L.gemm_bf16_epilogue(x.data_ptr(), ldx, w.data_ptr(), bias_ptr, bias_bf16, act, res_ptr,
+                                ldr, _ptr(z), out.data_ptr(), ldy, code, m, n, k, _ptr(ws),
+                                0 if ws is None else ws.numel() * ws.element_size(), _stream()))
+    return (out, z) if save_z else out
+
+
+def gemm_bf16_epilogue_backward(dy, x, w, z=None, activation="none", dw_dtype=torch.bfloat16,
+                                needs=(True, True, True), workspace=None):
+    """Gradients of act(x w^T + bias) (the residual's is dy itself): dy bf16
+    [m, n], x bf16 [m, k], w bf16 [n, k], z bf16 [m, n] as saved -> (dx bf16
+    [m, k], dw dw_dtype [n, k], dbias float32 [n]); `needs` leaves out (None)
+    what is not wanted."""
+    act = ACTIVATIONS[activation]
+    _dev(w, torch.bfloat16, "w")
+    lddy, ldx = _rows(dy, torch.bfloat16, "dy"), _rows(x, torch.bfloat16, "x")
+    m, k = x.shape
+    n = w.shape[0]
+    if w.shape != (n, k) or dy.shape != (m, n):
+        raise ValueError("operand shapes disagree")
+    if act:
+        if z is None:
+            raise ValueError("z is needed for the activation's slope")
+        _dev(z, torch.bfloat16, "z")
+        if z.shape != (m, n):
+            raise ValueError("z must have dy's shape")
+    dev = x.device
+    dx = torch.empty((m, k), dtype=torch.bfloat16, device=dev) if needs[0] else None
+    dw = torch.empty((n, k), dtype=dw_dtype, device=dev) if needs[1] else None
+    db = torch.empty((n,), dtype=torch.float32, device=dev) if needs[2] else None
+    L = lib()
+    ws = workspace
+    if ws is None:
+        ws = _workspace(L.fg8_gemm_bf16_backward_workspace_bytes(m, n, k), dev)
+    _check(L.gemm_bf16_epilogue_backward(
+        dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), _ptr(z), act, _ptr(dx), _ptr(dw),
+        _out_code(dw_dtype), _ptr(db), m, n, k, _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream()))
+    return dx, dw, db
+
+
+# --------------------------------------------------------------- layer norm
+def _norm_rows(t, dtype, name):
+    """(rows, cols, row stride) of [..., cols]; more than two dimensions have
+    to be contiguous."""
+    if t.dim() != 2:
+        _dev(t, dtype, name)
+        cols = t.shape[-1]
+        return t.numel() // cols if cols else 0, cols, cols
+    ld = _rows(t, dtype, name)
+    return t.shape[0], t.shape[1], ld if t.shape[0] > 1 else t.shape[1]
+
+
+def _norm_dtype(x):
+    return torch.bfloat16 if x.dtype == torch.bfloat16 else torch.float32
+
+
+def layer_norm(x, weight, bias=None, eps=1e-5):
+    """x float32 or bfloat16 [..., cols] (2-D rows may be strided), weight and
+    bias both float32 or both bfloat16 [cols] -> (y of x's type and shape, mean
+    and rstd float32 [...] for the backward pass)."""
+    dtype = _norm_dtype(x)
+    rows, cols, ldx = _norm_rows(x, dtype, "x")
+    w, w_bf16 = _param(weight, cols, "weight")
+    b, b_bf16 = _param(bias, cols, "bias")
+    if b is not None and b_bf16 != w_bf16:
+        raise TypeError("weight and bias must have one type")
+    y = torch.empty(x.shape, dtype=dtype, device=x.device)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _check(lib().layer_norm(x.data_ptr(), ldx, int(dtype == torch.bfloat16), w, b, w_bf16, eps, rows,
+                            cols, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _stream()))
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd):
+    """dy and x of one type [..., cols], weight [cols], mean and rstd as
+    layer_norm returned them -> (dx of x's type, dweight, dbias float32
+    [cols])."""
+    dtype = _norm_dtype(x)
+    rows, cols, ldx = _norm_rows(x, dtype, "x")
+    _, _, lddy = _norm_rows(dy, dtype, "dy")
+    w, w_bf16 = _param(weight, cols, "weight")
+    _dev(mean, torch.float32, "mean")
+    _dev(rstd, torch.float32, "rstd")
+    if dy.shape != x.shape or mean.shape != x.shape[:-1] or rstd.shape != x.shape[:-1]:
+        raise ValueError("operand shapes disagree")
+    dev = x.device
+    dx = torch.empty(x.shape, dtype=dtype, device=dev)
+    dw = torch.empty((cols,), dtype=torch.float32, device=dev)
+    db = torch.empty((cols,), dtype=torch.float32, device=dev)
+    L = lib()
+    bf16 = int(dtype == torch.bfloat16)
+    need = L.fg8_layer_norm_backward_workspace_bytes(rows, cols, bf16)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _check(L.layer_norm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, bf16, w, w_bf16,
+                                 mean.data_ptr(), rstd.data_ptr(), rows, cols, dx.data_ptr(),
+                                 dw.data_ptr(), db.data_ptr(), _ptr(ws), need, _stream()))
+    return dx, dw, db
+
+
+# -------------------------------------------------------------- MoE combine
+def _combine_args(y, token_row, weights):
+    dtype = _norm_dtype(y)
+    _dev(y, dtype, "y")
+    _dev(token_row, torch.int32, "token_row")
+    _dev(weights, torch.float32, "weights")
+    if y.dim() != 2 or token_row.dim() != 2 or weights.shape != token_row.shape:
+        raise ValueError("y must be [rows, hidden], token_row and weights [tokens, topk]")
+    return dtype, y.shape[0], y.shape[1], token_row.shape[0], token_row.shape[1]
+
+
+def moe_combine(y, token_row, weights, residual=None, out=None):
+    """Each token's expert rows weighted and summed: y float32 or bfloat16
+    [rows, hidden], token_row int32 [tokens, topk] (as
+    moe_contiguous_layout_fp8 returns it; positions outside [0, rows) add
+    nothing), weights float32 [tokens, topk], residual [tokens, hidden] of y's
+    type -> [tokens, hidden] of y's type."""
+    dtype, rows, hidden, tokens, topk = _combine_args(y, token_row, weights)
+    if out is None:
+        out = torch.empty((tokens, hidden), dtype=dtype, device=y.device)
+    for name, t in (("residual", residual), ("out", out)):
+        if t is not None:
+            _dev(t, dtype, name)
+            if t.shape != (tokens, hidden):
+                raise ValueError(f"{name} must have shape ({tokens}, {hidden})")
+    _check(lib().moe_combine(y.data_ptr(), int(dtype == torch.bfloat16), rows, token_row.data_ptr(),
+                             weights.data_ptr(), _ptr(residual), tokens, topk, hidden,
+                             out.data_ptr(), _stream()))
+    return out
+
+
+def moe_combine_backward(dout, y, token_row, row_token, weights):
+    """Gradients of moe_combine (the residual's is dout itself): row_token
+    int32 [rows] is token_row's inverse as moe_contiguous_layout_fp8 returns it
+    -> (dy [rows, hidden] of y's type, zeros in rows that hold no token,
+    dweights float32 [tokens, topk])."""
+    dtype, rows, hidden, tokens, topk = _combine_args(y, token_row, weights)
+    _dev(dout, dtype, "dout")
+    _dev(row_token, torch.int32, "row_token")
+    if dout.shape != (tokens, hidden) or row_token.shape != (rows,):
+        raise ValueError("operand shapes disagree")
+    dy = torch.empty((rows, hidden), dtype=dtype, device=y.device)
+    dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
+    _check(lib().moe_combine_backward(dout.data_ptr(), y.data_ptr(), int(dtype == torch.bfloat16),
+                                      rows, token_row.data_ptr(), row_token.data_ptr(),
+                                      weights.data_ptr(), tokens, topk, hidden, dy.data_ptr(),
+                                      dweights.data_ptr(), _stream()))
+    return dy, dweights

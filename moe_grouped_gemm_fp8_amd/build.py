@@ -9,6 +9,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -35,16 +37,25 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
 
 
-def compile_shared(srcs, out, extra=()):
-    tmp = out + ".tmp"
-    cmd = [HIPCC, *FLAGS, *extra, *srcs, "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+def _hipcc(args, out):
+    r = subprocess.run([HIPCC, *FLAGS, *args], capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError(f"hipcc failed ({r.returncode}) building {out}")
-    noise = [ln for ln in r.stderr.splitlines() if "packed-fp32-ops" not in ln and ln.strip()]
+    noise = [ln for ln in r.stderr.splitlines()
+             if "packed-fp32-ops" not in ln and "unused during compilation" not in ln and ln.strip()]
     if noise:
         sys.stderr.write("\n".join(noise) + "\n")
+
+
+def compile_shared(srcs, out, extra=()):
+    """Each source to an object of its own, side by side, then one link."""
+    tmp = out + ".tmp"
+    with tempfile.TemporaryDirectory() as work:
+        objs = [os.path.join(work, os.path.basename(s) + ".o") for s in srcs]
+        with ThreadPoolExecutor(max_workers=4) as pool:
+            list(pool.map(lambda so: _hipcc([*extra, "-c", so[0], "-o", so[1]], out), zip(srcs, objs)))
+        _hipcc([*objs, "-o", tmp], out)
     os.replace(tmp, out)
     return out
 

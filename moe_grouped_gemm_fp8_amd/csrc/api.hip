@@ -490,3 +490,411 @@ fg8_status moe_contiguous_layout_fp8(const void* x, int32_t x_is_bf16, int64_t t
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// BF16 products, layer norm, MoE combine.
+namespace {
+
+constexpr int64_t kMaxLd = (int64_t)1 << 22;   // 256 rows of a tile in 31-bit byte offsets
+
+#define FG8_CHECK_LD(ld, least, of)                                                              \
+  do {                                                                                           \
+    if ((ld) < (least) || (ld) % (of))                                                           \
+      return fail(FG8_EINVAL, "%s: %s=%lld must be at least %lld and a multiple of %d", fn, #ld, \
+                  (long long)(ld), (long long)(least), (int)(of));                               \
+    if ((ld) > kMaxLd)                                                                           \
+      return fail(FG8_EUNSUPPORTED, "%s: %s=%lld exceeds %lld", fn, #ld, (long long)(ld),        \
+                  (long long)kMaxLd);                                                            \
+  } while (0)
+
+fg8_status check_out(const char* fn, fg8_out out) {
+  if (out != FG8_OUT_F32 && out != FG8_OUT_BF16) return fail(FG8_EINVAL, "%s: bad out", fn);
+  return FG8_OK;
+}
+
+// n and k of a BF16 product whose rows are copied 16 bytes at a time
+fg8_status check_nk(const char* fn, int64_t n, bool n8, int64_t k) {
+  if (n < 1 || k < 1 || n >= kMaxDim || k >= kMaxDim)
+    return fail(FG8_EINVAL, "%s: bad sizes n=%lld k=%lld", fn, (long long)n, (long long)k);
+  if (k % 8 || (n8 && n % 8))
+    return fail(FG8_EUNSUPPORTED, "%s: %s must be a multiple of 8 (n=%lld k=%lld)", fn,
+                n8 ? "n and k" : "k", (long long)n, (long long)k);
+  return FG8_OK;
+}
+
+fg8_status check_runs(const char* fn, int64_t rows, int32_t num_experts) {
+  if (rows < 0 || rows >= kMaxDim) return fail(FG8_EINVAL, "%s: rows=%lld", fn, (long long)rows);
+  if (num_experts < 1 || num_experts > 1024)
+    return fail(FG8_EINVAL, "%s: num_experts=%d must be in [1, 1024]", fn, (int)num_experts);
+  return FG8_OK;
+}
+
+fg8_status run_bf16(const fg8::BfProblem& p, const char* fn, hipStream_t stream) {
+  const fg8::BfTile t = fg8::bf16_tile(p, fg8::device_cu_count());
+  const int64_t runs = p.mode == fg8::kBfKRuns ? p.groups : t.splits;
+  const int64_t mt = ((int64_t)p.M + t.bm - 1) / t.bm + (p.mode == fg8::kBfRowRuns ? p.groups + 1 : 0);
+  if (mt * (((int64_t)p.N + t.bn - 1) / t.bn) * runs >= INT32_MAX - 8)
+    return fail(FG8_EUNSUPPORTED, "%s: too many tiles for a 32-bit count", fn);
+  const hipError_t e = fg8::launch_bf16(p, t, stream);
+  if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  g_err[0] = 0;
+  return FG8_OK;
+}
+
+fg8::BfProblem dense_bf16(int64_t m, int64_t n, int64_t k, bool a_kmajor, bool b_kmajor) {
+  fg8::BfProblem p{};
+  p.mode = fg8::kBfDense;
+  p.M = (int)m; p.N = (int)n; p.K = (int)k;
+  p.a_kmajor = a_kmajor; p.b_kmajor = b_kmajor;
+  p.groups = 1; p.splits = 1;
+  return p;
+}
+
+// The workspace of a dense product: arrival counters, then partial tiles.
+fg8_status set_workspace(fg8::BfProblem& p, const char* fn, void* ws, size_t bytes, size_t need) {
+  if (need == 0) return FG8_OK;
+  if (!ws || bytes < need)
+    return fail(FG8_EINVAL, "%s: workspace of %zu bytes needed, %zu given", fn, need, ws ? bytes : (size_t)0);
+  if (!aligned16(ws)) return fail(FG8_EINVAL, "%s: workspace misaligned", fn);
+  p.counters = (int32_t*)ws;
+  p.partial = (float*)((char*)ws + fg8::kSplitKCounterBytes);
+  return FG8_OK;
+}
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// gemm_bf16_epilogue_backward's workspace: counters and the larger of its two
+// products' partial tiles, then dz, then the column sums' partials.
+struct BackwardSpace {
+  size_t products, dz, sums, total;
+  int64_t ldz;
+};
+BackwardSpace backward_space(int64_t m, int64_t n, int64_t k) {
+  const int cus = fg8::device_cu_count();
+  BackwardSpace s{};
+  const size_t dx = fg8::bf16_workspace_bytes(dense_bf16(m, k, n, false, true), cus);
+  const size_t dw = fg8::bf16_workspace_bytes(dense_bf16(n, k, m, true, true), cus);
+  // (the counters keep their place at the front whatever the shape: another
+  // call on the same workspace finds them at zero)
+  s.products = fg8::kSplitKCounterBytes;
+  if (dx > s.products) s.products = dx;
+  if (dw > s.products) s.products = dw;
+  s.ldz = up(n, 8);
+  s.dz = s.products;
+  s.sums = s.dz + (size_t)up(m * s.ldz * 2, 16);
+  s.total = s.sums + (size_t)fg8::act_backward_chunks(m, n) * n * 4;
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+fg8_status grouped_gemm_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w,
+                             const int32_t* row_offsets, void* y, int64_t ldy, fg8_out out,
+                             int64_t rows, int64_t n, int64_t k, int32_t num_experts,
+                             hipStream_t stream) {
+  const char* fn = "grouped_gemm_bf16";
+  if (fg8_status s = check_runs(fn, rows, num_experts)) return s;
+  if (fg8_status s = check_nk(fn, n, false, k)) return s;
+  if (fg8_status s = check_out(fn, out)) return s;
+  if (rows == 0) return FG8_OK;
+  FG8_CHECK_PTR(x);
+  FG8_CHECK_PTR(w);
+  FG8_CHECK_PTR(row_offsets);
+  FG8_CHECK_PTR(y);
+  FG8_CHECK_LD(ldx, k, 8);
+  FG8_CHECK_LD(ldy, n, 1);
+  FG8_CHECK_LD(k, 1, 1);
+  fg8::BfProblem p = dense_bf16(rows, n, k, false, false);
+  p.mode = fg8::kBfRowRuns;
+  p.a = x; p.lda = ldx; p.b = w; p.ldb = k; p.b_stride = n * k; p.d = y; p.ldd = ldy;
+  p.out_bf16 = out == FG8_OUT_BF16;
+  p.groups = num_experts; p.offsets = row_offsets;
+  return run_bf16(p, fn, stream);
+}
+
+fg8_status grouped_gemm_bf16_dgrad(const uint16_t* dy, int64_t lddy, const uint16_t* w,
+                                   const int32_t* row_offsets, void* dx, int64_t lddx, fg8_out out,
+                                   int64_t rows, int64_t n, int64_t k, int32_t num_experts,
+                                   hipStream_t stream) {
+  const char* fn = "grouped_gemm_bf16_dgrad";
+  if (fg8_status s = check_runs(fn, rows, num_experts)) return s;
+  if (fg8_status s = check_nk(fn, n, true, k)) return s;
+  if (fg8_status s = check_out(fn, out)) return s;
+  if (rows == 0) return FG8_OK;
+  FG8_CHECK_PTR(dy);
+  FG8_CHECK_PTR(w);
+  FG8_CHECK_PTR(row_offsets);
+  FG8_CHECK_PTR(dx);
+  FG8_CHECK_LD(lddy, n, 8);
+  FG8_CHECK_LD(lddx, k, 1);
+  FG8_CHECK_LD(k, 1, 1);
+  fg8::BfProblem p = dense_bf16(rows, k, n, false, true);
+  p.mode = fg8::kBfRowRuns;
+  p.a = dy; p.lda = lddy; p.b = w; p.ldb = k; p.b_stride = n * k; p.d = dx; p.ldd = lddx;
+  p.out_bf16 = out == FG8_OUT_BF16;
+  p.groups = num_experts; p.offsets = row_offsets;
+  return run_bf16(p, fn, stream);
+}
+
+fg8_status grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                                   const int32_t* row_offsets, void* dw, fg8_out out, int64_t rows,
+                                   int64_t n, int64_t k, int32_t num_experts, hipStream_t stream) {
+  const char* fn = "grouped_gemm_bf16_wgrad";
+  if (fg8_status s = check_runs(fn, rows, num_experts)) return s;
+  if (fg8_status s = check_nk(fn, n, true, k)) return s;
+  if (fg8_status s = check_out(fn, out)) return s;
+  if (rows > 0) {   // (without rows dw is all zeros and nothing is read)
+    FG8_CHECK_PTR(dy);
+    FG8_CHECK_PTR(x);
+  }
+  FG8_CHECK_PTR(row_offsets);
+  FG8_CHECK_PTR(dw);
+  FG8_CHECK_LD(lddy, n, 8);
+  FG8_CHECK_LD(ldx, k, 8);
+  fg8::BfProblem p = dense_bf16(n, k, rows, true, true);
+  p.mode = fg8::kBfKRuns;
+  p.a = dy; p.lda = lddy; p.b = x; p.ldb = ldx; p.d = dw; p.ldd = k; p.d_stride = n * k;
+  p.out_bf16 = out == FG8_OUT_BF16;
+  p.groups = num_experts; p.offsets = row_offsets;
+  return run_bf16(p, fn, stream);
+}
+
+size_t fg8_gemm_bf16_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m < 1 || n < 1 || k < 1 || m >= kMaxDim || n >= kMaxDim || k >= kMaxDim) return 0;
+  return fg8::bf16_workspace_bytes(dense_bf16(m, n, k, false, false), fg8::device_cu_count());
+}
+
+fg8_status gemm_bf16_epilogue(const uint16_t* x, int64_t ldx, const uint16_t* w, const void* bias,
+                              int32_t bias_is_bf16, fg8_activation activation,
+                              const uint16_t* residual, int64_t ldr, uint16_t* z, void* y,
+                              int64_t ldy, fg8_out out, int64_t m, int64_t n, int64_t k,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const char* fn = "gemm_bf16_epilogue";
+  if (m < 0 || m >= kMaxDim) return fail(FG8_EINVAL, "%s: m=%lld", fn, (long long)m);
+  if (fg8_status s = check_nk(fn, n, false, k)) return s;
+  if (fg8_status s = check_out(fn, out)) return s;
+  if ((int)activation < FG8_ACT_NONE || (int)activation > FG8_ACT_GELU)
+    return fail(FG8_EINVAL, "%s: unknown activation %d", fn, (int)activation);
+  if (bias_is_bf16 != 0 && bias_is_bf16 != 1) return fail(FG8_EINVAL, "%s: bias_is_bf16=%d", fn, (int)bias_is_bf16);
+  if (m == 0) return FG8_OK;
+  FG8_CHECK_PTR(x);
+  FG8_CHECK_PTR(w);
+  FG8_CHECK_PTR(y);
+  if (bias) FG8_CHECK_PTR(bias);
+  if (z) FG8_CHECK_PTR(z);
+  FG8_CHECK_LD(ldx, k, 8);
+  FG8_CHECK_LD(ldy, n, 1);
+  FG8_CHECK_LD(k, 1, 1);
+  if (residual) {
+    FG8_CHECK_PTR(residual);
+    FG8_CHECK_LD(ldr, n, 1);
+  }
+  fg8::BfProblem p = dense_bf16(m, n, k, false, false);
+  p.a = x; p.lda = ldx; p.b = w; p.ldb = k; p.d = y; p.ldd = ldy;
+  p.out_bf16 = out == FG8_OUT_BF16;
+  p.bias = bias; p.bias_bf16 = bias_is_bf16; p.act = (int)activation;
+  p.residual = residual; p.ldr = ldr; p.z = z; p.ldz = n;
+  if (fg8_status s = set_workspace(p, fn, workspace, workspace_bytes,
+                                   fg8::bf16_workspace_bytes(p, fg8::device_cu_count())))
+    return s;
+  return run_bf16(p, fn, stream);
+}
+
+size_t fg8_gemm_bf16_backward_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m < 1 || n < 1 || k < 1 || m >= kMaxDim || n >= kMaxDim || k >= kMaxDim) return 0;
+  return backward_space(m, n, k).total;
+}
+
+fg8_status gemm_bf16_epilogue_backward(const uint16_t* dy, int64_t lddy, const uint16_t* x,
+                                       int64_t ldx, const uint16_t* w, const uint16_t* z,
+                                       fg8_activation activation, uint16_t* dx, void* dw,
+                                       fg8_out dw_out, float* dbias, int64_t m, int64_t n,
+                                       int64_t k, void* workspace, size_t workspace_bytes,
+                                       hipStream_t stream) {
+  const char* fn = "gemm_bf16_epilogue_backward";
+  if (m < 1 || m >= kMaxDim) return fail(FG8_EINVAL, "%s: m=%lld", fn, (long long)m);
+  if (fg8_status s = check_nk(fn, n, false, k)) return s;
+  if (fg8_status s = check_out(fn, dw_out)) return s;
+  if ((int)activation < FG8_ACT_NONE || (int)activation > FG8_ACT_GELU)
+    return fail(FG8_EINVAL, "%s: unknown activation %d", fn, (int)activation);
+  FG8_CHECK_PTR(dy);
+  FG8_CHECK_LD(lddy, n, 1);
+  FG8_CHECK_LD(k, 1, 1);
+  FG8_CHECK_LD(n, 1, 1);
+  if (activation != FG8_ACT_NONE) FG8_CHECK_PTR(z);
+  if (dx) {
+    FG8_CHECK_PTR(dx);
+    FG8_CHECK_PTR(w);
+  }
+  if (dw) {
+    FG8_CHECK_PTR(dw);
+    FG8_CHECK_PTR(x);
+    FG8_CHECK_LD(ldx, k, 8);
+  }
+  if (dbias) FG8_CHECK_PTR(dbias);
+  if (!dx && !dw && !dbias) return fail(FG8_EINVAL, "%s: no output", fn);
+  // dz is dy itself where there is no activation and its rows can be copied
+  // 16 bytes at a time
+  const bool needs_dz = activation != FG8_ACT_NONE || n % 8 || lddy % 8;
+  const BackwardSpace here = backward_space(m, n, k);
+  fg8::BfProblem p = dense_bf16(m, k, n, false, true);
+  if (fg8_status e = set_workspace(p, fn, workspace, workspace_bytes, here.total)) return e;
+  uint16_t* dz = needs_dz ? (uint16_t*)((char*)workspace + here.dz) : nullptr;
+  if (needs_dz || dbias) {
+    const hipError_t e = fg8::launch_act_backward(dy, lddy, z, n, (int)activation, m, n, dz, here.ldz,
+                                                  (float*)((char*)workspace + here.sums), dbias, stream);
+    if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  }
+  const uint16_t* g = needs_dz ? dz : dy;
+  const int64_t ldg = needs_dz ? here.ldz : lddy;
+  if (dx) {
+    p.a = g; p.lda = ldg; p.b = w; p.ldb = k; p.d = dx; p.ldd = k; p.out_bf16 = 1;
+    if (fg8_status e = run_bf16(p, fn, stream)) return e;
+  }
+  if (dw) {
+    fg8::BfProblem q = dense_bf16(n, k, m, true, true);
+    q.counters = p.counters; q.partial = p.partial;
+    q.a = g; q.lda = ldg; q.b = x; q.ldb = ldx; q.d = dw; q.ldd = k;
+    q.out_bf16 = dw_out == FG8_OUT_BF16;
+    if (fg8_status e = run_bf16(q, fn, stream)) return e;
+  }
+  g_err[0] = 0;
+  return FG8_OK;
+}
+
+namespace {
+
+constexpr int64_t kMaxNormCols = 32768;
+
+fg8_status check_norm(const char* fn, int64_t rows, int64_t cols, int32_t x_is_bf16, int32_t w_is_bf16) {
+  if (rows < 0 || rows >= kMaxDim || cols < 1)
+    return fail(FG8_EINVAL, "%s: bad sizes rows=%lld cols=%lld", fn, (long long)rows, (long long)cols);
+  if ((x_is_bf16 != 0 && x_is_bf16 != 1) || (w_is_bf16 != 0 && w_is_bf16 != 1))
+    return fail(FG8_EINVAL, "%s: x_is_bf16=%d w_is_bf16=%d must be 0 or 1", fn, (int)x_is_bf16, (int)w_is_bf16);
+  if (cols > kMaxNormCols)
+    return fail(FG8_EUNSUPPORTED, "%s: cols=%lld exceeds %lld", fn, (long long)cols, (long long)kMaxNormCols);
+  return FG8_OK;
+}
+
+}  // namespace
+
+fg8_status layer_norm(const void* x, int64_t ldx, int32_t x_is_bf16, const void* weight,
+                      const void* bias, int32_t w_is_bf16, float eps, int64_t rows, int64_t cols,
+                      void* y, float* mean, float* rstd, hipStream_t stream) {
+  const char* fn = "layer_norm";
+  if (fg8_status s = check_norm(fn, rows, cols, x_is_bf16, w_is_bf16)) return s;
+  if (!(eps >= 0.f)) return fail(FG8_EINVAL, "%s: eps=%g", fn, (double)eps);
+  if (rows == 0) return FG8_OK;
+  FG8_CHECK_PTR(x);
+  FG8_CHECK_PTR(weight);
+  if (bias) FG8_CHECK_PTR(bias);
+  FG8_CHECK_PTR(y);
+  FG8_CHECK_PTR(mean);
+  FG8_CHECK_PTR(rstd);
+  FG8_CHECK_LD(ldx, cols, 1);
+  const hipError_t e = fg8::launch_layer_norm(x, ldx, x_is_bf16 == 1, weight, bias, w_is_bf16 == 1, eps,
+                                              rows, cols, y, mean, rstd, fg8::device_cu_count(), stream);
+  if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  g_err[0] = 0;
+  return FG8_OK;
+}
+
+size_t fg8_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols, int32_t x_is_bf16) {
+  if (rows < 1 || rows >= kMaxDim || cols < 1 || cols > kMaxNormCols) return 0;
+  return (size_t)fg8::layer_norm_teams(rows, cols, x_is_bf16 == 1, fg8::device_cu_count()) * 2 * cols * 4;
+}
+
+fg8_status layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                               int32_t x_is_bf16, const void* weight, int32_t w_is_bf16,
+                               const float* mean, const float* rstd, int64_t rows, int64_t cols,
+                               void* dx, float* dweight, float* dbias, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream) {
+  const char* fn = "layer_norm_backward";
+  if (fg8_status s = check_norm(fn, rows, cols, x_is_bf16, w_is_bf16)) return s;
+  if (rows > 0) {   // (without rows both parameters' gradients are zeros)
+    FG8_CHECK_PTR(dy);
+    FG8_CHECK_PTR(x);
+    FG8_CHECK_PTR(mean);
+    FG8_CHECK_PTR(rstd);
+    FG8_CHECK_PTR(dx);
+  }
+  FG8_CHECK_PTR(weight);
+  FG8_CHECK_PTR(dweight);
+  FG8_CHECK_PTR(dbias);
+  FG8_CHECK_LD(ldx, cols, 1);
+  FG8_CHECK_LD(lddy, cols, 1);
+  const size_t need = fg8_layer_norm_backward_workspace_bytes(rows, cols, x_is_bf16);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need)
+      return fail(FG8_EINVAL, "%s: workspace of %zu bytes needed, %zu given", fn, need,
+                  workspace ? workspace_bytes : (size_t)0);
+    if (!aligned16(workspace)) return fail(FG8_EINVAL, "%s: workspace misaligned", fn);
+  }
+  const hipError_t e = fg8::launch_layer_norm_backward(dy, lddy, x, ldx, x_is_bf16 == 1, weight, w_is_bf16 == 1,
+                                                       mean, rstd, rows, cols, dx, dweight, dbias,
+                                                       (float*)workspace, fg8::device_cu_count(), stream);
+  if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  g_err[0] = 0;
+  return FG8_OK;
+}
+
+namespace {
+
+fg8_status check_combine(const char* fn, int32_t is_bf16, int64_t rows, int64_t tokens, int32_t topk,
+                         int64_t hidden) {
+  if (is_bf16 != 0 && is_bf16 != 1) return fail(FG8_EINVAL, "%s: is_bf16=%d must be 0 or 1", fn, (int)is_bf16);
+  if (rows < 1 || rows >= kMaxDim || tokens < 0 || hidden < 1 || hidden >= kMaxDim)
+    return fail(FG8_EINVAL, "%s: bad sizes rows=%lld tokens=%lld hidden=%lld", fn, (long long)rows,
+                (long long)tokens, (long long)hidden);
+  if (topk < 1 || topk > 256) return fail(FG8_EINVAL, "%s: topk=%d must be in [1, 256]", fn, (int)topk);
+  if (hidden % 8) return fail(FG8_EUNSUPPORTED, "%s: hidden=%lld is not a multiple of 8", fn, (long long)hidden);
+  if (tokens * ((hidden + 255) / 256) >= kMaxDim || tokens + rows >= kMaxDim)
+    return fail(FG8_EUNSUPPORTED, "%s: too many tokens", fn);
+  return FG8_OK;
+}
+
+}  // namespace
+
+fg8_status moe_combine(const void* y, int32_t is_bf16, int64_t rows, const int32_t* token_row,
+                       const float* weights, const void* residual, int64_t tokens, int32_t topk,
+                       int64_t hidden, void* out, hipStream_t stream) {
+  const char* fn = "moe_combine";
+  if (fg8_status s = check_combine(fn, is_bf16, rows, tokens, topk, hidden)) return s;
+  if (tokens == 0) return FG8_OK;
+  FG8_CHECK_PTR(y);
+  FG8_CHECK_PTR(token_row);
+  FG8_CHECK_PTR(weights);
+  if (residual) FG8_CHECK_PTR(residual);
+  FG8_CHECK_PTR(out);
+  const hipError_t e = fg8::launch_combine(y, is_bf16 == 1, rows, token_row, weights, residual, tokens,
+                                           topk, hidden, out, stream);
+  if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  g_err[0] = 0;
+  return FG8_OK;
+}
+
+fg8_status moe_combine_backward(const void* dout, const void* y, int32_t is_bf16, int64_t rows,
+                                const int32_t* token_row, const int32_t* row_token,
+                                const float* weights, int64_t tokens, int32_t topk, int64_t hidden,
+                                void* dy, float* dweights, hipStream_t stream) {
+  const char* fn = "moe_combine_backward";
+  if (fg8_status s = check_combine(fn, is_bf16, rows, tokens, topk, hidden)) return s;
+  if (tokens > 0) {   // (without tokens every row's gradient is zeros)
+    FG8_CHECK_PTR(dout);
+    FG8_CHECK_PTR(token_row);
+    FG8_CHECK_PTR(weights);
+    FG8_CHECK_PTR(dweights);
+  }
+  FG8_CHECK_PTR(y);
+  FG8_CHECK_PTR(row_token);
+  FG8_CHECK_PTR(dy);
+  const hipError_t e = fg8::launch_combine_backward(dout, y, is_bf16 == 1, rows, token_row, row_token, weights,
+                                                    tokens, topk, hidden, dy, dweights, stream);
+  if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  g_err[0] = 0;
+  return FG8_OK;
+}
+
+}  // extern "C"

@@ -80,4 +80,71 @@ hipError_t launch_route_quantize(const void* x, bool bf16, int64_t tokens, int64
 
 int device_cu_count();
 
+// ---------------------------------------------------------- BF16 products
+// kBfDense: one product.  kBfRowRuns: D's rows (and A's) in runs by
+// `offsets`, each with its own B.  kBfKRuns: k in runs, each with its own D.
+enum BfMode : int { kBfDense = 0, kBfRowRuns = 1, kBfKRuns = 2 };
+enum BfAct : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+
+struct BfProblem {
+  const uint16_t* a;            // [M][K], or [K][M] if a_kmajor
+  const uint16_t* b;            // [N][K], or [K][N] if b_kmajor
+  void* d;                      // [M][N]
+  int64_t lda, ldb, ldd;        // elements between memory rows
+  int64_t b_stride, d_stride;   // elements between experts (row runs: b, k runs: d)
+  int M, N, K;
+  int a_kmajor, b_kmajor;
+  int out_bf16;
+  int mode;
+  int groups;
+  const int32_t* offsets;       // [groups + 1]
+  // epilogue (dense)
+  const void* bias;
+  int bias_bf16;
+  int act;
+  const uint16_t* residual;
+  int64_t ldr;
+  uint16_t* z;                  // the value before the activation, BF16
+  int64_t ldz;
+  // split k (dense)
+  int splits;
+  float* partial;
+  int32_t* counters;
+};
+struct BfTile {
+  int cfg, bm, bn, splits;
+};
+constexpr int kBfMaxSplits = 16;
+BfTile bf16_tile(const BfProblem& p, int num_cus);
+size_t bf16_workspace_bytes(const BfProblem& p, int num_cus);
+hipError_t launch_bf16(BfProblem p, const BfTile& t, hipStream_t stream);
+
+// dz = dy * act'(z) in BF16 (row stride ldz, zeros from column n up to it) and
+// its column sums, by `chunks` row ranges in partial [chunks][n], then in
+// dbias [n]; either result may be left out (NULL).
+int act_backward_chunks(int64_t m, int64_t n);
+hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldzin,
+                               int act, int64_t m, int64_t n, uint16_t* dz, int64_t ldz,
+                               float* partial, float* dbias, hipStream_t stream);
+
+// --------------------------------------------------------------- layer norm
+int64_t layer_norm_teams(int64_t rows, int64_t cols, bool bf16, int num_cus);
+hipError_t launch_layer_norm(const void* x, int64_t ldx, bool bf16, const void* weight,
+                             const void* bias, bool w_bf16, float eps, int64_t rows, int64_t cols,
+                             void* y, float* mean, float* rstd, int num_cus, hipStream_t stream);
+hipError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                      bool bf16, const void* weight, bool w_bf16,
+                                      const float* mean, const float* rstd, int64_t rows,
+                                      int64_t cols, void* dx, float* dweight, float* dbias,
+                                      float* partial, int num_cus, hipStream_t stream);
+
+// -------------------------------------------------------------- MoE combine
+hipError_t launch_combine(const void* y, bool bf16, int64_t rows, const int32_t* token_row,
+                          const float* weights, const void* residual, int64_t tokens, int topk,
+                          int64_t hidden, void* out, hipStream_t stream);
+hipError_t launch_combine_backward(const void* dout, const void* y, bool bf16, int64_t rows,
+                                   const int32_t* token_row, const int32_t* row_token,
+                                   const float* weights, int64_t tokens, int topk, int64_t hidden,
+                                   void* dy, float* dweights, hipStream_t stream);
+
 }  // namespace fg8

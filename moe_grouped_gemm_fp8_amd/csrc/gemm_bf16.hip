@@ -1,0 +1,521 @@
+// BF16 products for gfx950: the expert products over ragged row runs
+// (forward, input gradient, weight gradient) and the dense product with bias,
+// activation and residual in its epilogue.
+//
+// Every one is D[m][n] = sum_k A(m, k) B(n, k) with BF16 operands, FP32
+// accumulators and one rounding at the end; they differ in how the operands
+// lie in memory and in where a tile's rows, columns and k range come from:
+//   dense           A [M][K], B [N][K]            y  = x W^T
+//   dense, B by k   A [M][K], B [K][N]            dx = dz W
+//   dense, both     A [K][M], B [K][N]            dW = dz^T x
+//   row runs        the same first two, rows off[e] .. off[e + 1] - 1 of A and
+//                   D belonging to expert e, whose B is b + e * b_stride
+//   k runs          the third, k (a token row) off[e] .. off[e + 1] - 1
+//                   belonging to expert e, whose D is d + e * d_stride
+//
+// An operand tile of one 64-deep k step is copied from global memory straight
+// into LDS (16 bytes a lane, no staging registers).  The copies go through a
+// buffer resource that ends where the operand's run ends, so rows past a
+// ragged end arrive as zeros: for the k runs that is what keeps one expert's
+// rows (whatever they hold, NaN included) out of another expert's sum.
+//   k-contiguous operand: LDS [row][64 k], 128-byte rows, 16-byte chunk index
+//     XOR (row >> 1) & 7; a fragment is one ds_read_b128 a lane.
+//   k-major operand: LDS [64 k][cols], 32-byte granule index XOR a function of
+//     k; a fragment is two ds_read_b64_tr_b16, which hand lane i of a 16-lane
+//     group column i of a 4 x 16 block.  Eight rows of a half wave's read fall
+//     on eight granules, so neither read has bank conflicts.
+// MFMA 16x16x32: lane i + 16 g holds row i, k = 8 g .. 8 g + 7 of either
+// operand; result register v of that lane is row 4 g + v, column i.  B goes in
+// as the first operand, so a lane holds four consecutive columns n of one row.
+#include "fg8_device.h"
+#include "fg8_internal.h"
+
+namespace fg8 {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
+constexpr int kBK = 64;                       // k depth of one step
+constexpr uint32_t kNowhere = 0x80000000u;    // an offset past every buffer resource
+
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, int OCC_>
+struct BfCfg {
+  static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
+  static constexpr int STAGES = STAGES_, OCC = OCC_;
+  static constexpr int WAVES = WAVES_M * WAVES_N, THREADS = 64 * WAVES;
+  static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 16, TN = WN / 16;
+  static constexpr int A_BYTES = BM * kBK * 2, B_BYTES = BN * kBK * 2;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static_assert(WM % 16 == 0 && WN % 16 == 0 && STAGES >= 2, "whole MFMA tiles, two stages");
+  static_assert(STAGES * STAGE_BYTES <= 160 * 1024, "LDS of a CU");
+};
+
+// A copy of 16 bytes a lane into LDS at `lds` + 16 * lane.  The instruction
+// writes no VGPR; the wait state between the write of m0 and its use is ours
+// to keep inside an asm block.
+__device__ __forceinline__ void copy16(v4i rsrc, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(off), "s"(rsrc), "s"(lds)
+               : "memory", "m0");
+}
+
+__device__ __forceinline__ v4i resource(const void* base, int64_t bytes) {
+  const uint64_t a = uniform((uint64_t)base);
+  const int n = uniform((int)(bytes < 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : bytes));
+  return v4i{(int)(uint32_t)a, (int)((uint32_t)(a >> 32) & 0xffffu), n, kBufferDword3};
+}
+
+// One operand's tile: BX rows (m or n) by 64 k.  KMAJOR: memory is [k][x].
+template <bool KMAJOR, int BX, int WAVES>
+struct Operand {
+  static constexpr int BYTES = BX * kBK * 2;
+  static constexpr int COPIES = BYTES / 1024;                     // of a wave's 1 KB
+  static constexpr int PER = (COPIES + WAVES - 1) / WAVES;        // per wave (the last may be short)
+  static constexpr bool EVEN = COPIES % WAVES == 0;
+  static constexpr int PITCH = KMAJOR ? BX * 2 : kBK * 2;         // bytes of an LDS row
+  static_assert(!KMAJOR || BX >= 64, "a k-major tile is 64 columns at least");
+
+  const char* base;      // the tile's first element at the first k of the run
+  int64_t ld;            // bytes between memory rows
+  int64_t left;          // k-contiguous: bytes of the rows before the last one; k-major: bytes of a row
+  uint32_t off[PER];     // this lane's source of each copy, from base
+  int rem_k;             // k elements of the run
+
+  // XOR of the 32-byte granules of k-major row k
+  __device__ static int gran(int k) {
+    return BX >= 128 ? (k & 3) | ((k >> 3 & 1) << 2) : (k >> 1 & 1) | ((k >> 3 & 1) << 1);
+  }
+
+  // A memory row is whole 16-byte chunks: dz's rows end in zeros up to one, the
+  // row length of every other operand is a multiple of 8.
+  // x0: the tile's first row (m or n); xs: rows of the operand from there
+  // (>= 1); k0, ks: the run's first k and its length
+  __device__ void init(const uint16_t* p, int64_t ld_elems, int64_t x0, int xs, int64_t k0, int ks,
+                       int wave, int lane) {
+    ld = ld_elems * 2;
+    rem_k = ks;
+    if constexpr (KMAJOR) {
+      base = (const char*)(p + k0 * ld_elems + x0);
+      left = (int64_t)((xs < BX ? xs + 7 : BX) & ~7) * 2;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int at = (wave + i * WAVES) * 1024 + lane * 16;      // byte of the LDS tile
+        const int k = at / PITCH, c = (at % PITCH / 16) ^ (gran(k) << 1);
+        off[i] = c * 8 < xs ? (uint32_t)(k * ld) + c * 16 : kNowhere;
+      }
+    } else {
+      base = (const char*)(p + x0 * ld_elems + k0);
+      left = (int64_t)((xs < BX ? xs : BX) - 1) * ld;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int at = (wave + i * WAVES) * 1024 + lane * 16;
+        const int r = at / PITCH, c = (at % PITCH / 16) ^ swz(r);
+        off[i] = (uint32_t)(r * ld) + c * 16;
+      }
+    }
+  }
+
+  // the copies of k step kt into the LDS tile at `lds`
+  __device__ void issue(int kt, uint32_t lds, int wave, int lane) const {
+    const int rem = rem_k - kt * kBK;     // k elements from this step on (> 0)
+    if constexpr (KMAJOR) {
+      const v4i rs = resource(base + (int64_t)kt * kBK * ld, (int64_t)(rem - 1) * ld + left);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (EVEN || wave + i * WAVES < COPIES)
+          copy16(rs, off[i], uniform(lds + (uint32_t)(wave + i * WAVES) * 1024));
+    } else {
+      const v4i rs = resource(base + (int64_t)kt * (kBK * 2), left + (int64_t)((rem + 7) & ~7) * 2);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (EVEN || wave + i * WAVES < COPIES) {
+          // chunks at or past the end of k are zeros (K is a multiple of 8)
+          const int at = (wave + i * WAVES) * 1024 + lane * 16;
+          const int c = (at % PITCH / 16) ^ swz(at / PITCH);
+          copy16(rs, c * 8 < rem ? off[i] : kNowhere, uniform(lds + (uint32_t)(wave + i * WAVES) * 1024));
+        }
+    }
+  }
+
+  // fragment of rows x .. x + 15, k = 32 kk .. 32 kk + 31
+  __device__ static v8bf frag(const uint8_t* tile, int x, int kk, int lane) {
+    const int i = lane & 15, g = lane >> 4;
+    if constexpr (KMAJOR) {
+      const int k = kk * 32 + 8 * g + (i >> 2);
+      const uint8_t* p = tile + k * PITCH + (((x >> 4) ^ gran(k)) << 5) + (i & 3) * 8;
+      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
+      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * PITCH));
+      return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const int r = x + i;
+      return *reinterpret_cast<const v8bf*>(tile + r * PITCH + (((g + 4 * kk) ^ swz(r)) << 4));
+    }
+  }
+};
+
+// ------------------------------------------------------------ work units
+struct BfUnit {
+  int g;                 // expert (0 for dense), -1: rows of no run, written as zeros
+  int64_t m0, k0;        // first row of D / first k
+  int n0, rows, ks;      // first column; rows of D from m0 on; k length
+  int split, tile;
+};
+
+__device__ __forceinline__ int clamp_off(int v, int most) { return min(max(v, 0), most); }
+
+// The `row tile` of index u over the runs of `groups` experts: tiles of a run
+// are its rows in pieces of BM; the rows before the first run and after the
+// last one are two more runs (g = -1), whose output is zeros.  Every wave
+// scans the offsets by itself, 64 at a time.  Returns the number of row tiles;
+// looks u up where u >= 0.
+template <int BM>
+__device__ __forceinline__ int find_rows(const int32_t* off, int groups, int rows, int u, int lane,
+                                         int& g, int& m0, int& end) {
+  int base = 0;
+  g = -2;
+  for (int c = 0; c < groups + 2; c += 64) {
+    const int e = c + lane;
+    int a = 0, b = 0;
+    if (e < groups) {
+      a = clamp_off(off[e], rows);
+      b = clamp_off(off[e + 1], rows);
+    } else if (e == groups) {
+      a = clamp_off(off[groups], rows);
+      b = rows;
+    } else if (e == groups + 1) {
+      b = clamp_off(off[0], rows);
+    }
+    const int t = b > a ? (b - a + BM - 1) / BM : 0;
+    int incl = t;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
+    }
+    const uint64_t hit = __ballot(base + incl > u);
+    if (g == -2 && u >= 0 && hit) {
+      const int l = __builtin_ctzll(hit);
+      const int first = base + __builtin_amdgcn_readlane(incl - t, l);
+      const int start = __builtin_amdgcn_readlane(a, l);
+      g = c + l < groups ? c + l : -1;
+      m0 = start + (u - first) * BM;
+      end = __builtin_amdgcn_readlane(b, l);
+    }
+    base += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return base;
+}
+
+// Tile order: XCD x runs the workgroups of index x mod 8, so each XCD gets a
+// contiguous run of ids, and ids walk kRaster row tiles before the next
+// column, so the tiles an XCD runs together share operand rows in its L2.
+constexpr int kRaster = 8;
+__device__ __forceinline__ int xcd_id(int b, int total) {
+  const int per = (total + 7) / 8;
+  return b / 8 < per ? (b % 8) * per + b / 8 : total;
+}
+__device__ __forceinline__ void raster(int id, int mt, int nt, int& m, int& n) {
+  const int per = kRaster * nt, grp = id / per, first = grp * kRaster;
+  const int rows = min(mt - first, kRaster), r = id - grp * per;
+  m = first + r % rows;
+  n = r / rows;
+}
+
+// ---------------------------------------------------------------- epilogue
+__device__ __forceinline__ float act_of(int act, float z) {
+  if (act == kActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
+  if (act == kActSilu) return z / (1.f + __expf(-z));
+  if (act == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  return z;
+}
+
+// The four columns n .. n + 3 of row m that a lane holds: bias, activation,
+// residual, and the stores.
+struct BfOut {
+  const BfProblem& p;
+  char* d;               // the unit's D (first row of the tensor or expert)
+  __device__ BfOut(const BfProblem& q, int g) : p(q) {
+    d = (char*)p.d + (int64_t)(p.mode == kBfKRuns ? g : 0) * p.d_stride * (p.out_bf16 ? 2 : 4);
+  }
+  __device__ void four(int64_t m, int n, v4f v) const {
+    const int N = p.N;
+    if (p.bias) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < N)
+          v[i] += p.bias_bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p.bias)[n + i] << 16)
+                              : ((const float*)p.bias)[n + i];
+    }
+    if (p.z) store(p.z, p.ldz, true, m, n, v);
+    if (p.act != kActNone) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = act_of(p.act, v[i]);
+    }
+    if (p.residual) {
+      const uint16_t* r = (const uint16_t*)p.residual + m * p.ldr + n;
+      if (p.ldr % 4 == 0 && n + 4 <= N) {
+        const uint2 w = *reinterpret_cast<const uint2*>(r);
+        v[0] += __uint_as_float(w.x << 16);
+        v[1] += __uint_as_float(w.x & 0xffff0000u);
+        v[2] += __uint_as_float(w.y << 16);
+        v[3] += __uint_as_float(w.y & 0xffff0000u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < N) v[i] += __uint_as_float((uint32_t)r[i] << 16);
+      }
+    }
+    store(d, p.ldd, p.out_bf16, m, n, v);
+  }
+  __device__ void store(void* to, int64_t ld, bool bf16, int64_t m, int n, v4f v) const {
+    const int N = p.N;
+    if (bf16) {
+      uint16_t* q = (uint16_t*)to + m * ld + n;
+      const uint32_t lo = bf16x2(v[0], v[1]), hi = bf16x2(v[2], v[3]);
+      if (ld % 4 == 0 && n + 4 <= N) {
+        *reinterpret_cast<uint2*>(q) = make_uint2(lo, hi);
+      } else {
+        if (n < N) q[0] = (uint16_t)lo;
+        if (n + 1 < N) q[1] = (uint16_t)(lo >> 16);
+        if (n + 2 < N) q[2] = (uint16_t)hi;
+        if (n + 3 < N) q[3] = (uint16_t)(hi >> 16);
+      }
+    } else {
+      float* q = (float*)to + m * ld + n;
+      if (ld % 4 == 0 && n + 4 <= N) {
+        *reinterpret_cast<v4f*>(q) = v;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < N) q[i] = v[i];
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------ kernel
+template <class C, bool AK, bool BK, int MODE>
+__global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::STAGES * C::STAGE_BYTES];
+  __shared__ int last;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm0 = wave % C::WAVES_M * C::WM, wn0 = wave / C::WAVES_M * C::WN;
+  const int nt = (p.N + C::BN - 1) / C::BN;
+
+  BfUnit w{};
+  if constexpr (MODE == kBfRowRuns) {
+    int g, m0, end;
+    const int mt = find_rows<C::BM>(p.offsets, p.groups, p.M, -1, lane, g, m0, end);
+    const int id = xcd_id(blockIdx.x, mt * nt);
+    if (id >= mt * nt) return;
+    int m, n;
+    raster(id, mt, nt, m, n);
+    find_rows<C::BM>(p.offsets, p.groups, p.M, m, lane, g, m0, end);
+    w.g = uniform(g);
+    w.m0 = uniform(m0);
+    w.n0 = uniform(n) * C::BN;
+    w.rows = uniform(end - m0);
+    w.ks = w.g < 0 ? 0 : p.K;
+  } else {
+    const int mt = (p.M + C::BM - 1) / C::BM;
+    const int tiles = mt * nt;
+    int id = xcd_id(blockIdx.x, tiles * (MODE == kBfKRuns ? p.groups : p.splits));
+    if (id >= tiles * (MODE == kBfKRuns ? p.groups : p.splits)) return;
+    int m, n;
+    const int part = id / tiles;
+    id -= part * tiles;
+    raster(id, mt, nt, m, n);
+    w.m0 = (int64_t)m * C::BM;
+    w.n0 = n * C::BN;
+    w.rows = p.M - (int)w.m0;
+    if constexpr (MODE == kBfKRuns) {
+      const int a = clamp_off(p.offsets[part], p.K), b = clamp_off(p.offsets[part + 1], p.K);
+      w.g = part;
+      w.k0 = uniform(a);
+      w.ks = uniform(max(b - a, 0));
+    } else {
+      const int steps = (p.K + kBK - 1) / kBK;
+      const int s0 = (int)((int64_t)part * steps / p.splits), s1 = (int)((int64_t)(part + 1) * steps / p.splits);
+      w.split = part;
+      w.tile = id;
+      w.k0 = (int64_t)s0 * kBK;
+      w.ks = min(p.K, s1 * kBK) - s0 * kBK;
+    }
+  }
+
+  v4f acc[C::TM][C::TN];
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  const int steps = (w.ks + kBK - 1) / kBK;
+  if (steps > 0) {
+    typedef Operand<AK, C::BM, C::WAVES> OpA;
+    typedef Operand<BK, C::BN, C::WAVES> OpB;
+    OpA a;
+    OpB b;
+    a.init(p.a, p.lda, w.m0, w.rows, w.k0, w.ks, wave, lane);
+    b.init(p.b + (MODE == kBfRowRuns ? w.g * p.b_stride : 0), p.ldb, w.n0, p.N - w.n0, w.k0, w.ks, wave, lane);
+    const uint32_t lds0 = lds_addr(smem);
+    auto issue = [&](int kt) {
+      const uint32_t st = uniform(lds0 + (uint32_t)(kt % C::STAGES * C::STAGE_BYTES));
+      a.issue(kt, st, wave, lane);
+      b.issue(kt, st + C::A_BYTES, wave, lane);
+    };
+    // copies a wave has in flight for one step (uneven tiles: some waves have
+    // fewer, and then wait for a little more than they need)
+    constexpr int LEAST = OpA::COPIES / C::WAVES + OpB::COPIES / C::WAVES;
+    for (int s = 0; s < C::STAGES - 1; ++s)
+      if (s < steps) issue(s);
+    for (int kt = 0; kt < steps; ++kt) {
+      if (steps - 1 - kt >= C::STAGES - 2) wait_vmcnt<(C::STAGES - 2) * LEAST>();
+      else wait_vmcnt<0>();
+      __syncthreads();
+      if (kt + C::STAGES - 1 < steps) issue(kt + C::STAGES - 1);
+      const uint8_t* As = smem + kt % C::STAGES * C::STAGE_BYTES;
+      const uint8_t* Bs = As + C::A_BYTES;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        v8bf fa[C::TM], fb[C::TN];
+#pragma unroll
+        for (int i = 0; i < C::TM; ++i) fa[i] = OpA::frag(As, wm0 + 16 * i, kk, lane);
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j) fb[j] = OpB::frag(Bs, wn0 + 16 * j, kk, lane);
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+          for (int i = 0; i < C::TM; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      }
+    }
+  }
+
+  // ---- split k: every split publishes its FP32 tile past the caches of its
+  // XCD, the last one to arrive adds them up in the order of the splits (the
+  // same bits on every call) and leaves the counter at zero
+  if (MODE == kBfDense && p.splits > 1) {
+    constexpr uint32_t kTile = C::BM * C::BN * 4;
+    const __amdgpu_buffer_rsrc_t ws =
+        buffer_rsrc(p.partial + (int64_t)w.tile * p.splits * (C::BM * C::BN), kTile * p.splits);
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::TN; ++j)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, acc[i][j]), ws,
+                                               w.split * kTile + (((wave * C::TM + i) * C::TN + j) * 64 + lane) * 16,
+                                               0, kCoherent);
+    wait_all_memory();
+    __syncthreads();
+    if (tid == 0)
+      last = __hip_atomic_fetch_add(p.counters + w.tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
+    __syncthreads();
+    if (!last) return;
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::TN; ++j) {
+        const uint32_t at = (((wave * C::TM + i) * C::TN + j) * 64 + lane) * 16;
+        v4f sum = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < p.splits; ++s)
+          sum += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(ws, s * kTile + at, 0, kCoherent));
+        acc[i][j] = sum;
+      }
+    if (tid == 0) __hip_atomic_store(p.counters + w.tile, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+
+  const BfOut out(p, w.g);
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i) {
+    const int r = wm0 + 16 * i + (lane & 15);
+    if (r < w.rows) {
+#pragma unroll
+      for (int j = 0; j < C::TN; ++j) out.four(w.m0 + r, w.n0 + wn0 + 16 * j + 4 * (lane >> 4), acc[i][j]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host
+// Tile configurations.  Large: 128 accumulators a lane, two waves a SIMD.
+using BfHuge = BfCfg<256, 256, 2, 4, 2, 2>;
+using BfMid = BfCfg<128, 128, 2, 2, 3, 1>;
+using BfLow = BfCfg<64, 64, 2, 2, 4, 2>;
+using BfThin = BfCfg<16, 64, 1, 4, 7, 2>;
+
+namespace {
+
+template <class C, bool AK, bool BK, int MODE>
+hipError_t launch_as(const BfProblem& p, hipStream_t stream) {
+  const int64_t nt = (p.N + C::BN - 1) / C::BN;
+  int64_t units = (p.M + C::BM - 1) / C::BM * nt;
+  // row runs: a run may end inside a tile, so one more tile a run at most
+  if (MODE == kBfRowRuns) units = ((int64_t)(p.M + C::BM - 1) / C::BM + p.groups + 1) * nt;
+  if (MODE == kBfKRuns) units *= p.groups;
+  if (MODE == kBfDense) units *= p.splits;
+  const int64_t grid = (units + 7) / 8 * 8;
+  hipLaunchKernelGGL((bf16_kernel<C, AK, BK, MODE>), dim3((unsigned)grid), dim3(C::THREADS), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <bool AK, bool BK, int MODE>
+hipError_t launch_tile(const BfProblem& p, const BfTile& t, hipStream_t stream) {
+  if (t.cfg == 0) return launch_as<BfHuge, AK, BK, MODE>(p, stream);
+  if (t.cfg == 1) return launch_as<BfMid, AK, BK, MODE>(p, stream);
+  if constexpr (AK) {
+    return launch_as<BfLow, AK, BK, MODE>(p, stream);
+  } else {
+    if (t.cfg == 2) return launch_as<BfLow, AK, BK, MODE>(p, stream);
+    return launch_as<BfThin, AK, BK, MODE>(p, stream);
+  }
+}
+
+}  // namespace
+
+BfTile bf16_tile(const BfProblem& p, int cus) {
+  static constexpr int kBm[] = {BfHuge::BM, BfMid::BM, BfLow::BM, BfThin::BM};
+  static constexpr int kBn[] = {BfHuge::BN, BfMid::BN, BfLow::BN, BfThin::BN};
+  BfTile t{};
+  // rows of one tile column: a run's average for the row runs
+  const int64_t rows = p.mode == kBfRowRuns ? (p.M + p.groups - 1) / p.groups : p.M;
+  const int64_t runs = p.mode == kBfDense ? 1 : p.groups;
+  auto units = [&](int c) { return runs * ((rows + kBm[c] - 1) / kBm[c]) * ((p.N + kBn[c] - 1) / kBn[c]); };
+  if (units(0) >= cus) t.cfg = 0;
+  else if (rows > 64 && (p.N > 64 || !p.a_kmajor)) t.cfg = 1;
+  else if (rows > 16 || p.a_kmajor) t.cfg = 2;
+  else t.cfg = 3;
+  t.bm = kBm[t.cfg];
+  t.bn = kBn[t.cfg];
+  t.splits = 1;
+  if (p.mode == kBfDense) {
+    const int64_t u = units(t.cfg), steps = (p.K + kBK - 1) / kBK;
+    if (u < cus && u <= kSplitKMaxTiles) {
+      int64_t s = cus / u;
+      if (s > steps / 4) s = steps / 4;
+      if (s > kBfMaxSplits) s = kBfMaxSplits;
+      if (s > 1) t.splits = (int)s;
+    }
+  }
+  return t;
+}
+
+size_t bf16_workspace_bytes(const BfProblem& p, int cus) {
+  const BfTile t = bf16_tile(p, cus);
+  if (t.splits <= 1) return 0;
+  const size_t tiles = (size_t)((p.M + t.bm - 1) / t.bm) * ((p.N + t.bn - 1) / t.bn);
+  return kSplitKCounterBytes + tiles * t.splits * t.bm * t.bn * 4;
+}
+
+hipError_t launch_bf16(BfProblem p, const BfTile& t, hipStream_t stream) {
+  p.splits = t.splits;
+  if (p.mode == kBfRowRuns)
+    return p.b_kmajor ? launch_tile<false, true, kBfRowRuns>(p, t, stream)
+                      : launch_tile<false, false, kBfRowRuns>(p, t, stream);
+  if (p.mode == kBfKRuns) return launch_tile<true, true, kBfKRuns>(p, t, stream);
+  if (p.a_kmajor) return launch_tile<true, true, kBfDense>(p, t, stream);
+  return p.b_kmajor ? launch_tile<false, true, kBfDense>(p, t, stream)
+                    : launch_tile<false, false, kBfDense>(p, t, stream);
+}
+
+}  // namespace fg8

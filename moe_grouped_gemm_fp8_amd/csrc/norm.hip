@@ -1,0 +1,458 @@
+// Layer norm over the last axis and its gradient, and the column sums that
+// bias and weight gradients need.
+//
+//   y = (x - mean) * rstd * weight + bias,   rstd = 1 / sqrt(var + eps)
+//   g = dy * weight,  h = (x - mean) * rstd
+//   dx = rstd * (g - mean(g) - h * mean(g h))
+//   dweight = sum over rows of dy h,   dbias = sum over rows of dy
+//
+// All arithmetic is FP32.  HBM bounds these: a row is read once (x, and dy)
+// and written once.  A team of WAVES waves owns a row at a time and holds it
+// in registers, so the variance is taken around the mean (two passes over
+// registers, not the sum of squares); a thread owns the same columns of every
+// row its team takes, which keeps the weight and, backward, both parameters'
+// running sums in registers too.  Teams leave one partial sum each; a second
+// kernel adds them in team order, so the result is the same on every call.
+#include <type_traits>
+
+#include "fg8_device.h"
+#include "fg8_internal.h"
+
+namespace fg8 {
+
+namespace {
+
+// Sixteen bytes of a row at element `c` as FP32: the elements at or past
+// `cols` are zeros.  Rows need no alignment beyond their element's.
+template <class T>
+struct Piece {
+  static constexpr int N = 16 / sizeof(T);
+  __device__ static uint4 load(const T* row, int64_t c, int64_t cols) {
+    if (c + N <= cols) {
+      uint4 v;   // (one 16-byte load at any element's address)
+      __builtin_memcpy(&v, row + c, 16);
+      return v;
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c + i < cols) {
+        if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(row[c + i]);
+        else w[i / 2] |= (uint32_t)row[c + i] << (16 * (i & 1));
+      }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ static void store(T* row, int64_t c, int64_t cols, const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
+      else w[i] = bf16x2(f[2 * i], f[2 * i + 1]);
+    }
+    if (c + N <= cols) {
+      __builtin_memcpy(row + c, w, 16);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c + i < cols) {
+        if constexpr (sizeof(T) == 4) row[c + i] = f[i];
+        else row[c + i] = (T)(w[i / 2] >> (16 * (i & 1)));
+      }
+  }
+};
+
+// N parameter values from element c on (0 past cols), FP32 or BF16
+template <int N>
+__device__ __forceinline__ void params(const void* p, bool bf16, int64_t c, int64_t cols, float* f) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    f[i] = c + i < cols ? (bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p)[c + i] << 16)
+                                : ((const float*)p)[c + i])
+                        : 0.f;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// Sum over the team of `K` values at once; `at` alternates between the two
+// halves of the exchange buffer, so one barrier a call is enough.
+template <int WAVES, int K>
+__device__ __forceinline__ void team_sum(float (&v)[K], float (*buf)[16][2], int& at, int wave, int lane) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
+  if constexpr (WAVES > 1) {
+    if (lane == 0)
+#pragma unroll
+      for (int k = 0; k < K; ++k) buf[at][wave][k] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) s += buf[at][w][k];
+      v[k] = s;
+    }
+    at ^= 1;
+  }
+}
+
+// Threads of a workgroup: one team of WAVES waves, or four teams of one wave.
+template <int WAVES>
+constexpr int threads_of() { return WAVES == 1 ? 256 : 64 * WAVES; }
+template <int WAVES>
+constexpr int teams_of() { return WAVES == 1 ? 4 : 1; }
+
+template <class T, int WAVES, int NV>
+__global__ __launch_bounds__(threads_of<WAVES>()) void norm_kernel(
+    const T* __restrict__ x, int64_t ldx, const void* __restrict__ weight,
+    const void* __restrict__ bias, bool w_bf16, float eps, int64_t rows, int64_t cols,
+    T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd) {
+  constexpr int N = Piece<T>::N;
+  __shared__ float buf[2][16][2];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int me = WAVES == 1 ? lane : threadIdx.x;
+  const int64_t team = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+  const int64_t teams = (int64_t)gridDim.x * teams_of<WAVES>();
+  int at = 0;
+  uint4 raw[NV];
+  auto fetch = [&](int64_t r) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)(i * 64 * WAVES + me) * N;
+      raw[i] = c < cols ? Piece<T>::load(x + r * ldx, c, cols) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (team < rows) fetch(team);
+  float w[NV][N], b[NV][N];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = (int64_t)(i * 64 * WAVES + me) * N;
+    params<N>(weight, w_bf16, c, cols, w[i]);
+    if (bias) params<N>(bias, w_bf16, c, cols, b[i]);
+    else
+#pragma unroll
+      for (int j = 0; j < N; ++j) b[i][j] = 0.f;
+  }
+  for (int64_t r = team; r < rows; r += teams) {
+    float f[NV][N];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      RowVec<T>::widen(raw[i], f[i]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) s[0] += f[i][j];
+    }
+    if (r + teams < rows) fetch(r + teams);   // in flight under this row's arithmetic
+    team_sum<WAVES, 1>(s, buf, at, wave, lane);
+    const float m = s[0] / (float)cols;   // (a row of one value has that mean)
+    float q[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int64_t c = (int64_t)(i * 64 * WAVES + me) * N + j;
+        f[i][j] = c < cols ? f[i][j] - m : 0.f;
+        q[0] = fmaf(f[i][j], f[i][j], q[0]);
+      }
+    team_sum<WAVES, 1>(q, buf, at, wave, lane);
+    const float rs = 1.f / sqrtf(q[0] / (float)cols + eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)(i * 64 * WAVES + me) * N;
+      float o[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[j] = fmaf(f[i][j] * rs, w[i][j], b[i][j]);
+      if (c < cols) Piece<T>::store(y + r * cols, c, cols, o);
+    }
+    if (me == 0) {
+      mean[r] = m;
+      rstd[r] = rs;
+    }
+  }
+}
+
+template <class T, int WAVES, int NV>
+__global__ __launch_bounds__(threads_of<WAVES>()) void norm_backward_kernel(
+    const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
+    const void* __restrict__ weight, bool w_bf16, const float* __restrict__ mean,
+    const float* __restrict__ rstd, int64_t rows, int64_t cols, T* __restrict__ dx,
+    float* __restrict__ partial) {
+  constexpr int N = Piece<T>::N;
+  __shared__ float buf[2][16][2];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int me = WAVES == 1 ? lane : threadIdx.x;
+  const int64_t team = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+  const int64_t teams = (int64_t)gridDim.x * teams_of<WAVES>();
+  const float inv = 1.f / (float)cols;
+  int at = 0;
+  uint4 rx[NV], rd[NV];
+  float m = 0.f, rs = 0.f;
+  auto fetch = [&](int64_t r) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)(i * 64 * WAVES + me) * N;
+      rx[i] = c < cols ? Piece<T>::load(x + r * ldx, c, cols) : make_uint4(0, 0, 0, 0);
+      rd[i] = c < cols ? Piece<T>::load(dy + r * lddy, c, cols) : make_uint4(0, 0, 0, 0);
+    }
+    m = mean[r];
+    rs = rstd[r];
+  };
+  if (team < rows) fetch(team);
+  float w[NV][N], dw[NV][N], db[NV][N];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    params<N>(weight, w_bf16, (int64_t)(i * 64 * WAVES + me) * N, cols, w[i]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) dw[i][j] = db[i][j] = 0.f;
+  }
+  for (int64_t r = team; r < rows; r += teams) {
+    float h[NV][N], g[NV][N];
+    float s[2] = {0.f, 0.f};
+    const float m0 = m, rs0 = rs;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      RowVec<T>::widen(rx[i], h[i]);
+      RowVec<T>::widen(rd[i], g[i]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        // past the last column dy is zero and the weight too: h adds nothing
+        h[i][j] = (h[i][j] - m0) * rs0;
+        dw[i][j] = fmaf(g[i][j], h[i][j], dw[i][j]);
+        db[i][j] += g[i][j];
+        g[i][j] *= w[i][j];
+        s[0] += g[i][j];
+        s[1] = fmaf(g[i][j], h[i][j], s[1]);
+      }
+    }
+    if (r + teams < rows) fetch(r + teams);
+    team_sum<WAVES, 2>(s, buf, at, wave, lane);
+    const float c1 = s[0] * inv, c2 = s[1] * inv;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)(i * 64 * WAVES + me) * N;
+      float o[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[j] = rs0 * (g[i][j] - c1 - h[i][j] * c2);
+      if (c < cols) Piece<T>::store(dx + r * cols, c, cols, o);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = (int64_t)(i * 64 * WAVES + me) * N;
+    if (c < cols) {
+      Piece<float>::store(partial + team * 2 * cols, c, cols, dw[i]);
+      Piece<float>::store(partial + (team * 2 + 1) * cols, c, cols, db[i]);
+      if constexpr (N == 8) {
+        if (c + 4 < cols) {
+          Piece<float>::store(partial + team * 2 * cols, c + 4, cols, dw[i] + 4);
+          Piece<float>::store(partial + (team * 2 + 1) * cols, c + 4, cols, db[i] + 4);
+        }
+      }
+    }
+  }
+}
+
+// out[c] = sum over p < parts of partial[p * stride + c], each column's parts
+// added in a fixed order: 16 waves take every sixteenth part, then meet in LDS.
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restrict__ partial,
+                                                          int64_t stride, int parts, int64_t cols,
+                                                          float* __restrict__ out) {
+  __shared__ float buf[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int p = wave; p < parts; p += 16) s += partial[p * stride + c];
+  }
+  buf[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < cols) {
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) t += buf[k][lane];
+    out[c] = t;
+  }
+}
+
+// The team shape for a row length: waves a row and 16-byte pieces a thread.
+template <class F>
+hipError_t with_shape(int64_t cols, bool bf16, F f) {
+  if (bf16) {
+    if (cols <= 512) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+    if (cols <= 1024) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
+    if (cols <= 2048) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+    if (cols <= 4096) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+    if (cols <= 8192) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
+    if (cols <= 16384) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+  }
+  if (cols <= 256) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+  if (cols <= 1024) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
+  if (cols <= 2048) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+  if (cols <= 4096) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
+  if (cols <= 8192) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+  if (cols <= 16384) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
+}
+
+// Workgroups: enough for two or more a SIMD, and no more than there are rows.
+int64_t groups_of(int waves, int64_t rows, int cus) {
+  const int64_t most = (int64_t)cus * (waves <= 4 ? 4 : waves == 8 ? 2 : 1);
+  const int64_t need = waves == 1 ? (rows + 3) / 4 : rows;
+  return need < most ? need : most;
+}
+
+}  // namespace
+
+int64_t layer_norm_teams(int64_t rows, int64_t cols, bool bf16, int cus) {
+  int64_t teams = 0;
+  (void)with_shape(cols, bf16, [&](auto waves, auto) {
+    teams = groups_of(waves, rows, cus) * teams_of<decltype(waves)::value>();
+    return hipSuccess;
+  });
+  return teams;
+}
+
+namespace {
+
+template <class T>
+hipError_t norm_as(const void* x, int64_t ldx, const void* weight, const void* bias, bool w_bf16,
+                   float eps, int64_t rows, int64_t cols, void* y, float* mean, float* rstd, int cus,
+                   hipStream_t stream) {
+  return with_shape(cols, sizeof(T) == 2, [&](auto waves, auto nv) {
+    constexpr int W = decltype(waves)::value, NV = decltype(nv)::value;
+    hipLaunchKernelGGL((norm_kernel<T, W, NV>), dim3((unsigned)groups_of(W, rows, cus)),
+                       dim3(threads_of<W>()), 0, stream, (const T*)x, ldx, weight, bias, w_bf16, eps,
+                       rows, cols, (T*)y, mean, rstd);
+    return hipGetLastError();
+  });
+}
+
+template <class T>
+hipError_t norm_backward_as(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                            const void* weight, bool w_bf16, const float* mean, const float* rstd,
+                            int64_t rows, int64_t cols, void* dx, float* partial, int cus,
+                            hipStream_t stream) {
+  return with_shape(cols, sizeof(T) == 2, [&](auto waves, auto nv) {
+    constexpr int W = decltype(waves)::value, NV = decltype(nv)::value;
+    hipLaunchKernelGGL((norm_backward_kernel<T, W, NV>), dim3((unsigned)groups_of(W, rows, cus)),
+                       dim3(threads_of<W>()), 0, stream, (const T*)dy, lddy, (const T*)x, ldx, weight,
+                       w_bf16, mean, rstd, rows, cols, (T*)dx, partial);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace
+
+hipError_t launch_layer_norm(const void* x, int64_t ldx, bool bf16, const void* weight,
+                             const void* bias, bool w_bf16, float eps, int64_t rows, int64_t cols,
+                             void* y, float* mean, float* rstd, int cus, hipStream_t stream) {
+  return bf16 ? norm_as<uint16_t>(x, ldx, weight, bias, w_bf16, eps, rows, cols, y, mean, rstd, cus, stream)
+              : norm_as<float>(x, ldx, weight, bias, w_bf16, eps, rows, cols, y, mean, rstd, cus, stream);
+}
+
+hipError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                      bool bf16, const void* weight, bool w_bf16,
+                                      const float* mean, const float* rstd, int64_t rows,
+                                      int64_t cols, void* dx, float* dweight, float* dbias,
+                                      float* partial, int cus, hipStream_t stream) {
+  const int64_t teams = rows > 0 ? layer_norm_teams(rows, cols, bf16, cus) : 0;
+  if (rows > 0) {
+    const hipError_t e =
+        bf16 ? norm_backward_as<uint16_t>(dy, lddy, x, ldx, weight, w_bf16, mean, rstd, rows, cols, dx, partial, cus, stream)
+             : norm_backward_as<float>(dy, lddy, x, ldx, weight, w_bf16, mean, rstd, rows, cols, dx, partial, cus, stream);
+    if (e != hipSuccess) return e;
+  }
+  const dim3 grid((unsigned)((cols + 63) / 64));
+  hipLaunchKernelGGL(column_sum_kernel, grid, dim3(1024), 0, stream, partial, 2 * cols, (int)teams, cols, dweight);
+  hipLaunchKernelGGL(column_sum_kernel, grid, dim3(1024), 0, stream, partial + cols, 2 * cols, (int)teams, cols, dbias);
+  return hipGetLastError();
+}
+
+// ------------------------------------------- the activation's backward pass
+namespace {
+
+__device__ __forceinline__ float act_slope(int act, float z) {
+  if (act == kActRelu) return z > 0.f ? 1.f : (z != z ? z : 0.f);
+  if (act == kActSilu) {
+    const float p = 1.f / (1.f + __expf(-z));
+    return p * (1.f + z * (1.f - p));
+  }
+  if (act == kActGelu)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * (__expf(-0.5f * z * z) * 0.39894228040143268f);
+  return 1.f;
+}
+
+constexpr int kActCols = 512;   // columns of a workgroup: eight a lane
+
+// Workgroup (column block, row chunk): its four waves take the chunk's rows in
+// turn and meet in LDS for the column sums, taken before dz is rounded.
+__global__ __launch_bounds__(256) void act_backward_kernel(
+    const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ z, int64_t ldzin,
+    int act, int64_t m, int64_t n, int64_t per, uint16_t* __restrict__ dz, int64_t ldz,
+    float* __restrict__ partial) {
+  __shared__ float buf[4][kActCols];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * kActCols + lane * 8;
+  const int64_t r1 = min((int64_t)(blockIdx.y + 1) * per, m);
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (c < n) {
+#pragma unroll 4
+    for (int64_t r = blockIdx.y * per + wave; r < r1; r += 4) {
+      float d[8];
+      RowVec<uint16_t>::widen(Piece<uint16_t>::load(dy + r * lddy, c, n), d);
+      if (act != kActNone) {
+        float v[8];
+        RowVec<uint16_t>::widen(Piece<uint16_t>::load(z + r * ldzin, c, n), v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] *= act_slope(act, v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // (a slope of NaN past the last column would not reach dz's padding)
+        if (c + i >= n) d[i] = 0.f;
+        s[i] += d[i];
+      }
+      if (dz) Piece<uint16_t>::store(dz + r * ldz, c, ldz, d);
+    }
+  }
+  if (!partial) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) buf[wave][lane * 8 + i] = s[i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kActCols; i += 256) {
+    const int64_t col = (int64_t)blockIdx.x * kActCols + i;
+    if (col < n) partial[blockIdx.y * n + col] = (buf[0][i] + buf[1][i]) + (buf[2][i] + buf[3][i]);
+  }
+}
+
+}  // namespace
+
+int act_backward_chunks(int64_t m, int64_t n) {
+  // about 2048 workgroups, of 16 rows at least
+  const int64_t blocks = (n + kActCols - 1) / kActCols;
+  int64_t chunks = (2048 + blocks - 1) / blocks;
+  if (chunks > (m + 15) / 16) chunks = (m + 15) / 16;
+  return (int)(chunks < 1 ? 1 : chunks);
+}
+
+hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldzin,
+                               int act, int64_t m, int64_t n, uint16_t* dz, int64_t ldz,
+                               float* partial, float* dbias, hipStream_t stream) {
+  const int chunks = act_backward_chunks(m, n);
+  const int64_t per = (m + chunks - 1) / chunks;
+  hipLaunchKernelGGL(act_backward_kernel, dim3((unsigned)((n + kActCols - 1) / kActCols), (unsigned)chunks),
+                     dim3(256), 0, stream, dy, lddy, z, ldzin, act, m, n, per, dz, ldz,
+                     dbias ? partial : nullptr);
+  if (dbias)
+    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((n + 63) / 64)), dim3(1024), 0, stream,
+                       partial, n, chunks, n, dbias);
+  return hipGetLastError();
+}
+
+}  // namespace fg8
