@@ -111,6 +111,27 @@ struct RowVec<uint16_t> {   // BF16 bits widen exactly to FP32
   }
 };
 
+// ----------------------------------------------------------- activations
+// The normal distribution function and density (times sqrt 2 pi): erfc(x) =
+// (a1 t + .. + a5 t^5) e^(-x^2), t = 1 / (1 + 0.3275911 x), x = |z| / sqrt 2
+// (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26, error
+// below 1.5e-7).  Taken as it is for z < 0, so the lower tail has no
+// cancellation; in FP32 z Phi(z) is within 4.2e-7 of the exact value and
+// within 2.9e-7 |z|.  Twelve plain operations and two quarter-rate ones, where
+// the library's erff runs both of its branches.
+__device__ __forceinline__ float normal_cdf(float z, float* bell) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+  const float e = __builtin_amdgcn_exp2f(x * x * -1.4426950408889634f);
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  const float n = 0.5f * p * t * e;
+  *bell = e;
+  return z < 0.f ? n : 1.f - n;
+}
+
 // ---------------------------------------------------------------- GEMM helpers
 // 16-byte chunk swizzle of LDS row r.  Measured with SQ_LDS_BANK_CONFLICT on
 // gfx950: (r >> 1) & 7 leaves the MFMA operand reads (one chunk of 16

@@ -106,6 +106,7 @@ struct BfProblem {
   int64_t ldr;
   uint16_t* z;                  // the value before the activation, BF16
   int64_t ldz;
+  int grid;                     // workgroups of a persistent launch (set by the launcher)
   // split k (dense)
   int splits;
   float* partial;

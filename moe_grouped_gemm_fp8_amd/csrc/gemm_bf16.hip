@@ -27,6 +27,8 @@
 // MFMA 16x16x32: lane i + 16 g holds row i, k = 8 g .. 8 g + 7 of either
 // operand; result register v of that lane is row 4 g + v, column i.  B goes in
 // as the first operand, so a lane holds four consecutive columns n of one row.
+#include <type_traits>
+
 #include "fg8_device.h"
 #include "fg8_internal.h"
 
@@ -208,13 +210,67 @@ __device__ __forceinline__ int find_rows(const int32_t* off, int groups, int row
   return base;
 }
 
-// Tile order: XCD x runs the workgroups of index x mod 8, so each XCD gets a
-// contiguous run of ids, and ids walk kRaster row tiles before the next
-// column, so the tiles an XCD runs together share operand rows in its L2.
+// The same for a persistent workgroup that looks up many units: the runs'
+// tile counts as a running sum in LDS, with each run's start and end.
+constexpr int kMaxRuns = 1024 + 2;
+template <int CAP>
+struct RunTable {
+  int sum[CAP], start[CAP], end[CAP];   // sum: tiles of the runs up to and with this one
+};
+// Filled by one wave (the caller's barrier makes it visible).
+template <int BM, class Table>
+__device__ __forceinline__ void fill_runs(Table& t, const int32_t* off, int groups, int rows, int lane) {
+  int base = 0;
+  for (int c = 0; c < groups + 2; c += 64) {
+    const int e = c + lane;
+    int a = 0, b = 0;
+    if (e < groups) {
+      a = clamp_off(off[e], rows);
+      b = clamp_off(off[e + 1], rows);
+    } else if (e == groups) {
+      a = clamp_off(off[groups], rows);
+      b = rows;
+    } else if (e == groups + 1) {
+      b = clamp_off(off[0], rows);
+    }
+    int incl = b > a ? (b - a + BM - 1) / BM : 0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
+    }
+    if (e < groups + 2) {
+      t.sum[e] = base + incl;
+      t.start[e] = a;
+      t.end[e] = b;
+    }
+    base += __builtin_amdgcn_readlane(incl, 63);
+  }
+}
+template <int BM, class Table>
+__device__ __forceinline__ void look_up_run(const Table& t, int groups, int m, int& g, int& m0, int& rows) {
+  int lo = 0, hi = groups + 1;      // the first run whose sum exceeds m
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (uniform(t.sum[mid]) > m) hi = mid; else lo = mid + 1;
+  }
+  const int first = lo > 0 ? uniform(t.sum[lo - 1]) : 0;
+  g = lo < groups ? lo : -1;
+  m0 = uniform(t.start[lo]) + (m - first) * BM;
+  rows = uniform(t.end[lo]) - m0;
+}
+
+// Tile order: XCD x runs the workgroups of index x mod 8.  In every round of G
+// units (a CU's worth each) it takes a contiguous run of ids, and ids walk
+// kRaster row tiles before the next column, so the tiles an XCD runs together
+// share operand rows in its L2.
 constexpr int kRaster = 8;
-__device__ __forceinline__ int xcd_id(int b, int total) {
-  const int per = (total + 7) / 8;
-  return b / 8 < per ? (b % 8) * per + b / 8 : total;
+constexpr int kCus = 256;     // of the device; only the tile order goes by it
+__device__ __forceinline__ int xcd_round(int u, int total, int G) {
+  const int base = u / G * G;
+  if (G % 8 || base + G > total) return u;
+  const int b = u - base;
+  return base + (b % 8) * (G / 8) + b / 8;
 }
 __device__ __forceinline__ void raster(int id, int mt, int nt, int& m, int& n) {
   const int per = kRaster * nt, grp = id / per, first = grp * kRaster;
@@ -223,12 +279,87 @@ __device__ __forceinline__ void raster(int id, int mt, int nt, int& m, int& n) {
   n = r / rows;
 }
 
+// The unit of this workgroup; false where it has none (the grid is an upper
+// bound: how the rows fall into runs is known on the device only).
+template <int BM, int BN, int MODE>
+__device__ __forceinline__ bool find_unit(const BfProblem& p, int lane, BfUnit& w) {
+  const int nt = (p.N + BN - 1) / BN;
+  w = BfUnit{};
+  if constexpr (MODE == kBfRowRuns) {
+    int g, m0, end;
+    const int mt = find_rows<BM>(p.offsets, p.groups, p.M, -1, lane, g, m0, end);
+    if ((int)blockIdx.x >= mt * nt) return false;
+    const int id = xcd_round(blockIdx.x, mt * nt, kCus);
+    int m, n;
+    raster(id, mt, nt, m, n);
+    find_rows<BM>(p.offsets, p.groups, p.M, m, lane, g, m0, end);
+    w.g = uniform(g);
+    w.m0 = uniform(m0);
+    w.n0 = uniform(n) * BN;
+    w.rows = uniform(end - m0);
+    w.ks = w.g < 0 ? 0 : p.K;
+  } else {
+    const int mt = (p.M + BM - 1) / BM, tiles = mt * nt;
+    const int total = tiles * (MODE == kBfKRuns ? p.groups : p.splits);
+    if ((int)blockIdx.x >= total) return false;
+    int id = xcd_round(blockIdx.x, total, kCus);
+    int m, n;
+    const int part = id / tiles;
+    id -= part * tiles;
+    raster(id, mt, nt, m, n);
+    w.m0 = (int64_t)m * BM;
+    w.n0 = n * BN;
+    w.rows = p.M - (int)w.m0;
+    if constexpr (MODE == kBfKRuns) {
+      const int a = clamp_off(p.offsets[part], p.K), b = clamp_off(p.offsets[part + 1], p.K);
+      w.g = part;
+      w.k0 = uniform(a);
+      w.ks = uniform(max(b - a, 0));
+    } else {
+      const int steps = (p.K + kBK - 1) / kBK;
+      const int s0 = (int)((int64_t)part * steps / p.splits), s1 = (int)((int64_t)(part + 1) * steps / p.splits);
+      w.split = part;
+      w.tile = id;
+      w.k0 = (int64_t)s0 * kBK;
+      w.ks = min(p.K, s1 * kBK) - s0 * kBK;
+    }
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------- epilogue
 __device__ __forceinline__ float act_of(int act, float z) {
   if (act == kActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
-  if (act == kActSilu) return z / (1.f + __expf(-z));
-  if (act == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if (act == kActSilu)   // (-0 for very negative z: exp2 gives inf, its reciprocal 0)
+    return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+  if (act == kActGelu) {
+    float bell;
+    return z * normal_cdf(z, &bell);
+  }
   return z;
+}
+
+// bias[n .. n + 3] (0 past N, or without a bias)
+__device__ __forceinline__ v4f bias4(const BfProblem& p, int n) {
+  v4f v = {0.f, 0.f, 0.f, 0.f};
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < p.N)
+        v[i] = p.bias_bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p.bias)[n + i] << 16)
+                           : ((const float*)p.bias)[n + i];
+  }
+  return v;
+}
+// residual[m][n .. n + 3] as BF16 bits (0 past N)
+__device__ __forceinline__ uint2 residual4(const BfProblem& p, int64_t m, int n) {
+  const uint16_t* r = p.residual + m * p.ldr + n;
+  if (p.ldr % 4 == 0 && n + 4 <= p.N) return *reinterpret_cast<const uint2*>(r);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < p.N) w[i / 2] |= (uint32_t)r[i] << (16 * (i & 1));
+  return make_uint2(w[0], w[1]);
 }
 
 // The four columns n .. n + 3 of row m that a lane holds: bias, activation,
@@ -240,32 +371,16 @@ struct BfOut {
     d = (char*)p.d + (int64_t)(p.mode == kBfKRuns ? g : 0) * p.d_stride * (p.out_bf16 ? 2 : 4);
   }
   __device__ void four(int64_t m, int n, v4f v) const {
-    const int N = p.N;
-    if (p.bias) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < N)
-          v[i] += p.bias_bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p.bias)[n + i] << 16)
-                              : ((const float*)p.bias)[n + i];
-    }
+    if (p.bias) v += bias4(p, n);
     if (p.z) store(p.z, p.ldz, true, m, n, v);
     if (p.act != kActNone) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = act_of(p.act, v[i]);
     }
     if (p.residual) {
-      const uint16_t* r = (const uint16_t*)p.residual + m * p.ldr + n;
-      if (p.ldr % 4 == 0 && n + 4 <= N) {
-        const uint2 w = *reinterpret_cast<const uint2*>(r);
-        v[0] += __uint_as_float(w.x << 16);
-        v[1] += __uint_as_float(w.x & 0xffff0000u);
-        v[2] += __uint_as_float(w.y << 16);
-        v[3] += __uint_as_float(w.y & 0xffff0000u);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < N) v[i] += __uint_as_float((uint32_t)r[i] << 16);
-      }
+      const uint2 w = residual4(p, m, n);
+      v += v4f{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+               __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
     }
     store(d, p.ldd, p.out_bf16, m, n, v);
   }
@@ -302,48 +417,8 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
   __shared__ int last;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm0 = wave % C::WAVES_M * C::WM, wn0 = wave / C::WAVES_M * C::WN;
-  const int nt = (p.N + C::BN - 1) / C::BN;
-
-  BfUnit w{};
-  if constexpr (MODE == kBfRowRuns) {
-    int g, m0, end;
-    const int mt = find_rows<C::BM>(p.offsets, p.groups, p.M, -1, lane, g, m0, end);
-    const int id = xcd_id(blockIdx.x, mt * nt);
-    if (id >= mt * nt) return;
-    int m, n;
-    raster(id, mt, nt, m, n);
-    find_rows<C::BM>(p.offsets, p.groups, p.M, m, lane, g, m0, end);
-    w.g = uniform(g);
-    w.m0 = uniform(m0);
-    w.n0 = uniform(n) * C::BN;
-    w.rows = uniform(end - m0);
-    w.ks = w.g < 0 ? 0 : p.K;
-  } else {
-    const int mt = (p.M + C::BM - 1) / C::BM;
-    const int tiles = mt * nt;
-    int id = xcd_id(blockIdx.x, tiles * (MODE == kBfKRuns ? p.groups : p.splits));
-    if (id >= tiles * (MODE == kBfKRuns ? p.groups : p.splits)) return;
-    int m, n;
-    const int part = id / tiles;
-    id -= part * tiles;
-    raster(id, mt, nt, m, n);
-    w.m0 = (int64_t)m * C::BM;
-    w.n0 = n * C::BN;
-    w.rows = p.M - (int)w.m0;
-    if constexpr (MODE == kBfKRuns) {
-      const int a = clamp_off(p.offsets[part], p.K), b = clamp_off(p.offsets[part + 1], p.K);
-      w.g = part;
-      w.k0 = uniform(a);
-      w.ks = uniform(max(b - a, 0));
-    } else {
-      const int steps = (p.K + kBK - 1) / kBK;
-      const int s0 = (int)((int64_t)part * steps / p.splits), s1 = (int)((int64_t)(part + 1) * steps / p.splits);
-      w.split = part;
-      w.tile = id;
-      w.k0 = (int64_t)s0 * kBK;
-      w.ks = min(p.K, s1 * kBK) - s0 * kBK;
-    }
-  }
+  BfUnit w;
+  if (!find_unit<C::BM, C::BN, MODE>(p, lane, w)) return;
 
   v4f acc[C::TM][C::TN];
 #pragma unroll
@@ -437,31 +512,408 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
   }
 }
 
+// ------------------------------------------------------- the 256 x 256 tile
+// Half of an operand's 256 x 64 tile: the 128 rows (m or n) that the waves
+// multiply together in one phase.  Row x of half h is tile row
+// (x / RUN) * 2 RUN + h * RUN + x % RUN, RUN being the rows of a wave's half.
+// A half is sixteen 1 KB copies, two a wave.
+template <bool KMAJOR, int RUN>
+struct HalfTile {
+  static constexpr int ROWS = 128, BYTES = ROWS * kBK * 2;
+  static constexpr int PITCH = KMAJOR ? ROWS * 2 : kBK * 2;
+  typedef Operand<KMAJOR, ROWS, 8> Frag;    // the layout inside a half
+
+  const char* base;
+  int64_t ld;
+  int64_t left;
+  uint32_t off[2][2];     // [half][copy]
+  int rem_k;
+
+  __device__ static int tile_row(int x, int h) { return x / RUN * (2 * RUN) + h * RUN + x % RUN; }
+
+  __device__ void init(const uint16_t* p, int64_t ld_elems, int64_t x0, int xs, int64_t k0, int ks,
+                       int wave, int lane) {
+    ld = ld_elems * 2;
+    rem_k = ks;
+    base = KMAJOR ? (const char*)(p + k0 * ld_elems + x0) : (const char*)(p + x0 * ld_elems + k0);
+    left = KMAJOR ? (int64_t)((xs < 256 ? xs + 7 : 256) & ~7) * 2 : (int64_t)((xs < 256 ? xs : 256) - 1) * ld;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = (wave * 2 + i) * 1024 + lane * 16;
+        if constexpr (KMAJOR) {
+          const int k = at / PITCH, c = tile_row(((at % PITCH / 16) ^ (Frag::gran(k) << 1)) * 8, h);
+          off[h][i] = c < xs ? (uint32_t)(k * ld) + c * 2 : kNowhere;
+        } else {
+          const int r = at / PITCH;
+          off[h][i] = (uint32_t)(tile_row(r, h) * ld) + (((at % PITCH / 16) ^ swz(r)) << 4);
+        }
+      }
+  }
+
+  // this wave's two copies of half h of k step kt into LDS; past the last step
+  // they copy zeros, so the count of copies in flight stays what the waits
+  // assume
+  __device__ void issue(int kt, int h, uint32_t lds, int wave, int lane) const {
+    const int rem = rem_k - kt * kBK;
+    const int64_t bytes = KMAJOR ? (int64_t)(rem - 1) * ld + left : left + (int64_t)((rem + 7) & ~7) * 2;
+    const v4i rs = resource(base + (int64_t)kt * (KMAJOR ? kBK * ld : kBK * 2), rem > 0 ? bytes : 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t o = off[h][i];
+      if constexpr (!KMAJOR) {
+        const int c = (lane & 7) ^ (4 * i + (lane >> 4));     // the chunk of k, swz(row) undone
+        o = c * 8 < rem ? o : kNowhere;
+      }
+      copy16(rs, o, uniform(lds + (uint32_t)(wave * 2 + i) * 1024));
+    }
+  }
+};
+
+// A copy of a per-lane value that the compiler cannot trace: what is computed
+// from it is computed here, not before the loop over units, where it would
+// take registers through the main loop.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Between the phases of the big tile: neither the compiler's memory accesses
+// nor its instruction scheduling move across.
+__device__ __forceinline__ void phase_fence() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void phase_barrier() {
+  phase_fence();
+  __builtin_amdgcn_s_barrier();
+  phase_fence();
+}
+
+// The epilogue of the big tile: `full` where every row and column of the tile
+// exists and rows are whole 16-byte pieces, so stores need no checks (and
+// their number is known).  EPI: bias, activation, residual and z are compiled in.
+//
+// Columns: a lane holds columns 4 g .. 4 g + 3 of two neighbouring 16-column
+// tiles.  As BF16 those are two dwords each; exchanging the odd 16-lane rows of
+// the first tile with the even ones of the second leaves each lane eight
+// neighbouring columns, one 16-byte store.
+__device__ __forceinline__ uint4 swap_columns(v4f a, v4f b) {
+  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+  const u2 lo = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(bf16x2(a[0], a[1]), bf16x2(b[0], b[1]), false, false));
+  const u2 hi = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(bf16x2(a[2], a[3]), bf16x2(b[2], b[3]), false, false));
+  return make_uint4(lo.x, hi.x, lo.y, hi.y);
+}
+__device__ __forceinline__ int swapped_column(int lane) { return (lane >> 4 & 1) * 16 + (lane >> 5) * 8; }
+
+__device__ __forceinline__ void stream16(void* to, uint4 v) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store(u4{v.x, v.y, v.z, v.w}, reinterpret_cast<u4*>(to));
+}
+
+// Eight BF16 or four FP32 columns from c on of the row at q, those below N.
+__device__ __forceinline__ void store_eight(uint16_t* q, int64_t ld, int c, int N, bool full, uint4 v) {
+  if (full) {
+    stream16(q + c, v);
+  } else if (ld % 8 == 0 && c + 8 <= N) {
+    *reinterpret_cast<uint4*>(q + c) = v;
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < N) q[c + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+  }
+}
+__device__ __forceinline__ void store_four(float* q, int64_t ld, int c, int N, bool full, v4f v) {
+  if (full) {
+    __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(q + c));
+  } else if (ld % 4 == 0 && c + 4 <= N) {
+    *reinterpret_cast<v4f*>(q + c) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < N) q[c + i] = v[i];
+  }
+}
+
+// (the exchange needs every lane; only live rows are stored)
+__device__ __forceinline__ void store_rows(void* to, int64_t ld, bool bf16, int64_t m, int n, int N,
+                                           int lane, bool full, bool live, v4f a, v4f b) {
+  if (bf16) {
+    const uint4 v = swap_columns(a, b);
+    if (live) store_eight((uint16_t*)to + m * ld, ld, n + swapped_column(lane), N, full, v);
+  } else if (live) {
+    store_four((float*)to + m * ld, ld, n + 4 * (lane >> 4), N, full, a);
+    store_four((float*)to + m * ld, ld, n + 16 + 4 * (lane >> 4), N, full, b);
+  }
+}
+
+// Eight waves, two a SIMD, in two groups of four: group 0 owns the upper 128
+// rows, group 1 the lower, wave q of a group columns 64 q .. 64 q + 63.  A k
+// step is four phases, one quadrant (64 x 32) of the wave's tile each: 16
+// MFMAs on fragments read once.  A phase is a memory part (fragment reads, two
+// copies of a later step) and an MFMA part with a workgroup barrier after
+// each; group 1 runs one part behind group 0, so on every SIMD one wave feeds
+// the matrix unit while the other one waits for memory.
+//
+//   phase   reads (step t)      copies                MFMAs on
+//   0       A half 0            B half 1 of t + 1     A0 B0
+//   1       B half 1            A half 1 of t + 1     A0 B1
+//   2       A half 1            A half 0 of t + 2     A1 B1
+//   3       B half 0 of t + 1   B half 0 of t + 2     A1 B0
+//
+// A copy may overwrite a half two parts after every wave has issued the last
+// read of it: a group waits for its reads at the head of its MFMA part, so by
+// then they are done.  (A0 of t: read in phase 0, overwritten from phase 2 of
+// the same step; the others are further apart.)  A copy has five phases or
+// more to land: each wave waits for its own, oldest first, in the phase before
+// the first read, and the barrier after that makes it everybody's.
+//
+// The grid is one workgroup a CU, each walking the units; a unit's first
+// copies are issued before the last unit's epilogue, which they run under.
+template <bool AK, bool BK, int MODE, bool EPI>
+__global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
+  typedef HalfTile<AK, 64> HalfA;
+  typedef HalfTile<BK, 32> HalfB;
+  constexpr uint32_t kHalf = HalfA::BYTES;         // LDS: per stage A0, A1, B0, B1
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[8 * kHalf];
+  __shared__ RunTable<MODE == kBfRowRuns ? kMaxRuns : 1> runs;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wave >> 2, q = wave & 3;
+  const int nt = (p.N + 255) / 256;
+  int mt = (p.M + 255) / 256;
+  if constexpr (MODE == kBfRowRuns) {
+    if (wave == 0) fill_runs<256>(runs, p.offsets, p.groups, p.M, lane);
+    __syncthreads();
+    mt = uniform(runs.sum[p.groups + 1]);
+  }
+  const int total = mt * nt * (MODE == kBfKRuns ? p.groups : 1), G = p.grid;
+
+  auto find = [&](int u, BfUnit& w) {
+    int id = xcd_round(u, total, G), m, n;
+    w = BfUnit{};
+    if constexpr (MODE == kBfRowRuns) {
+      raster(id, mt, nt, m, n);
+      int m0;
+      look_up_run<256>(runs, p.groups, m, w.g, m0, w.rows);
+      w.m0 = m0;
+      w.ks = w.g < 0 ? 0 : p.K;
+    } else {
+      const int part = MODE == kBfKRuns ? id / (mt * nt) : 0;
+      raster(id - part * (mt * nt), mt, nt, m, n);
+      w.m0 = (int64_t)m * 256;
+      w.rows = p.M - (int)w.m0;
+      w.ks = p.K;
+      w.g = part;
+      if constexpr (MODE == kBfKRuns) {
+        const int a = clamp_off(p.offsets[part], p.K), b = clamp_off(p.offsets[part + 1], p.K);
+        w.k0 = uniform(a);
+        w.ks = uniform(max(b - a, 0));
+      }
+    }
+    w.n0 = n * 256;
+  };
+
+  HalfA a;
+  HalfB b;
+  const uint32_t lds0 = lds_addr(smem);
+  auto copy_a = [&](int t, int h) { a.issue(t, h, lds0 + ((t & 1) * 4 + h) * kHalf, wave, lane); };
+  auto copy_b = [&](int t, int h) { b.issue(t, h, lds0 + ((t & 1) * 4 + 2 + h) * kHalf, wave, lane); };
+  auto start = [&](const BfUnit& w) {     // the first twelve copies of a unit
+    const int here = opaque(lane);
+    a.init(p.a, p.lda, w.m0, w.rows, w.k0, w.ks, wave, here);
+    b.init(p.b + (MODE == kBfRowRuns ? w.g * p.b_stride : 0), p.ldb, w.n0, p.N - w.n0, w.k0, w.ks, wave, here);
+    copy_a(0, 0);
+    copy_b(0, 0);
+    copy_b(0, 1);
+    copy_a(0, 1);
+    copy_a(1, 0);
+    copy_b(1, 0);
+  };
+
+  BfUnit w;
+  int u = blockIdx.x;
+  if (u >= total) return;
+  find(u, w);
+  if (w.ks > 0) start(w);
+  while (true) {
+    v4f acc[2][4][2][2];    // [A half][row tile][B half][column tile]
+#pragma unroll
+    for (int i = 0; i < 32; ++i) (&acc[0][0][0][0])[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    const int steps = (w.ks + kBK - 1) / kBK;
+    if (steps > 0) {
+      v8bf fa[4][2], fb[2][2][2], fb1[2][2];       // A half in use; B half 0 of two steps; B half 1
+      auto read_a = [&](int st, int h) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            fa[i][kk] = HalfA::Frag::frag(smem + (st * 4 + h) * kHalf, grp * 64 + 16 * i, kk, lane);
+      };
+      auto read_b = [&](v8bf (&f)[2][2], int st, int h) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            f[j][kk] = HalfB::Frag::frag(smem + (st * 4 + 2 + h) * kHalf, q * 32 + 16 * j, kk, lane);
+      };
+      auto multiply = [&](auto ha, auto hb, v8bf (&f)[2][2]) {
+        phase_barrier();
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[ha][i][hb][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[j][kk], fa[i][kk], acc[ha][i][hb][j], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+        phase_barrier();
+      };
+      constexpr std::integral_constant<int, 0> c0{};
+      constexpr std::integral_constant<int, 1> c1{};
+      wait_vmcnt<8>();              // A0 and B0 of step 0
+      phase_barrier();
+      read_b(fb[0], 0, 0);
+      if (grp == 1) phase_barrier();
+      auto step = [&](auto par, int t) {
+        constexpr int P = decltype(par)::value;
+        read_a(P, 0);
+        copy_b(t + 1, 1);
+        wait_vmcnt<8>();            // B1 of step t
+        multiply(c0, c0, fb[P]);
+        read_b(fb1, P, 1);
+        copy_a(t + 1, 1);
+        wait_vmcnt<8>();            // A1 of step t
+        multiply(c0, c1, fb1);
+        read_a(P, 1);
+        copy_a(t + 2, 0);
+        wait_vmcnt<6>();            // A0 and B0 of step t + 1
+        multiply(c1, c1, fb1);
+        read_b(fb[P ^ 1], P ^ 1, 0);
+        copy_b(t + 2, 0);
+        multiply(c1, c0, fb[P]);
+      };
+      for (int t = 0; t < steps; t += 2) {
+        step(c0, t);
+        if (t + 1 < steps) step(c1, t + 1);
+      }
+      if (grp == 0) phase_barrier();
+      wait_vmcnt<0>();              // (the copies of zeros past the last step)
+      __syncthreads();              // every wave's, and its reads
+    }
+
+    // the next unit's first copies, under this one's epilogue
+    BfUnit next{};
+    u += G;
+    if (u < total) {
+      find(u, next);
+      if (next.ks > 0) start(next);
+    }
+
+    const int here = opaque(lane);
+    char* d = (char*)p.d + (int64_t)(MODE == kBfKRuns ? w.g : 0) * p.d_stride * (p.out_bf16 ? 2 : 4);
+    const int per = p.out_bf16 ? 8 : 4;
+    const bool full = w.rows >= 256 && w.n0 + 256 <= p.N && p.ldd % per == 0;
+    const int n1 = w.n0 + q * 64;
+    v4f bias[2][2];
+    if constexpr (EPI) {
+#pragma unroll
+      for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) bias[hb][j] = bias4(p, n1 + hb * 32 + 16 * j + 4 * (here >> 4));
+    }
+#pragma unroll
+    for (int ha = 0; ha < 2; ++ha) {
+      const int r0 = grp * 128 + ha * 64 + (here & 15);
+      uint2 res[4][2][2];
+      if constexpr (EPI) {
+        if (p.residual) {       // all of a half's loads before its stores
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (r0 + 16 * i < w.rows)
+                res[i][k / 2][k % 2] = residual4(p, w.m0 + r0 + 16 * i, n1 + k / 2 * 32 + k % 2 * 16 + 4 * (here >> 4));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t m = w.m0 + r0 + 16 * i;
+        const bool live = r0 + 16 * i < w.rows;
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {
+          v4f v[2] = {acc[ha][i][hb][0], acc[ha][i][hb][1]};
+          const int n = n1 + hb * 32;
+          if constexpr (EPI) {
+            v[0] += bias[hb][0];
+            v[1] += bias[hb][1];
+            if (p.z) store_rows(p.z, p.ldz, true, m, n, p.N, here, full && p.ldz % 8 == 0, live, v[0], v[1]);
+            if (p.act != kActNone) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e / 4][e % 4] = act_of(p.act, v[e / 4][e % 4]);
+            }
+            if (p.residual) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint2 r = res[i][hb][j];
+                v[j] += v4f{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
+                            __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u)};
+              }
+            }
+          }
+          store_rows(d, p.ldd, p.out_bf16, m, n, p.N, here, full, live, v[0], v[1]);
+        }
+      }
+    }
+    if (u >= total) return;
+    w = next;
+  }
+}
+
 // ------------------------------------------------------------------- host
-// Tile configurations.  Large: 128 accumulators a lane, two waves a SIMD.
-using BfHuge = BfCfg<256, 256, 2, 4, 2, 2>;
+// Tile configurations beside the 256 x 256 one.
 using BfMid = BfCfg<128, 128, 2, 2, 3, 1>;
 using BfLow = BfCfg<64, 64, 2, 2, 4, 2>;
 using BfThin = BfCfg<16, 64, 1, 4, 7, 2>;
 
 namespace {
 
+// Workgroups for tiles of bm x bn, a multiple of the eight XCDs.
+unsigned grid_of(const BfProblem& p, int bm, int bn) {
+  const int64_t nt = ((int64_t)p.N + bn - 1) / bn;
+  int64_t units = ((int64_t)p.M + bm - 1) / bm * nt;
+  // row runs: a run may end inside a tile, so one more tile a run at most
+  if (p.mode == kBfRowRuns) units += (int64_t)(p.groups + 1) * nt;
+  if (p.mode == kBfKRuns) units *= p.groups;
+  if (p.mode == kBfDense) units *= p.splits;
+  return (unsigned)((units + 7) / 8 * 8);
+}
+
 template <class C, bool AK, bool BK, int MODE>
 hipError_t launch_as(const BfProblem& p, hipStream_t stream) {
-  const int64_t nt = (p.N + C::BN - 1) / C::BN;
-  int64_t units = (p.M + C::BM - 1) / C::BM * nt;
-  // row runs: a run may end inside a tile, so one more tile a run at most
-  if (MODE == kBfRowRuns) units = ((int64_t)(p.M + C::BM - 1) / C::BM + p.groups + 1) * nt;
-  if (MODE == kBfKRuns) units *= p.groups;
-  if (MODE == kBfDense) units *= p.splits;
-  const int64_t grid = (units + 7) / 8 * 8;
-  hipLaunchKernelGGL((bf16_kernel<C, AK, BK, MODE>), dim3((unsigned)grid), dim3(C::THREADS), 0, stream, p);
+  hipLaunchKernelGGL((bf16_kernel<C, AK, BK, MODE>), dim3(grid_of(p, C::BM, C::BN)), dim3(C::THREADS), 0,
+                     stream, p);
   return hipGetLastError();
 }
 
 template <bool AK, bool BK, int MODE>
 hipError_t launch_tile(const BfProblem& p, const BfTile& t, hipStream_t stream) {
-  if (t.cfg == 0) return launch_as<BfHuge, AK, BK, MODE>(p, stream);
+  if (t.cfg == 0) {
+    BfProblem q = p;
+    const unsigned units = grid_of(p, 256, 256), cus = (unsigned)device_cu_count();
+    q.grid = (int)(units < cus ? units : cus);
+    constexpr bool kMayEpi = MODE == kBfDense && !AK && !BK;
+    if constexpr (kMayEpi) {
+      if (p.bias || p.act != kActNone || p.residual || p.z) {
+        hipLaunchKernelGGL((bf16_big_kernel<AK, BK, MODE, true>), dim3(q.grid), dim3(512), 0, stream, q);
+        return hipGetLastError();
+      }
+    }
+    hipLaunchKernelGGL((bf16_big_kernel<AK, BK, MODE, false>), dim3(q.grid), dim3(512), 0, stream, q);
+    return hipGetLastError();
+  }
   if (t.cfg == 1) return launch_as<BfMid, AK, BK, MODE>(p, stream);
   if constexpr (AK) {
     return launch_as<BfLow, AK, BK, MODE>(p, stream);
@@ -474,8 +926,8 @@ hipError_t launch_tile(const BfProblem& p, const BfTile& t, hipStream_t stream) 
 }  // namespace
 
 BfTile bf16_tile(const BfProblem& p, int cus) {
-  static constexpr int kBm[] = {BfHuge::BM, BfMid::BM, BfLow::BM, BfThin::BM};
-  static constexpr int kBn[] = {BfHuge::BN, BfMid::BN, BfLow::BN, BfThin::BN};
+  static constexpr int kBm[] = {256, BfMid::BM, BfLow::BM, BfThin::BM};
+  static constexpr int kBn[] = {256, BfMid::BN, BfLow::BN, BfThin::BN};
   BfTile t{};
   // rows of one tile column: a run's average for the row runs
   const int64_t rows = p.mode == kBfRowRuns ? (p.M + p.groups - 1) / p.groups : p.M;

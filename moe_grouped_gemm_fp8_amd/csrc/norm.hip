@@ -383,8 +383,11 @@ __device__ __forceinline__ float act_slope(int act, float z) {
     const float p = 1.f / (1.f + __expf(-z));
     return p * (1.f + z * (1.f - p));
   }
-  if (act == kActGelu)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * (__expf(-0.5f * z * z) * 0.39894228040143268f);
+  if (act == kActGelu) {
+    float bell;
+    const float cdf = normal_cdf(z, &bell);
+    return fmaf(z, bell * 0.39894228040143268f, cdf);
+  }
   return 1.f;
 }
 
