@@ -410,6 +410,34 @@ struct BfOut {
   }
 };
 
+// ---------------------------------------------------------------- split k
+// Every split publishes its FP32 tile past the caches of its XCD and counts
+// itself in; the last one to arrive adds them up in the order of the splits
+// (the same bits on every call) and leaves the counter at zero.  False: this
+// workgroup is not the last.
+__device__ __forceinline__ bool last_of_splits(const BfProblem& p, const BfUnit& w, int tid, int* last) {
+  wait_all_memory();        // this thread's part has reached the point of coherence
+  __syncthreads();          // ... and every other thread's
+  if (tid == 0) {
+    *last = __hip_atomic_fetch_add(p.counters + w.tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
+    if (*last) __hip_atomic_store(p.counters + w.tile, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return *last;
+}
+// One value's parts: all loads are issued before the first is added.
+__device__ __forceinline__ v4f sum_splits(__amdgpu_buffer_rsrc_t ws, uint32_t tile, uint32_t at, int splits) {
+  v4f part[kBfMaxSplits], sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < kBfMaxSplits; ++s)
+    if (s < splits)
+      part[s] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(ws, s * tile + at, 0, kCoherent));
+#pragma unroll
+  for (int s = 0; s < kBfMaxSplits; ++s)
+    if (s < splits) sum += part[s];
+  return sum;
+}
+
 // ------------------------------------------------------------------ kernel
 template <class C, bool AK, bool BK, int MODE>
 __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
@@ -468,9 +496,6 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
     }
   }
 
-  // ---- split k: every split publishes its FP32 tile past the caches of its
-  // XCD, the last one to arrive adds them up in the order of the splits (the
-  // same bits on every call) and leaves the counter at zero
   if (MODE == kBfDense && p.splits > 1) {
     constexpr uint32_t kTile = C::BM * C::BN * 4;
     const __amdgpu_buffer_rsrc_t ws =
@@ -482,23 +507,19 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, acc[i][j]), ws,
                                                w.split * kTile + (((wave * C::TM + i) * C::TN + j) * 64 + lane) * 16,
                                                0, kCoherent);
-    wait_all_memory();
-    __syncthreads();
-    if (tid == 0)
-      last = __hip_atomic_fetch_add(p.counters + w.tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.splits - 1;
-    __syncthreads();
-    if (!last) return;
+    if (!last_of_splits(p, w, tid, &last)) return;
+    // (a split's tiles are loaded together, one split after the other: all
+    // splits at once would not fit in registers)
+    for (int s = 0; s < p.splits; ++s)
 #pragma unroll
-    for (int i = 0; i < C::TM; ++i)
+      for (int i = 0; i < C::TM; ++i)
 #pragma unroll
-      for (int j = 0; j < C::TN; ++j) {
-        const uint32_t at = (((wave * C::TM + i) * C::TN + j) * 64 + lane) * 16;
-        v4f sum = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < p.splits; ++s)
-          sum += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(ws, s * kTile + at, 0, kCoherent));
-        acc[i][j] = sum;
-      }
-    if (tid == 0) __hip_atomic_store(p.counters + w.tile, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        for (int j = 0; j < C::TN; ++j) {
+          const v4f v = __builtin_bit_cast(
+              v4f, __builtin_amdgcn_raw_buffer_load_b128(
+                       ws, s * kTile + (((wave * C::TM + i) * C::TN + j) * 64 + lane) * 16, 0, kCoherent));
+          acc[i][j] = s == 0 ? v : acc[i][j] + v;
+        }
   }
 
   const BfOut out(p, w.g);
@@ -509,6 +530,120 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
 #pragma unroll
       for (int j = 0; j < C::TN; ++j) out.four(w.m0 + r, w.n0 + wn0 + 16 * j + 4 * (lane >> 4), acc[i][j]);
     }
+  }
+}
+
+// ------------------------------------------------------------ few rows
+// At most 16 TM rows a run, both operands k-contiguous: the time is that of
+// streaming the weights once.  The eight waves of a workgroup split k among
+// themselves, 64 at a time in turn, and each loads its fragments of both
+// operands straight into registers (16 bytes a lane, a lane's k are
+// contiguous): no LDS and no barrier stands between a wave and its loads, and
+// 2 U steps of them are in flight.  The waves' sums meet in LDS at the end.
+template <int TM, int TN, int U, int MODE>
+__global__ __launch_bounds__(512, 2) void bf16_few_kernel(BfProblem p) {
+  constexpr int BM = 16 * TM, BN = 16 * TN, TILES = TM * TN;
+  __shared__ v4f sums[8][TILES][64];
+  __shared__ int last;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  BfUnit w;
+  if (!find_unit<BM, BN, MODE>(p, lane, w)) return;
+  const int i = lane & 15, g = lane >> 4;
+
+  v4f acc[TM][TN];
+#pragma unroll
+  for (int a = 0; a < TILES; ++a) (&acc[0][0])[a] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int steps = (w.ks + kBK - 1) / kBK;
+  // Offsets of a lane's row in the run's (column's) tile; rows and columns past
+  // the end read the last one and are not stored.  k goes into the scalar
+  // offset, and a lane whose k lies past the end of the run loads zeros.
+  const uint16_t* xp = p.a + w.m0 * p.lda + w.k0;
+  const uint16_t* wp = p.b + (MODE == kBfRowRuns ? max(w.g, 0) * p.b_stride : 0) + (int64_t)w.n0 * p.ldb + w.k0;
+  const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(uniform((const void*)xp), 0x7fffffff);
+  const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(uniform((const void*)wp), 0x7fffffff);
+  uint32_t xo[TM], wo[TN];
+#pragma unroll
+  for (int t = 0; t < TM; ++t) xo[t] = (uint32_t)(min(16 * t + i, w.rows - 1) * (int)p.lda + 8 * g) * 2;
+#pragma unroll
+  for (int t = 0; t < TN; ++t) wo[t] = (uint32_t)(min(16 * t + i, p.N - 1 - w.n0) * (int)p.ldb + 8 * g) * 2;
+  struct Batch {
+    v4i x[U][2][TM], w[U][2][TN];
+  };
+  // steps s0, s0 + 8, .. of this wave
+  auto fetch = [&](Batch& f, int s0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const int k = uniform((s0 + 8 * u) * kBK + 32 * kk);
+        const bool in = 8 * g < w.ks - k;
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+          f.w[u][kk][t] = __builtin_bit_cast(
+              v4i, __builtin_amdgcn_raw_buffer_load_b128(wr, in ? wo[t] : kNowhere, k * 2, kStream));
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+          f.x[u][kk][t] = __builtin_bit_cast(
+              v4i, __builtin_amdgcn_raw_buffer_load_b128(xr, in ? xo[t] : kNowhere, k * 2, 0));
+      }
+  };
+  auto multiply = [&](const Batch& f) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int b = 0; b < TN; ++b)
+#pragma unroll
+          for (int a = 0; a < TM; ++a)
+            acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, f.w[u][kk][b]),
+                                                                __builtin_bit_cast(v8bf, f.x[u][kk][a]),
+                                                                acc[a][b], 0, 0, 0);
+  };
+  if (wave < steps) {
+    Batch f0, f1;
+    fetch(f0, wave);
+    for (int s = wave; s < steps; s += 16 * U) {
+      fetch(f1, s + 8 * U);
+      multiply(f0);
+      if (s + 8 * U >= steps) break;
+      fetch(f0, s + 16 * U);
+      multiply(f1);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) sums[wave][t][lane] = (&acc[0][0])[t];
+  __syncthreads();
+  // tile t's sum goes to wave t mod 8
+  constexpr int MINE = (TILES + 7) / 8;
+  v4f mine[MINE];
+#pragma unroll
+  for (int j = 0; j < MINE; ++j) {
+    const int t = wave + 8 * j;
+    mine[j] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (t < TILES)
+#pragma unroll
+      for (int v = 0; v < 8; ++v) mine[j] += sums[v][t][lane];
+  }
+  if (MODE == kBfDense && p.splits > 1) {
+    constexpr uint32_t kTile = BM * BN * 4;
+    const __amdgpu_buffer_rsrc_t ws =
+        buffer_rsrc(p.partial + (int64_t)w.tile * p.splits * (BM * BN), kTile * p.splits);
+#pragma unroll
+    for (int j = 0; j < MINE; ++j)
+      if (wave + 8 * j < TILES)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, mine[j]), ws,
+                                               w.split * kTile + ((wave + 8 * j) * 64 + lane) * 16, 0, kCoherent);
+    if (!last_of_splits(p, w, tid, &last)) return;
+#pragma unroll
+    for (int j = 0; j < MINE; ++j)
+      if (wave + 8 * j < TILES) mine[j] = sum_splits(ws, kTile, ((wave + 8 * j) * 64 + lane) * 16, p.splits);
+  }
+  const BfOut out(p, w.g);
+#pragma unroll
+  for (int j = 0; j < MINE; ++j) {
+    const int t = wave + 8 * j, r = 16 * (t / TN) + i;
+    if (t < TILES && r < w.rows) out.four(w.m0 + r, w.n0 + 16 * (t % TN) + 4 * g, mine[j]);
   }
 }
 
@@ -607,6 +742,9 @@ __device__ __forceinline__ uint4 swap_columns(v4f a, v4f b) {
 }
 __device__ __forceinline__ int swapped_column(int lane) { return (lane >> 4 & 1) * 16 + (lane >> 5) * 8; }
 
+// (with the non-temporal hint the BF16 tiles of 8191 x 7168 x 2048 took 300 us
+// for 334 without; FP32 tiles, whose 256 KB drain under the next unit, ran 5%
+// slower with it and go without)
 __device__ __forceinline__ void stream16(void* to, uint4 v) {
   typedef uint32_t u4 __attribute__((ext_vector_type(4)));
   __builtin_nontemporal_store(u4{v.x, v.y, v.z, v.w}, reinterpret_cast<u4*>(to));
@@ -626,9 +764,7 @@ __device__ __forceinline__ void store_eight(uint16_t* q, int64_t ld, int c, int 
   }
 }
 __device__ __forceinline__ void store_four(float* q, int64_t ld, int c, int N, bool full, v4f v) {
-  if (full) {
-    __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(q + c));
-  } else if (ld % 4 == 0 && c + 4 <= N) {
+  if (full || (ld % 4 == 0 && c + 4 <= N)) {
     *reinterpret_cast<v4f*>(q + c) = v;
   } else {
 #pragma unroll
@@ -651,24 +787,25 @@ __device__ __forceinline__ void store_rows(void* to, int64_t ld, bool bf16, int6
 
 // Eight waves, two a SIMD, in two groups of four: group 0 owns the upper 128
 // rows, group 1 the lower, wave q of a group columns 64 q .. 64 q + 63.  A k
-// step is four phases, one quadrant (64 x 32) of the wave's tile each: 16
-// MFMAs on fragments read once.  A phase is a memory part (fragment reads, two
-// copies of a later step) and an MFMA part with a workgroup barrier after
-// each; group 1 runs one part behind group 0, so on every SIMD one wave feeds
-// the matrix unit while the other one waits for memory.
+// step is two phases, half of the wave's rows each: 32 MFMAs on fragments that
+// are read once.  A phase is a memory part (fragment reads, four copies of a
+// later step) and an MFMA part, with a workgroup barrier after each; group 1
+// runs one part behind group 0, so on every SIMD one wave feeds the matrix
+// unit while the other one waits for memory.  (Four phases of 16 MFMAs ran
+// 8% slower: every change of the wave that feeds the unit costs a barrier.)
 //
-//   phase   reads (step t)      copies                MFMAs on
-//   0       A half 0            B half 1 of t + 1     A0 B0
-//   1       B half 1            A half 1 of t + 1     A0 B1
-//   2       A half 1            A half 0 of t + 2     A1 B1
-//   3       B half 0 of t + 1   B half 0 of t + 2     A1 B0
+//   phase   reads of step t             copies                   MFMAs on
+//   0       B half 1, A half 0          A0 and B1 of t + 1       A0 B0, A0 B1
+//   1       B half 0 of t + 1, A half 1 A1 of t + 1, B0 of t + 2 A1 B1, A1 B0
 //
-// A copy may overwrite a half two parts after every wave has issued the last
-// read of it: a group waits for its reads at the head of its MFMA part, so by
-// then they are done.  (A0 of t: read in phase 0, overwritten from phase 2 of
-// the same step; the others are further apart.)  A copy has five phases or
-// more to land: each wave waits for its own, oldest first, in the phase before
-// the first read, and the barrier after that makes it everybody's.
+// Number the parts of group 0 from 4 t (phase 0 of step t, memory), those of
+// group 1 one later.  A wave has its reads of a memory part by the end of the
+// MFMA part after it (LDS reads return in order, and each part's last ones are
+// used there), so what was read in part s by group 0 is read by everybody
+// before part s + 3.  A0 and B1 of t (s = 4 t) are overwritten from part 4 t + 4
+// on, A1 of t and B0 of t + 1 (s = 4 t + 2) from part 4 t + 6.  A wave waits
+// for its own copies in the memory part before the first read of them, and the
+// barrier after that makes it everybody's: a copy has a whole step to land.
 //
 // The grid is one workgroup a CU, each walking the units; a unit's first
 // copies are issued before the last unit's epilogue, which they run under.
@@ -728,7 +865,6 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
     copy_b(0, 0);
     copy_b(0, 1);
     copy_a(0, 1);
-    copy_a(1, 0);
     copy_b(1, 0);
   };
 
@@ -758,7 +894,8 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
           for (int j = 0; j < 2; ++j)
             f[j][kk] = HalfB::Frag::frag(smem + (st * 4 + 2 + h) * kHalf, q * 32 + 16 * j, kk, lane);
       };
-      auto multiply = [&](auto ha, auto hb, v8bf (&f)[2][2]) {
+      // 32 MFMAs: row half ha against column halves hb, then the other one
+      auto multiply = [&](auto ha, v8bf (&f)[2][2], auto hb, v8bf (&f2)[2][2]) {
         phase_barrier();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -768,32 +905,37 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               acc[ha][i][hb][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[j][kk], fa[i][kk], acc[ha][i][hb][j], 0, 0, 0);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[ha][i][1 - hb][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f2[j][kk], fa[i][kk], acc[ha][i][1 - hb][j], 0, 0, 0);
         __builtin_amdgcn_s_setprio(0);
         phase_barrier();
       };
       constexpr std::integral_constant<int, 0> c0{};
       constexpr std::integral_constant<int, 1> c1{};
-      wait_vmcnt<8>();              // A0 and B0 of step 0
+      wait_vmcnt<4>();              // step 0 but for A1
       phase_barrier();
       read_b(fb[0], 0, 0);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (grp == 1) phase_barrier();
       auto step = [&](auto par, int t) {
         constexpr int P = decltype(par)::value;
-        read_a(P, 0);
-        copy_b(t + 1, 1);
-        wait_vmcnt<8>();            // B1 of step t
-        multiply(c0, c0, fb[P]);
         read_b(fb1, P, 1);
-        copy_a(t + 1, 1);
-        wait_vmcnt<8>();            // A1 of step t
-        multiply(c0, c1, fb1);
-        read_a(P, 1);
-        copy_a(t + 2, 0);
-        wait_vmcnt<6>();            // A0 and B0 of step t + 1
-        multiply(c1, c1, fb1);
+        read_a(P, 0);
+        copy_a(t + 1, 0);
+        copy_b(t + 1, 1);
+        wait_vmcnt<4>();            // A1 of step t, B0 of step t + 1
+        multiply(c0, fb[P], c0, fb1);
         read_b(fb[P ^ 1], P ^ 1, 0);
+        read_a(P, 1);
+        copy_a(t + 1, 1);
         copy_b(t + 2, 0);
-        multiply(c1, c0, fb[P]);
+        wait_vmcnt<4>();            // A0 and B1 of step t + 1
+        multiply(c1, fb1, c1, fb[P]);
       };
       for (int t = 0; t < steps; t += 2) {
         step(c0, t);
@@ -873,10 +1015,13 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
 }
 
 // ------------------------------------------------------------------- host
-// Tile configurations beside the 256 x 256 one.
-using BfMid = BfCfg<128, 128, 2, 2, 3, 1>;
+// Tile configurations.  kBig: bf16_big_kernel; kMid, kLow: bf16_kernel, with
+// two workgroups a CU; kFew..: bf16_few_kernel of 16, 32 or 64 rows.
+enum { kBig = 0, kMid, kLow, kFew16, kFew32, kFew64, kConfigs };
+using BfMid = BfCfg<128, 128, 2, 2, 2, 2>;
 using BfLow = BfCfg<64, 64, 2, 2, 4, 2>;
-using BfThin = BfCfg<16, 64, 1, 4, 7, 2>;
+constexpr int kBm[kConfigs] = {256, BfMid::BM, BfLow::BM, 16, 32, 64};
+constexpr int kBn[kConfigs] = {256, BfMid::BN, BfLow::BN, 16, 32, 32};
 
 namespace {
 
@@ -891,60 +1036,53 @@ unsigned grid_of(const BfProblem& p, int bm, int bn) {
   return (unsigned)((units + 7) / 8 * 8);
 }
 
-template <class C, bool AK, bool BK, int MODE>
-hipError_t launch_as(const BfProblem& p, hipStream_t stream) {
-  hipLaunchKernelGGL((bf16_kernel<C, AK, BK, MODE>), dim3(grid_of(p, C::BM, C::BN)), dim3(C::THREADS), 0,
-                     stream, p);
+template <class K>
+hipError_t start(K kernel, const BfProblem& p, unsigned grid, int threads, hipStream_t stream) {
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, stream, p);
   return hipGetLastError();
 }
 
 template <bool AK, bool BK, int MODE>
-hipError_t launch_tile(const BfProblem& p, const BfTile& t, hipStream_t stream) {
-  if (t.cfg == 0) {
-    BfProblem q = p;
-    const unsigned units = grid_of(p, 256, 256), cus = (unsigned)device_cu_count();
-    q.grid = (int)(units < cus ? units : cus);
-    constexpr bool kMayEpi = MODE == kBfDense && !AK && !BK;
-    if constexpr (kMayEpi) {
-      if (p.bias || p.act != kActNone || p.residual || p.z) {
-        hipLaunchKernelGGL((bf16_big_kernel<AK, BK, MODE, true>), dim3(q.grid), dim3(512), 0, stream, q);
-        return hipGetLastError();
-      }
-    }
-    hipLaunchKernelGGL((bf16_big_kernel<AK, BK, MODE, false>), dim3(q.grid), dim3(512), 0, stream, q);
-    return hipGetLastError();
+hipError_t launch_tile(BfProblem p, const BfTile& t, hipStream_t stream) {
+  const unsigned units = grid_of(p, t.bm, t.bn);
+  if constexpr (!AK && !BK) {
+    if (t.cfg == kFew16) return start(bf16_few_kernel<1, 1, 4, MODE>, p, units, 512, stream);
+    if (t.cfg == kFew32) return start(bf16_few_kernel<2, 2, 3, MODE>, p, units, 512, stream);
+    if (t.cfg == kFew64) return start(bf16_few_kernel<4, 2, 2, MODE>, p, units, 512, stream);
   }
-  if (t.cfg == 1) return launch_as<BfMid, AK, BK, MODE>(p, stream);
-  if constexpr (AK) {
-    return launch_as<BfLow, AK, BK, MODE>(p, stream);
-  } else {
-    if (t.cfg == 2) return launch_as<BfLow, AK, BK, MODE>(p, stream);
-    return launch_as<BfThin, AK, BK, MODE>(p, stream);
+  if (t.cfg == kLow) return start(bf16_kernel<BfLow, AK, BK, MODE>, p, units, BfLow::THREADS, stream);
+  if (t.cfg == kMid) return start(bf16_kernel<BfMid, AK, BK, MODE>, p, units, BfMid::THREADS, stream);
+  const unsigned cus = (unsigned)device_cu_count();
+  p.grid = (int)(units < cus ? units : cus);
+  if constexpr (MODE == kBfDense && !AK && !BK) {
+    if (p.bias || p.act != kActNone || p.residual || p.z)
+      return start(bf16_big_kernel<AK, BK, MODE, true>, p, p.grid, 512, stream);
   }
+  return start(bf16_big_kernel<AK, BK, MODE, false>, p, p.grid, 512, stream);
 }
 
 }  // namespace
 
 BfTile bf16_tile(const BfProblem& p, int cus) {
-  static constexpr int kBm[] = {256, BfMid::BM, BfLow::BM, BfThin::BM};
-  static constexpr int kBn[] = {256, BfMid::BN, BfLow::BN, BfThin::BN};
   BfTile t{};
   // rows of one tile column: a run's average for the row runs
   const int64_t rows = p.mode == kBfRowRuns ? (p.M + p.groups - 1) / p.groups : p.M;
   const int64_t runs = p.mode == kBfDense ? 1 : p.groups;
-  auto units = [&](int c) { return runs * ((rows + kBm[c] - 1) / kBm[c]) * ((p.N + kBn[c] - 1) / kBn[c]); };
-  if (units(0) >= cus) t.cfg = 0;
-  else if (rows > 64 && (p.N > 64 || !p.a_kmajor)) t.cfg = 1;
-  else if (rows > 16 || p.a_kmajor) t.cfg = 2;
-  else t.cfg = 3;
+  auto units = [&](int c) { return runs * ((rows + kBm[c] - 1) / kBm[c]) * (((int64_t)p.N + kBn[c] - 1) / kBn[c]); };
+  const bool few = !p.a_kmajor && !p.b_kmajor;
+  if (few && rows <= 64) t.cfg = rows <= 16 ? kFew16 : rows <= 32 ? kFew32 : kFew64;
+  else if (rows > 64 && units(kBig) * 5 >= cus * 2) t.cfg = kBig;
+  else if (rows > 64 && p.N > 64) t.cfg = kMid;
+  else t.cfg = kLow;
   t.bm = kBm[t.cfg];
   t.bn = kBn[t.cfg];
   t.splits = 1;
-  if (p.mode == kBfDense) {
+  if (p.mode == kBfDense && t.cfg != kBig) {
     const int64_t u = units(t.cfg), steps = (p.K + kBK - 1) / kBK;
     if (u < cus && u <= kSplitKMaxTiles) {
       int64_t s = cus / u;
-      if (s > steps / 4) s = steps / 4;
+      const int64_t least = t.cfg >= kFew16 ? 8 : 4;     // steps of a split
+      if (s > steps / least) s = steps / least;
       if (s > kBfMaxSplits) s = kBfMaxSplits;
       if (s > 1) t.splits = (int)s;
     }

@@ -62,14 +62,20 @@ struct Piece {
   }
 };
 
-// N parameter values from element c on (0 past cols), FP32 or BF16
+// N parameter values from element c on (0 past cols), FP32 or BF16, in
+// 16-byte loads where all of them exist
 template <int N>
 __device__ __forceinline__ void params(const void* p, bool bf16, int64_t c, int64_t cols, float* f) {
+  if (bf16) {
+    float w[8];
+    RowVec<uint16_t>::widen(c < cols ? Piece<uint16_t>::load((const uint16_t*)p, c, cols) : make_uint4(0, 0, 0, 0), w);
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    f[i] = c + i < cols ? (bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p)[c + i] << 16)
-                                : ((const float*)p)[c + i])
-                        : 0.f;
+    for (int i = 0; i < N; ++i) f[i] = w[i];
+  } else {
+#pragma unroll
+    for (int h = 0; h < N; h += 4)
+      RowVec<float>::widen(c + h < cols ? Piece<float>::load((const float*)p, c + h, cols) : make_uint4(0, 0, 0, 0), f + h);
+  }
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -106,71 +112,100 @@ constexpr int threads_of() { return WAVES == 1 ? 256 : 64 * WAVES; }
 template <int WAVES>
 constexpr int teams_of() { return WAVES == 1 ? 4 : 1; }
 
+// What a thread of a team holds: NV pieces of N columns each.  LEAN (the
+// longest rows, sixteen waves of 128 registers a lane): no row ahead in
+// registers, and the weight is read again for every row.
+template <class T, int WAVES, int NV, bool BACKWARD>
+struct Team {
+  static constexpr int N = Piece<T>::N;
+  static constexpr bool LEAN = NV * N > 16 || (BACKWARD && WAVES == 16);
+  int lane, wave, me, cols;
+  int64_t team, teams;
+  __device__ Team(int cols_) : cols(cols_) {
+    lane = threadIdx.x & 63;
+    wave = threadIdx.x >> 6;
+    me = WAVES == 1 ? lane : threadIdx.x;
+    team = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+    teams = (int64_t)gridDim.x * teams_of<WAVES>();
+  }
+  __device__ int column(int i) const { return (i * 64 * WAVES + me) * N; }
+  __device__ void load(const T* row, uint4 (&raw)[NV]) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      raw[i] = column(i) < cols ? Piece<T>::load(row, column(i), cols) : make_uint4(0, 0, 0, 0);
+  }
+};
+
 template <class T, int WAVES, int NV>
 __global__ __launch_bounds__(threads_of<WAVES>()) void norm_kernel(
     const T* __restrict__ x, int64_t ldx, const void* __restrict__ weight,
-    const void* __restrict__ bias, bool w_bf16, float eps, int64_t rows, int64_t cols,
+    const void* __restrict__ bias, bool w_bf16, float eps, int64_t rows, int cols,
     T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd) {
-  constexpr int N = Piece<T>::N;
+  typedef Team<T, WAVES, NV, false> Me;
+  constexpr int N = Me::N;
   __shared__ float buf[2][16][2];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int me = WAVES == 1 ? lane : threadIdx.x;
-  const int64_t team = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
-  const int64_t teams = (int64_t)gridDim.x * teams_of<WAVES>();
+  const Me t(cols);
   int at = 0;
-  uint4 raw[NV];
-  auto fetch = [&](int64_t r) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(i * 64 * WAVES + me) * N;
-      raw[i] = c < cols ? Piece<T>::load(x + r * ldx, c, cols) : make_uint4(0, 0, 0, 0);
-    }
-  };
-  if (team < rows) fetch(team);
+  uint4 raw[NV], ahead[NV];
   float w[NV][N], b[NV][N];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t c = (int64_t)(i * 64 * WAVES + me) * N;
+  auto parameters = [&](int i) {
+    const int c = t.column(i);
     params<N>(weight, w_bf16, c, cols, w[i]);
-    if (bias) params<N>(bias, w_bf16, c, cols, b[i]);
-    else
+    if (bias) {
+      params<N>(bias, w_bf16, c, cols, b[i]);
+    } else {
 #pragma unroll
       for (int j = 0; j < N; ++j) b[i][j] = 0.f;
+    }
+  };
+  if (t.team < rows) t.load(x + t.team * ldx, raw);
+  if constexpr (!Me::LEAN) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) parameters(i);
   }
-  for (int64_t r = team; r < rows; r += teams) {
-    float f[NV][N];
+  for (int64_t r = t.team; r < rows; r += t.teams) {
+    const bool more = r + t.teams < rows;
+    if (!Me::LEAN && more) t.load(x + (r + t.teams) * ldx, ahead);   // in flight under this row's sums
     float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      RowVec<T>::widen(raw[i], f[i]);
+      float f[N];
+      RowVec<T>::widen(raw[i], f);
 #pragma unroll
-      for (int j = 0; j < N; ++j) s[0] += f[i][j];
+      for (int j = 0; j < N; ++j) s[0] += f[j];
     }
-    if (r + teams < rows) fetch(r + teams);   // in flight under this row's arithmetic
-    team_sum<WAVES, 1>(s, buf, at, wave, lane);
+    team_sum<WAVES, 1>(s, buf, at, t.wave, t.lane);
     const float m = s[0] / (float)cols;   // (a row of one value has that mean)
     float q[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      float f[N];
+      RowVec<T>::widen(raw[i], f);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const int64_t c = (int64_t)(i * 64 * WAVES + me) * N + j;
-        f[i][j] = c < cols ? f[i][j] - m : 0.f;
-        q[0] = fmaf(f[i][j], f[i][j], q[0]);
+        const float d = t.column(i) + j < cols ? f[j] - m : 0.f;
+        q[0] = fmaf(d, d, q[0]);
       }
-    team_sum<WAVES, 1>(q, buf, at, wave, lane);
+    }
+    team_sum<WAVES, 1>(q, buf, at, t.wave, t.lane);
     const float rs = 1.f / sqrtf(q[0] / (float)cols + eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(i * 64 * WAVES + me) * N;
-      float o[N];
+      float f[N], o[N];
+      if constexpr (Me::LEAN) parameters(i);
+      RowVec<T>::widen(raw[i], f);
 #pragma unroll
-      for (int j = 0; j < N; ++j) o[j] = fmaf(f[i][j] * rs, w[i][j], b[i][j]);
-      if (c < cols) Piece<T>::store(y + r * cols, c, cols, o);
+      for (int j = 0; j < N; ++j) o[j] = fmaf((f[j] - m) * rs, w[i][j], b[i][j]);
+      if (t.column(i) < cols) Piece<T>::store(y + r * cols, t.column(i), cols, o);
     }
-    if (me == 0) {
+    if (t.me == 0) {
       mean[r] = m;
       rstd[r] = rs;
+    }
+    if (Me::LEAN && more) t.load(x + (r + t.teams) * ldx, raw);
+    if constexpr (!Me::LEAN) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) raw[i] = ahead[i];
     }
   }
 }
@@ -179,95 +214,100 @@ template <class T, int WAVES, int NV>
 __global__ __launch_bounds__(threads_of<WAVES>()) void norm_backward_kernel(
     const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
     const void* __restrict__ weight, bool w_bf16, const float* __restrict__ mean,
-    const float* __restrict__ rstd, int64_t rows, int64_t cols, T* __restrict__ dx,
+    const float* __restrict__ rstd, int64_t rows, int cols, T* __restrict__ dx,
     float* __restrict__ partial) {
-  constexpr int N = Piece<T>::N;
+  typedef Team<T, WAVES, NV, true> Me;
+  constexpr int N = Me::N;
   __shared__ float buf[2][16][2];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int me = WAVES == 1 ? lane : threadIdx.x;
-  const int64_t team = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
-  const int64_t teams = (int64_t)gridDim.x * teams_of<WAVES>();
+  const Me t(cols);
   const float inv = 1.f / (float)cols;
   int at = 0;
-  uint4 rx[NV], rd[NV];
-  float m = 0.f, rs = 0.f;
-  auto fetch = [&](int64_t r) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(i * 64 * WAVES + me) * N;
-      rx[i] = c < cols ? Piece<T>::load(x + r * ldx, c, cols) : make_uint4(0, 0, 0, 0);
-      rd[i] = c < cols ? Piece<T>::load(dy + r * lddy, c, cols) : make_uint4(0, 0, 0, 0);
-    }
-    m = mean[r];
-    rs = rstd[r];
+  uint4 rx[NV], rd[NV], nx[NV], nd[NV];
+  float w[NV][N], dw[NV][N], db[NV][N], m = 0.f, rs = 0.f, nm = 0.f, nrs = 0.f;
+  auto fetch = [&](int64_t r, uint4 (&fx)[NV], uint4 (&fd)[NV], float& fm, float& fr) {
+    t.load(x + r * ldx, fx);
+    t.load(dy + r * lddy, fd);
+    fm = mean[r];
+    fr = rstd[r];
   };
-  if (team < rows) fetch(team);
-  float w[NV][N], dw[NV][N], db[NV][N];
+  if (t.team < rows) fetch(t.team, rx, rd, m, rs);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    params<N>(weight, w_bf16, (int64_t)(i * 64 * WAVES + me) * N, cols, w[i]);
+    if constexpr (!Me::LEAN) params<N>(weight, w_bf16, t.column(i), cols, w[i]);
 #pragma unroll
     for (int j = 0; j < N; ++j) dw[i][j] = db[i][j] = 0.f;
   }
-  for (int64_t r = team; r < rows; r += teams) {
-    float h[NV][N], g[NV][N];
+  for (int64_t r = t.team; r < rows; r += t.teams) {
+    const bool more = r + t.teams < rows;
+    if (!Me::LEAN && more) fetch(r + t.teams, nx, nd, nm, nrs);
     float s[2] = {0.f, 0.f};
-    const float m0 = m, rs0 = rs;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      RowVec<T>::widen(rx[i], h[i]);
-      RowVec<T>::widen(rd[i], g[i]);
+      float h[N], g[N];
+      RowVec<T>::widen(rx[i], h);
+      RowVec<T>::widen(rd[i], g);
+      if constexpr (Me::LEAN) params<N>(weight, w_bf16, t.column(i), cols, w[i]);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        // past the last column dy is zero and the weight too: h adds nothing
-        h[i][j] = (h[i][j] - m0) * rs0;
-        dw[i][j] = fmaf(g[i][j], h[i][j], dw[i][j]);
-        db[i][j] += g[i][j];
-        g[i][j] *= w[i][j];
-        s[0] += g[i][j];
-        s[1] = fmaf(g[i][j], h[i][j], s[1]);
+        // past the last column dy and the weight are zeros: h adds nothing
+        h[j] = (h[j] - m) * rs;
+        dw[i][j] = fmaf(g[j], h[j], dw[i][j]);
+        db[i][j] += g[j];
+        g[j] *= w[i][j];
+        s[0] += g[j];
+        s[1] = fmaf(g[j], h[j], s[1]);
       }
     }
-    if (r + teams < rows) fetch(r + teams);
-    team_sum<WAVES, 2>(s, buf, at, wave, lane);
+    team_sum<WAVES, 2>(s, buf, at, t.wave, t.lane);
     const float c1 = s[0] * inv, c2 = s[1] * inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(i * 64 * WAVES + me) * N;
-      float o[N];
+      float h[N], g[N], o[N];
+      RowVec<T>::widen(rx[i], h);
+      RowVec<T>::widen(rd[i], g);
+      if constexpr (Me::LEAN) params<N>(weight, w_bf16, t.column(i), cols, w[i]);
 #pragma unroll
-      for (int j = 0; j < N; ++j) o[j] = rs0 * (g[i][j] - c1 - h[i][j] * c2);
-      if (c < cols) Piece<T>::store(dx + r * cols, c, cols, o);
+      for (int j = 0; j < N; ++j) o[j] = rs * (g[j] * w[i][j] - c1 - (h[j] - m) * rs * c2);
+      if (t.column(i) < cols) Piece<T>::store(dx + r * cols, t.column(i), cols, o);
+    }
+    if (Me::LEAN && more) fetch(r + t.teams, rx, rd, m, rs);
+    if constexpr (!Me::LEAN) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        rx[i] = nx[i];
+        rd[i] = nd[i];
+      }
+      m = nm;
+      rs = nrs;
     }
   }
+  float* mine = partial + t.team * 2 * cols;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t c = (int64_t)(i * 64 * WAVES + me) * N;
-    if (c < cols) {
-      Piece<float>::store(partial + team * 2 * cols, c, cols, dw[i]);
-      Piece<float>::store(partial + (team * 2 + 1) * cols, c, cols, db[i]);
-      if constexpr (N == 8) {
-        if (c + 4 < cols) {
-          Piece<float>::store(partial + team * 2 * cols, c + 4, cols, dw[i] + 4);
-          Piece<float>::store(partial + (team * 2 + 1) * cols, c + 4, cols, db[i] + 4);
-        }
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const int c = t.column(i) + j;
+      if (c < cols) {
+        Piece<float>::store(mine, c, cols, dw[i] + j);
+        Piece<float>::store(mine + cols, c, cols, db[i] + j);
       }
     }
-  }
 }
 
-// out[c] = sum over p < parts of partial[p * stride + c], each column's parts
-// added in a fixed order: 16 waves take every sixteenth part, then meet in LDS.
+// Column sums of partial [parts][cols]: each column's parts are added in a
+// fixed order (16 waves take every sixteenth, then meet in LDS).  Columns from
+// `split` on go to the second output.
 __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restrict__ partial,
-                                                          int64_t stride, int parts, int64_t cols,
-                                                          float* __restrict__ out) {
+                                                          int parts, int64_t cols, int64_t split,
+                                                          float* __restrict__ out,
+                                                          float* __restrict__ out2) {
   __shared__ float buf[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.f;
   if (c < cols) {
 #pragma unroll 8
-    for (int p = wave; p < parts; p += 16) s += partial[p * stride + c];
+    for (int p = wave; p < parts; p += 16) s += partial[p * cols + c];
   }
   buf[wave][lane] = s;
   __syncthreads();
@@ -275,29 +315,31 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
     float t = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) t += buf[k][lane];
-    out[c] = t;
+    (c < split ? out + c : out2 + (c - split))[0] = t;
   }
 }
 
 // The team shape for a row length: waves a row and 16-byte pieces a thread.
-template <class F>
-hipError_t with_shape(int64_t cols, bool bf16, F f) {
-  if (bf16) {
-    if (cols <= 512) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-    if (cols <= 1024) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
-    if (cols <= 2048) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
-    if (cols <= 4096) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-    if (cols <= 8192) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
-    if (cols <= 16384) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
-    return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
-  }
-  if (cols <= 256) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-  if (cols <= 1024) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
-  if (cols <= 2048) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-  if (cols <= 4096) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
-  if (cols <= 8192) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
-  if (cols <= 16384) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
-  return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
+// Sixteen columns a thread are the rule (registers for a row ahead and,
+// backward, both running sums); the longest rows have no more waves to spread
+// over.
+template <class T, class F>
+hipError_t with_shape(int64_t cols, F f) {
+  constexpr int P = sizeof(T) == 4 ? 2 : 1;        // pieces of eight columns
+  constexpr std::integral_constant<int, P> p1{};
+  constexpr std::integral_constant<int, 2 * P> p2{};
+  constexpr std::integral_constant<int, 4 * P> p4{};
+  constexpr std::integral_constant<int, 1> w1{};
+  constexpr std::integral_constant<int, 4> w4{};
+  constexpr std::integral_constant<int, 8> w8{};
+  constexpr std::integral_constant<int, 16> w16{};
+  if (cols <= 512) return f(w1, p1);
+  if (cols <= 1024) return f(w1, p2);
+  if (cols <= 2048) return f(w4, p1);
+  if (cols <= 4096) return f(w4, p2);
+  if (cols <= 8192) return f(w8, p2);
+  if (cols <= 16384) return f(w16, p2);
+  return f(w16, p4);
 }
 
 // Workgroups: enough for two or more a SIMD, and no more than there are rows.
@@ -309,26 +351,27 @@ int64_t groups_of(int waves, int64_t rows, int cus) {
 
 }  // namespace
 
-int64_t layer_norm_teams(int64_t rows, int64_t cols, bool bf16, int cus) {
+namespace {
+
+template <class T>
+int64_t teams_as(int64_t rows, int64_t cols, int cus) {
   int64_t teams = 0;
-  (void)with_shape(cols, bf16, [&](auto waves, auto) {
+  (void)with_shape<T>(cols, [&](auto waves, auto) {
     teams = groups_of(waves, rows, cus) * teams_of<decltype(waves)::value>();
     return hipSuccess;
   });
   return teams;
 }
 
-namespace {
-
 template <class T>
 hipError_t norm_as(const void* x, int64_t ldx, const void* weight, const void* bias, bool w_bf16,
                    float eps, int64_t rows, int64_t cols, void* y, float* mean, float* rstd, int cus,
                    hipStream_t stream) {
-  return with_shape(cols, sizeof(T) == 2, [&](auto waves, auto nv) {
+  return with_shape<T>(cols, [&](auto waves, auto nv) {
     constexpr int W = decltype(waves)::value, NV = decltype(nv)::value;
     hipLaunchKernelGGL((norm_kernel<T, W, NV>), dim3((unsigned)groups_of(W, rows, cus)),
                        dim3(threads_of<W>()), 0, stream, (const T*)x, ldx, weight, bias, w_bf16, eps,
-                       rows, cols, (T*)y, mean, rstd);
+                       rows, (int)cols, (T*)y, mean, rstd);
     return hipGetLastError();
   });
 }
@@ -338,16 +381,20 @@ hipError_t norm_backward_as(const void* dy, int64_t lddy, const void* x, int64_t
                             const void* weight, bool w_bf16, const float* mean, const float* rstd,
                             int64_t rows, int64_t cols, void* dx, float* partial, int cus,
                             hipStream_t stream) {
-  return with_shape(cols, sizeof(T) == 2, [&](auto waves, auto nv) {
+  return with_shape<T>(cols, [&](auto waves, auto nv) {
     constexpr int W = decltype(waves)::value, NV = decltype(nv)::value;
     hipLaunchKernelGGL((norm_backward_kernel<T, W, NV>), dim3((unsigned)groups_of(W, rows, cus)),
                        dim3(threads_of<W>()), 0, stream, (const T*)dy, lddy, (const T*)x, ldx, weight,
-                       w_bf16, mean, rstd, rows, cols, (T*)dx, partial);
+                       w_bf16, mean, rstd, rows, (int)cols, (T*)dx, partial);
     return hipGetLastError();
   });
 }
 
 }  // namespace
+
+int64_t layer_norm_teams(int64_t rows, int64_t cols, bool bf16, int cus) {
+  return bf16 ? teams_as<uint16_t>(rows, cols, cus) : teams_as<float>(rows, cols, cus);
+}
 
 hipError_t launch_layer_norm(const void* x, int64_t ldx, bool bf16, const void* weight,
                              const void* bias, bool w_bf16, float eps, int64_t rows, int64_t cols,
@@ -368,9 +415,8 @@ hipError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void* 
              : norm_backward_as<float>(dy, lddy, x, ldx, weight, w_bf16, mean, rstd, rows, cols, dx, partial, cus, stream);
     if (e != hipSuccess) return e;
   }
-  const dim3 grid((unsigned)((cols + 63) / 64));
-  hipLaunchKernelGGL(column_sum_kernel, grid, dim3(1024), 0, stream, partial, 2 * cols, (int)teams, cols, dweight);
-  hipLaunchKernelGGL(column_sum_kernel, grid, dim3(1024), 0, stream, partial + cols, 2 * cols, (int)teams, cols, dbias);
+  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((2 * cols + 63) / 64)), dim3(1024), 0, stream, partial,
+                     (int)teams, 2 * cols, cols, dweight, dbias);
   return hipGetLastError();
 }
 
@@ -454,7 +500,7 @@ hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const uint16_t*
                      dbias ? partial : nullptr);
   if (dbias)
     hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((n + 63) / 64)), dim3(1024), 0, stream,
-                       partial, n, chunks, n, dbias);
+                       partial, chunks, n, n, dbias, dbias);
   return hipGetLastError();
 }
 
