@@ -430,6 +430,25 @@ def moe_contiguous_layout_fp8(x, topk_ids, num_experts, m_cap=None, out=None):
 
 
 # ------------------------------------------- BF16 products over ragged runs
+# These calls are made many times a layer and some run for a few microseconds,
+# so their host side is kept short: the stream as a plain number, outputs from
+# an operand's new_empty.
+def _stream_of(t):
+    """The current stream of t's device, as a number."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _workspace_of(nbytes, t, stream):
+    """_workspace for a stream given as a number."""
+    if nbytes == 0:
+        return None, 0
+    key = (t.device, stream)
+    ws = _ws_cache.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _ws_cache[key] = torch.zeros(nbytes, dtype=torch.uint8, device=t.device)
+    return ws.data_ptr(), ws.numel()
+
+
 def _rows(t, dtype, name):
     """Row stride of a 2-D tensor whose rows are contiguous but may be part of
     wider ones."""
@@ -450,10 +469,10 @@ def _rows(t, dtype, name):
     return ld
 
 
-def _out_rows(out, shape, dtype, device, name="out"):
+def _out_rows(out, shape, dtype, like, name="out"):
     """(tensor, row stride, dtype code) of a given or new 2-D output."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device), shape[1], _out_code(dtype)
+        return like.new_empty(shape, dtype=dtype), shape[1], _out_code(dtype)
     code = _out_code(out.dtype)
     ld = _rows(out, out.dtype, name)
     if tuple(out.shape) != tuple(shape):
@@ -479,9 +498,9 @@ def grouped_gemm_bf16(x, w, row_offsets, out_dtype=torch.bfloat16, out=None):
     rows = x.shape[0]
     if x.shape[1] != k:
         raise ValueError("operand shapes disagree")
-    out, ldy, code = _out_rows(out, (rows, n), out_dtype, x.device)
+    out, ldy, code = _out_rows(out, (rows, n), out_dtype, x)
     _check(lib().grouped_gemm_bf16(x.data_ptr(), ldx, w.data_ptr(), row_offsets.data_ptr(),
-                                   out.data_ptr(), ldy, code, rows, n, k, E, _stream()))
+                                   out.data_ptr(), ldy, code, rows, n, k, E, _stream_of(x)))
     return out
 
 
@@ -493,9 +512,9 @@ def grouped_gemm_bf16_dgrad(dy, w, row_offsets, out_dtype=torch.bfloat16, out=No
     rows = dy.shape[0]
     if dy.shape[1] != n:
         raise ValueError("operand shapes disagree")
-    out, ldx, code = _out_rows(out, (rows, k), out_dtype, dy.device)
+    out, ldx, code = _out_rows(out, (rows, k), out_dtype, dy)
     _check(lib().grouped_gemm_bf16_dgrad(dy.data_ptr(), lddy, w.data_ptr(), row_offsets.data_ptr(),
-                                         out.data_ptr(), ldx, code, rows, n, k, E, _stream()))
+                                         out.data_ptr(), ldx, code, rows, n, k, E, _stream_of(dy)))
     return out
 
 
@@ -511,13 +530,13 @@ def grouped_gemm_bf16_wgrad(dy, x, row_offsets, out_dtype=torch.float32, out=Non
     if x.shape[0] != rows or row_offsets.dim() != 1 or E < 1:
         raise ValueError("operand shapes disagree")
     if out is None:
-        out = torch.empty((E, n, k), dtype=out_dtype, device=dy.device)
+        out = dy.new_empty((E, n, k), dtype=out_dtype)
     _dev(out, out.dtype, "out")
     if out.shape != (E, n, k):
         raise ValueError("output shape disagrees")
     _check(lib().grouped_gemm_bf16_wgrad(dy.data_ptr(), lddy, x.data_ptr(), ldx,
                                          row_offsets.data_ptr(), out.data_ptr(),
-                                         _out_code(out.dtype), rows, n, k, E, _stream()))
+                                         _out_code(out.dtype), rows, n, k, E, _stream_of(dy)))
     return out
 
 
@@ -556,15 +575,17 @@ def gemm_bf16_epilogue(x, w, bias=None, residual=None, activation="none", save_z
         res_ptr = residual.data_ptr()
         if m == 1:
             ldr = n
-    out, ldy, code = _out_rows(out, (m, n), out_dtype, x.device)
-    z = torch.empty((m, n), dtype=torch.bfloat16, device=x.device) if save_z else None
+    out, ldy, code = _out_rows(out, (m, n), out_dtype, x)
+    z = x.new_empty((m, n)) if save_z else None
     L = lib()
-    ws = workspace
-    if ws is None:
-        ws = _workspace(L.fg8_gemm_bf16_workspace_bytes(m, n, k), x.device)
+    stream = _stream_of(x)
+    if workspace is None:
+        ws, ws_bytes = _workspace_of(L.fg8_gemm_bf16_workspace_bytes(m, n, k), x, stream)
+    else:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(L.gemm_bf16_epilogue(x.data_ptr(), ldx, w.data_ptr(), bias_ptr, bias_bf16, act, res_ptr,
-                                ldr, _ptr(z), out.data_ptr(), ldy, code, m, n, k, _ptr(ws),
-                                0 if ws is None else ws.numel() * ws.element_size(), _stream()))
+                                ldr, z.data_ptr() if save_z else None, out.data_ptr(), ldy, code, m,
+                                n, k, ws, ws_bytes, stream))
     return (out, z) if save_z else out
 
 
@@ -587,18 +608,18 @@ def gemm_bf16_epilogue_backward(dy, x, w, z=None, activation="none", dw_dtype=to
         _dev(z, torch.bfloat16, "z")
         if z.shape != (m, n):
             raise ValueError("z must have dy's shape")
-    dev = x.device
-    dx = torch.empty((m, k), dtype=torch.bfloat16, device=dev) if needs[0] else None
-    dw = torch.empty((n, k), dtype=dw_dtype, device=dev) if needs[1] else None
-    db = torch.empty((n,), dtype=torch.float32, device=dev) if needs[2] else None
+    dx = x.new_empty((m, k)) if needs[0] else None
+    dw = x.new_empty((n, k), dtype=dw_dtype) if needs[1] else None
+    db = x.new_empty(n, dtype=torch.float32) if needs[2] else None
     L = lib()
-    ws = workspace
-    if ws is None:
-        ws = _workspace(L.fg8_gemm_bf16_backward_workspace_bytes(m, n, k), dev)
+    stream = _stream_of(x)
+    if workspace is None:
+        ws, ws_bytes = _workspace_of(L.fg8_gemm_bf16_backward_workspace_bytes(m, n, k), x, stream)
+    else:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(L.gemm_bf16_epilogue_backward(
         dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), _ptr(z), act, _ptr(dx), _ptr(dw),
-        _out_code(dw_dtype), _ptr(db), m, n, k, _ptr(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream()))
+        _out_code(dw_dtype), _ptr(db), m, n, k, ws, ws_bytes, stream))
     return dx, dw, db
 
 
@@ -628,11 +649,11 @@ def layer_norm(x, weight, bias=None, eps=1e-5):
     b, b_bf16 = _param(bias, cols, "bias")
     if b is not None and b_bf16 != w_bf16:
         raise TypeError("weight and bias must have one type")
-    y = torch.empty(x.shape, dtype=dtype, device=x.device)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    y = x.new_empty(x.shape)
+    mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
     _check(lib().layer_norm(x.data_ptr(), ldx, int(dtype == torch.bfloat16), w, b, w_bf16, eps, rows,
-                            cols, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _stream()))
+                            cols, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _stream_of(x)))
     return y, mean, rstd
 
 
@@ -648,17 +669,16 @@ def layer_norm_backward(dy, x, weight, mean, rstd):
     _dev(rstd, torch.float32, "rstd")
     if dy.shape != x.shape or mean.shape != x.shape[:-1] or rstd.shape != x.shape[:-1]:
         raise ValueError("operand shapes disagree")
-    dev = x.device
-    dx = torch.empty(x.shape, dtype=dtype, device=dev)
-    dw = torch.empty((cols,), dtype=torch.float32, device=dev)
-    db = torch.empty((cols,), dtype=torch.float32, device=dev)
+    dx = x.new_empty(x.shape)
+    dw = x.new_empty(cols, dtype=torch.float32)
+    db = x.new_empty(cols, dtype=torch.float32)
     L = lib()
     bf16 = int(dtype == torch.bfloat16)
     need = L.fg8_layer_norm_backward_workspace_bytes(rows, cols, bf16)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None
     _check(L.layer_norm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, bf16, w, w_bf16,
                                  mean.data_ptr(), rstd.data_ptr(), rows, cols, dx.data_ptr(),
-                                 dw.data_ptr(), db.data_ptr(), _ptr(ws), need, _stream()))
+                                 dw.data_ptr(), db.data_ptr(), _ptr(ws), need, _stream_of(x)))
     return dx, dw, db
 
 
@@ -681,7 +701,7 @@ def moe_combine(y, token_row, weights, residual=None, out=None):
     type -> [tokens, hidden] of y's type."""
     dtype, rows, hidden, tokens, topk = _combine_args(y, token_row, weights)
     if out is None:
-        out = torch.empty((tokens, hidden), dtype=dtype, device=y.device)
+        out = y.new_empty((tokens, hidden))
     for name, t in (("residual", residual), ("out", out)):
         if t is not None:
             _dev(t, dtype, name)
@@ -689,7 +709,7 @@ def moe_combine(y, token_row, weights, residual=None, out=None):
                 raise ValueError(f"{name} must have shape ({tokens}, {hidden})")
     _check(lib().moe_combine(y.data_ptr(), int(dtype == torch.bfloat16), rows, token_row.data_ptr(),
                              weights.data_ptr(), _ptr(residual), tokens, topk, hidden,
-                             out.data_ptr(), _stream()))
+                             out.data_ptr(), _stream_of(y)))
     return out
 
 
@@ -703,10 +723,10 @@ def moe_combine_backward(dout, y, token_row, row_token, weights):
     _dev(row_token, torch.int32, "row_token")
     if dout.shape != (tokens, hidden) or row_token.shape != (rows,):
         raise ValueError("operand shapes disagree")
-    dy = torch.empty((rows, hidden), dtype=dtype, device=y.device)
-    dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
+    dy = y.new_empty((rows, hidden))
+    dweights = y.new_empty((tokens, topk), dtype=torch.float32)
     _check(lib().moe_combine_backward(dout.data_ptr(), y.data_ptr(), int(dtype == torch.bfloat16),
                                       rows, token_row.data_ptr(), row_token.data_ptr(),
                                       weights.data_ptr(), tokens, topk, hidden, dy.data_ptr(),
-                                      dweights.data_ptr(), _stream()))
+                                      dweights.data_ptr(), _stream_of(y)))
     return dy, dweights

@@ -41,13 +41,15 @@ typedef __attribute__((address_space(3))) v4s lds_v4s;
 constexpr int kBK = 64;                       // k depth of one step
 constexpr uint32_t kNowhere = 0x80000000u;    // an offset past every buffer resource
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, int OCC_>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, int OCC_, int DEPTH_ = kBK>
 struct BfCfg {
+  static constexpr int DEPTH = DEPTH_;     // k of a stage
+
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
   static constexpr int STAGES = STAGES_, OCC = OCC_;
   static constexpr int WAVES = WAVES_M * WAVES_N, THREADS = 64 * WAVES;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 16, TN = WN / 16;
-  static constexpr int A_BYTES = BM * kBK * 2, B_BYTES = BN * kBK * 2;
+  static constexpr int A_BYTES = BM * DEPTH * 2, B_BYTES = BN * DEPTH * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static_assert(WM % 16 == 0 && WN % 16 == 0 && STAGES >= 2, "whole MFMA tiles, two stages");
   static_assert(STAGES * STAGE_BYTES <= 160 * 1024, "LDS of a CU");
@@ -70,13 +72,13 @@ __device__ __forceinline__ v4i resource(const void* base, int64_t bytes) {
 }
 
 // One operand's tile: BX rows (m or n) by 64 k.  KMAJOR: memory is [k][x].
-template <bool KMAJOR, int BX, int WAVES>
+template <bool KMAJOR, int BX, int WAVES, int DEPTH = kBK>
 struct Operand {
-  static constexpr int BYTES = BX * kBK * 2;
+  static constexpr int BYTES = BX * DEPTH * 2;
   static constexpr int COPIES = BYTES / 1024;                     // of a wave's 1 KB
   static constexpr int PER = (COPIES + WAVES - 1) / WAVES;        // per wave (the last may be short)
   static constexpr bool EVEN = COPIES % WAVES == 0;
-  static constexpr int PITCH = KMAJOR ? BX * 2 : kBK * 2;         // bytes of an LDS row
+  static constexpr int PITCH = KMAJOR ? BX * 2 : DEPTH * 2;       // bytes of an LDS row
   static_assert(!KMAJOR || BX >= 64, "a k-major tile is 64 columns at least");
 
   const char* base;      // the tile's first element at the first k of the run
@@ -85,6 +87,9 @@ struct Operand {
   uint32_t off[PER];     // this lane's source of each copy, from base
   int rem_k;             // k elements of the run
 
+  // XOR of the 16-byte chunks of k-contiguous row r: with 64-byte rows two rows
+  // share the 128 bytes that the 64-deep layout gives one
+  __device__ static int chunk_xor(int r) { return DEPTH == 64 ? swz(r) : r >> 2 & 3; }
   // XOR of the 32-byte granules of k-major row k
   __device__ static int gran(int k) {
     return BX >= 128 ? (k & 3) | ((k >> 3 & 1) << 2) : (k >> 1 & 1) | ((k >> 3 & 1) << 1);
@@ -113,7 +118,7 @@ struct Operand {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int at = (wave + i * WAVES) * 1024 + lane * 16;
-        const int r = at / PITCH, c = (at % PITCH / 16) ^ swz(r);
+        const int r = at / PITCH, c = (at % PITCH / 16) ^ chunk_xor(r);
         off[i] = (uint32_t)(r * ld) + c * 16;
       }
     }
@@ -121,21 +126,21 @@ struct Operand {
 
   // the copies of k step kt into the LDS tile at `lds`
   __device__ void issue(int kt, uint32_t lds, int wave, int lane) const {
-    const int rem = rem_k - kt * kBK;     // k elements from this step on (> 0)
+    const int rem = rem_k - kt * DEPTH;   // k elements from this step on (> 0)
     if constexpr (KMAJOR) {
-      const v4i rs = resource(base + (int64_t)kt * kBK * ld, (int64_t)(rem - 1) * ld + left);
+      const v4i rs = resource(base + (int64_t)kt * DEPTH * ld, (int64_t)(rem - 1) * ld + left);
 #pragma unroll
       for (int i = 0; i < PER; ++i)
         if (EVEN || wave + i * WAVES < COPIES)
           copy16(rs, off[i], uniform(lds + (uint32_t)(wave + i * WAVES) * 1024));
     } else {
-      const v4i rs = resource(base + (int64_t)kt * (kBK * 2), left + (int64_t)((rem + 7) & ~7) * 2);
+      const v4i rs = resource(base + (int64_t)kt * (DEPTH * 2), left + (int64_t)((rem + 7) & ~7) * 2);
 #pragma unroll
       for (int i = 0; i < PER; ++i)
         if (EVEN || wave + i * WAVES < COPIES) {
           // chunks at or past the end of k are zeros (K is a multiple of 8)
           const int at = (wave + i * WAVES) * 1024 + lane * 16;
-          const int c = (at % PITCH / 16) ^ swz(at / PITCH);
+          const int c = (at % PITCH / 16) ^ chunk_xor(at / PITCH);
           copy16(rs, c * 8 < rem ? off[i] : kNowhere, uniform(lds + (uint32_t)(wave + i * WAVES) * 1024));
         }
     }
@@ -152,7 +157,7 @@ struct Operand {
       return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
       const int r = x + i;
-      return *reinterpret_cast<const v8bf*>(tile + r * PITCH + (((g + 4 * kk) ^ swz(r)) << 4));
+      return *reinterpret_cast<const v8bf*>(tile + r * PITCH + (((g + 4 * kk) ^ chunk_xor(r)) << 4));
     }
   }
 };
@@ -410,6 +415,167 @@ struct BfOut {
   }
 };
 
+// The epilogue of waves that own 64 columns.  In registers a lane holds four
+// columns of one row, and neighbouring lanes hold neighbouring rows; memory
+// wants neighbouring lanes on neighbouring columns (256 KB tiles written
+// straight from the registers leave a CU at 36 GB/s, as whole rows at 120
+// GB/s; non-temporal stores of such 16-byte pieces reach 3 TB/s over the chip,
+// whole rows 5.2).  So each wave turns sixteen rows of its columns at a time
+// in a piece of LDS of its own, without a barrier.  In the staged rows the
+// 16-byte chunk index is XORed with a function of the row, which keeps writes
+// and reads free of bank conflicts.
+__device__ __forceinline__ void stream16(void* to, uint4 v) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store(u4{v.x, v.y, v.z, v.w}, reinterpret_cast<u4*>(to));
+}
+
+// Eight BF16 or four FP32 columns from c on of the row at q, those below N.
+__device__ __forceinline__ void store_eight(uint16_t* q, int64_t ld, int c, int N, bool full, uint4 v) {
+  if (full) {
+    stream16(q + c, v);
+  } else if (ld % 8 == 0 && c + 8 <= N) {
+    *reinterpret_cast<uint4*>(q + c) = v;
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < N) q[c + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+  }
+}
+__device__ __forceinline__ void store_four(float* q, int64_t ld, int c, int N, bool full, v4f v) {
+  if (full) {
+    __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(q + c));
+  } else if (ld % 4 == 0 && c + 4 <= N) {
+    *reinterpret_cast<v4f*>(q + c) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < N) q[c + i] = v[i];
+  }
+}
+
+// Sixteen rows x 64 columns as BF16 (2 KB of LDS) -> rows m + l / 8 (+ 8),
+// columns n + 8 (l % 8) ..: eight lanes a row, 128 bytes.
+__device__ __forceinline__ void store_bf16_rows(uint8_t* turn, const v4f (&v)[4], uint16_t* to, int64_t ld,
+                                                int rows, int n, int N, int lane, bool full) {
+  const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    *reinterpret_cast<uint2*>(turn + i * 128 + (((2 * t + (g >> 1)) ^ swz(i)) << 4) + (g & 1) * 8) =
+        make_uint2(bf16x2(v[t][0], v[t][1]), bf16x2(v[t][2], v[t][3]));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 8 * h + (lane >> 3), c = lane & 7;
+    const uint4 u = *reinterpret_cast<const uint4*>(turn + r * 128 + ((c ^ swz(r)) << 4));
+    if (full || r < rows) store_eight(to + r * ld, ld, n + 8 * c, N, full, u);
+  }
+}
+// Sixteen rows x 32 columns as FP32 (2 KB): eight lanes a row, 128 bytes.
+__device__ __forceinline__ void store_f32_rows(uint8_t* turn, v4f a, v4f b, float* to, int64_t ld, int rows,
+                                               int n, int N, int lane, bool full) {
+  const int i = lane & 15, g = lane >> 4;
+  *reinterpret_cast<v4f*>(turn + i * 128 + ((g ^ swz(i)) << 4)) = a;
+  *reinterpret_cast<v4f*>(turn + i * 128 + (((4 + g) ^ swz(i)) << 4)) = b;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 8 * h + (lane >> 3), c = lane & 7;
+    const v4f u = *reinterpret_cast<const v4f*>(turn + r * 128 + ((c ^ swz(r)) << 4));
+    if (full || r < rows) store_four(to + r * ld, ld, n + 4 * c, N, full, u);
+  }
+}
+// Sixteen rows x 64 columns staged as FP32 (4 KB), the residual's piece (res)
+// added on the way out.
+__device__ __forceinline__ void store_rows_plus(uint8_t* turn, const v4f (&v)[4], const uint4 (&res)[2], bool has_res,
+                                                void* to, int64_t ld, bool bf16, int rows, int n, int N, int lane,
+                                                bool full) {
+  const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) *reinterpret_cast<v4f*>(turn + i * 256 + (((4 * t + g) ^ i) << 4)) = v[t];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 8 * h + (lane >> 3), c = lane & 7;
+    v4f a = *reinterpret_cast<const v4f*>(turn + r * 256 + (((2 * c) ^ r) << 4));
+    v4f b = *reinterpret_cast<const v4f*>(turn + r * 256 + (((2 * c + 1) ^ r) << 4));
+    if (has_res) {
+      float f[8];
+      RowVec<uint16_t>::widen(res[h], f);
+      a += v4f{f[0], f[1], f[2], f[3]};
+      b += v4f{f[4], f[5], f[6], f[7]};
+    }
+    if (full || r < rows) {
+      if (bf16) {
+        store_eight((uint16_t*)to + r * ld, ld, n + 8 * c, N, full,
+                    make_uint4(bf16x2(a[0], a[1]), bf16x2(a[2], a[3]), bf16x2(b[0], b[1]), bf16x2(b[2], b[3])));
+      } else {
+        store_four((float*)to + r * ld, ld, n + 8 * c, N, full, a);
+        store_four((float*)to + r * ld, ld, n + 8 * c + 4, N, full, b);
+      }
+    }
+  }
+}
+// residual[m][c .. c + 7] (0 past N)
+__device__ __forceinline__ uint4 residual8(const BfProblem& p, int64_t m, int c) {
+  const uint16_t* r = p.residual + m * p.ldr + c;
+  if (p.ldr % 8 == 0 && c + 8 <= p.N) return *reinterpret_cast<const uint4*>(r);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c + i < p.N) w[i / 2] |= (uint32_t)r[i] << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One unit's output: what rows16() needs beside the values.
+template <bool EPI>
+struct TileOut {
+  static constexpr int kTurn = EPI ? 4096 : 2048;    // LDS of a wave
+  const BfProblem& p;
+  char* d;             // the unit's D
+  uint8_t* turn;
+  int64_t m0;
+  int rows, n, lane;   // rows of D from m0 on; the wave's first column
+  bool whole, full;    // the tile exists whole; and rows are whole 16-byte pieces
+  v4f bias[EPI ? 4 : 1];
+  __device__ TileOut(const BfProblem& q, const BfUnit& w, int bm, int bn, int wave_n, uint8_t* t, int l)
+      : p(q), turn(t), m0(w.m0), rows(w.rows), n(w.n0 + wave_n), lane(l) {
+    d = (char*)p.d + (int64_t)(p.mode == kBfKRuns ? w.g : 0) * p.d_stride * (p.out_bf16 ? 2 : 4);
+    whole = w.rows >= bm && w.n0 + bn <= p.N;
+    full = whole && p.ldd % (p.out_bf16 ? 8 : 4) == 0;
+    if constexpr (EPI) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bias[i] = bias4(p, n + 16 * i + 4 * (lane >> 4));
+    }
+  }
+  // the residual of rows r .. r + 15, as rows16() takes it
+  __device__ void residual(int r, uint4 (&res)[2]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = r + 8 * h + (lane >> 3);
+      res[h] = p.residual && at < rows ? residual8(p, m0 + at, n + 8 * (lane & 7)) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  // rows r .. r + 15 of the tile, the wave's 64 columns
+  __device__ void rows16(int r, v4f (&v)[4], const uint4 (&res)[2]) const {
+    const int64_t m = m0 + r;
+    const int left = rows - r;
+    if constexpr (EPI) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += bias[i];
+      if (p.z) store_bf16_rows(turn, v, p.z + m * p.ldz, p.ldz, left, n, p.N, lane, whole && p.ldz % 8 == 0);
+      if (p.act != kActNone) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e / 4][e % 4] = act_of(p.act, v[e / 4][e % 4]);
+      }
+      store_rows_plus(turn, v, res, p.residual != nullptr, d + m * p.ldd * (p.out_bf16 ? 2 : 4), p.ldd, p.out_bf16,
+                      left, n, p.N, lane, full);
+    } else if (p.out_bf16) {
+      store_bf16_rows(turn, v, (uint16_t*)d + m * p.ldd, p.ldd, left, n, p.N, lane, full);
+    } else {
+      store_f32_rows(turn, v[0], v[1], (float*)d + m * p.ldd, p.ldd, left, n, p.N, lane, full);
+      store_f32_rows(turn, v[2], v[3], (float*)d + m * p.ldd, p.ldd, left, n + 32, p.N, lane, full);
+    }
+  }
+};
+
 // ---------------------------------------------------------------- split k
 // Every split publishes its FP32 tile past the caches of its XCD and counts
 // itself in; the last one to arrive adds them up in the order of the splits
@@ -454,10 +620,10 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
 #pragma unroll
     for (int j = 0; j < C::TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  const int steps = (w.ks + kBK - 1) / kBK;
+  const int steps = (w.ks + C::DEPTH - 1) / C::DEPTH;
   if (steps > 0) {
-    typedef Operand<AK, C::BM, C::WAVES> OpA;
-    typedef Operand<BK, C::BN, C::WAVES> OpB;
+    typedef Operand<AK, C::BM, C::WAVES, C::DEPTH> OpA;
+    typedef Operand<BK, C::BN, C::WAVES, C::DEPTH> OpB;
     OpA a;
     OpB b;
     a.init(p.a, p.lda, w.m0, w.rows, w.k0, w.ks, wave, lane);
@@ -481,7 +647,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
       const uint8_t* As = smem + kt % C::STAGES * C::STAGE_BYTES;
       const uint8_t* Bs = As + C::A_BYTES;
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      for (int kk = 0; kk < C::DEPTH / 32; ++kk) {
         v8bf fa[C::TM], fb[C::TN];
 #pragma unroll
         for (int i = 0; i < C::TM; ++i) fa[i] = OpA::frag(As, wm0 + 16 * i, kk, lane);
@@ -508,27 +674,51 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
                                                w.split * kTile + (((wave * C::TM + i) * C::TN + j) * 64 + lane) * 16,
                                                0, kCoherent);
     if (!last_of_splits(p, w, tid, &last)) return;
-    // (a split's tiles are loaded together, one split after the other: all
-    // splits at once would not fit in registers)
-    for (int s = 0; s < p.splits; ++s)
+    // as many splits' tiles at a time as registers hold, all their loads
+    // before the first addition
+    constexpr int TILES = C::TM * C::TN, AT_ONCE = TILES >= 16 ? 2 : 32 / TILES;
+    for (int s0 = 0; s0 < p.splits; s0 += AT_ONCE) {
+      v4f part[AT_ONCE][TILES];
 #pragma unroll
-      for (int i = 0; i < C::TM; ++i)
+      for (int s = 0; s < AT_ONCE; ++s)
 #pragma unroll
-        for (int j = 0; j < C::TN; ++j) {
-          const v4f v = __builtin_bit_cast(
-              v4f, __builtin_amdgcn_raw_buffer_load_b128(
-                       ws, s * kTile + (((wave * C::TM + i) * C::TN + j) * 64 + lane) * 16, 0, kCoherent));
-          acc[i][j] = s == 0 ? v : acc[i][j] + v;
-        }
+        for (int t = 0; t < TILES; ++t)
+          if (s0 + s < p.splits)
+            part[s][t] = __builtin_bit_cast(
+                v4f, __builtin_amdgcn_raw_buffer_load_b128(
+                         ws, (s0 + s) * kTile + ((wave * TILES + t) * 64 + lane) * 16, 0, kCoherent));
+#pragma unroll
+      for (int s = 0; s < AT_ONCE; ++s)
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+          if (s0 + s < p.splits) {
+            v4f& a = acc[t / C::TN][t % C::TN];
+            a = s0 + s == 0 ? part[s][t] : a + part[s][t];
+          }
+    }
   }
 
-  const BfOut out(p, w.g);
+  if constexpr (C::WN == 64) {
+    constexpr bool EPI = MODE == kBfDense && !AK && !BK;
+    static_assert(C::WAVES * TileOut<EPI>::kTurn <= C::STAGES * C::STAGE_BYTES, "rows turn in the stages");
+    __syncthreads();      // every wave is done with the stages
+    const TileOut<EPI> out(p, w, C::BM, C::BN, wn0, smem + wave * TileOut<EPI>::kTurn, lane);
 #pragma unroll
-  for (int i = 0; i < C::TM; ++i) {
-    const int r = wm0 + 16 * i + (lane & 15);
-    if (r < w.rows) {
+    for (int i = 0; i < C::TM; ++i) {
+      uint4 res[2];
+      if constexpr (EPI) out.residual(wm0 + 16 * i, res);
+      v4f v[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+      out.rows16(wm0 + 16 * i, v, res);
+    }
+  } else {
+    const BfOut out(p, w.g);
 #pragma unroll
-      for (int j = 0; j < C::TN; ++j) out.four(w.m0 + r, w.n0 + wn0 + 16 * j + 4 * (lane >> 4), acc[i][j]);
+    for (int i = 0; i < C::TM; ++i) {
+      const int r = wm0 + 16 * i + (lane & 15);
+      if (r < w.rows) {
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j) out.four(w.m0 + r, w.n0 + wn0 + 16 * j + 4 * (lane >> 4), acc[i][j]);
+      }
     }
   }
 }
@@ -726,65 +916,6 @@ __device__ __forceinline__ void phase_barrier() {
   phase_fence();
 }
 
-// The epilogue of the big tile: `full` where every row and column of the tile
-// exists and rows are whole 16-byte pieces, so stores need no checks (and
-// their number is known).  EPI: bias, activation, residual and z are compiled in.
-//
-// Columns: a lane holds columns 4 g .. 4 g + 3 of two neighbouring 16-column
-// tiles.  As BF16 those are two dwords each; exchanging the odd 16-lane rows of
-// the first tile with the even ones of the second leaves each lane eight
-// neighbouring columns, one 16-byte store.
-__device__ __forceinline__ uint4 swap_columns(v4f a, v4f b) {
-  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-  const u2 lo = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(bf16x2(a[0], a[1]), bf16x2(b[0], b[1]), false, false));
-  const u2 hi = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(bf16x2(a[2], a[3]), bf16x2(b[2], b[3]), false, false));
-  return make_uint4(lo.x, hi.x, lo.y, hi.y);
-}
-__device__ __forceinline__ int swapped_column(int lane) { return (lane >> 4 & 1) * 16 + (lane >> 5) * 8; }
-
-// (with the non-temporal hint the BF16 tiles of 8191 x 7168 x 2048 took 300 us
-// for 334 without; FP32 tiles, whose 256 KB drain under the next unit, ran 5%
-// slower with it and go without)
-__device__ __forceinline__ void stream16(void* to, uint4 v) {
-  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-  __builtin_nontemporal_store(u4{v.x, v.y, v.z, v.w}, reinterpret_cast<u4*>(to));
-}
-
-// Eight BF16 or four FP32 columns from c on of the row at q, those below N.
-__device__ __forceinline__ void store_eight(uint16_t* q, int64_t ld, int c, int N, bool full, uint4 v) {
-  if (full) {
-    stream16(q + c, v);
-  } else if (ld % 8 == 0 && c + 8 <= N) {
-    *reinterpret_cast<uint4*>(q + c) = v;
-  } else {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < N) q[c + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-  }
-}
-__device__ __forceinline__ void store_four(float* q, int64_t ld, int c, int N, bool full, v4f v) {
-  if (full || (ld % 4 == 0 && c + 4 <= N)) {
-    *reinterpret_cast<v4f*>(q + c) = v;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c + i < N) q[c + i] = v[i];
-  }
-}
-
-// (the exchange needs every lane; only live rows are stored)
-__device__ __forceinline__ void store_rows(void* to, int64_t ld, bool bf16, int64_t m, int n, int N,
-                                           int lane, bool full, bool live, v4f a, v4f b) {
-  if (bf16) {
-    const uint4 v = swap_columns(a, b);
-    if (live) store_eight((uint16_t*)to + m * ld, ld, n + swapped_column(lane), N, full, v);
-  } else if (live) {
-    store_four((float*)to + m * ld, ld, n + 4 * (lane >> 4), N, full, a);
-    store_four((float*)to + m * ld, ld, n + 16 + 4 * (lane >> 4), N, full, b);
-  }
-}
-
 // Eight waves, two a SIMD, in two groups of four: group 0 owns the upper 128
 // rows, group 1 the lower, wave q of a group columns 64 q .. 64 q + 63.  A k
 // step is two phases, half of the wave's rows each: 32 MFMAs on fragments that
@@ -814,7 +945,7 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
   typedef HalfTile<AK, 64> HalfA;
   typedef HalfTile<BK, 32> HalfB;
   constexpr uint32_t kHalf = HalfA::BYTES;         // LDS: per stage A0, A1, B0, B1
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[8 * kHalf];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[8 * kHalf + 8 * TileOut<EPI>::kTurn];
   __shared__ RunTable<MODE == kBfRowRuns ? kMaxRuns : 1> runs;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int grp = wave >> 2, q = wave & 3;
@@ -955,58 +1086,19 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
     }
 
     const int here = opaque(lane);
-    char* d = (char*)p.d + (int64_t)(MODE == kBfKRuns ? w.g : 0) * p.d_stride * (p.out_bf16 ? 2 : 4);
-    const int per = p.out_bf16 ? 8 : 4;
-    const bool full = w.rows >= 256 && w.n0 + 256 <= p.N && p.ldd % per == 0;
-    const int n1 = w.n0 + q * 64;
-    v4f bias[2][2];
-    if constexpr (EPI) {
-#pragma unroll
-      for (int hb = 0; hb < 2; ++hb)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) bias[hb][j] = bias4(p, n1 + hb * 32 + 16 * j + 4 * (here >> 4));
-    }
+    const TileOut<EPI> out(p, w, 256, 256, q * 64, smem + 8 * kHalf + wave * TileOut<EPI>::kTurn, here);
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha) {
-      const int r0 = grp * 128 + ha * 64 + (here & 15);
-      uint2 res[4][2][2];
-      if constexpr (EPI) {
-        if (p.residual) {       // all of a half's loads before its stores
+      const int r0 = grp * 128 + ha * 64;
+      uint4 res[4][2];
+      if constexpr (EPI) {      // all of a half's loads before its stores
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (r0 + 16 * i < w.rows)
-                res[i][k / 2][k % 2] = residual4(p, w.m0 + r0 + 16 * i, n1 + k / 2 * 32 + k % 2 * 16 + 4 * (here >> 4));
-        }
+        for (int i = 0; i < 4; ++i) out.residual(r0 + 16 * i, res[i]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t m = w.m0 + r0 + 16 * i;
-        const bool live = r0 + 16 * i < w.rows;
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
-          v4f v[2] = {acc[ha][i][hb][0], acc[ha][i][hb][1]};
-          const int n = n1 + hb * 32;
-          if constexpr (EPI) {
-            v[0] += bias[hb][0];
-            v[1] += bias[hb][1];
-            if (p.z) store_rows(p.z, p.ldz, true, m, n, p.N, here, full && p.ldz % 8 == 0, live, v[0], v[1]);
-            if (p.act != kActNone) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e / 4][e % 4] = act_of(p.act, v[e / 4][e % 4]);
-            }
-            if (p.residual) {
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint2 r = res[i][hb][j];
-                v[j] += v4f{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
-                            __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u)};
-              }
-            }
-          }
-          store_rows(d, p.ldd, p.out_bf16, m, n, p.N, here, full, live, v[0], v[1]);
-        }
+        v4f v[4] = {acc[ha][i][0][0], acc[ha][i][0][1], acc[ha][i][1][0], acc[ha][i][1][1]};
+        out.rows16(r0 + 16 * i, v, res[i]);
       }
     }
     if (u >= total) return;
@@ -1015,13 +1107,17 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
 }
 
 // ------------------------------------------------------------------- host
-// Tile configurations.  kBig: bf16_big_kernel; kMid, kLow: bf16_kernel, with
-// two workgroups a CU; kFew..: bf16_few_kernel of 16, 32 or 64 rows.
-enum { kBig = 0, kMid, kLow, kFew16, kFew32, kFew64, kConfigs };
+// Tile configurations.  kBig: bf16_big_kernel; kFew: bf16_few_kernel; the
+// others: bf16_kernel with two workgroups a CU.
+enum { kBig = 0, kDuo, kMid, kHigh, kLow, kFlat, kThin, kFew, kConfigs };
+using BfDuo = BfCfg<128, 256, 1, 4, 3, 2, 32>;
 using BfMid = BfCfg<128, 128, 2, 2, 2, 2>;
+using BfHigh = BfCfg<128, 64, 2, 2, 3, 2>;
 using BfLow = BfCfg<64, 64, 2, 2, 4, 2>;
-constexpr int kBm[kConfigs] = {256, BfMid::BM, BfLow::BM, 16, 32, 64};
-constexpr int kBn[kConfigs] = {256, BfMid::BN, BfLow::BN, 16, 32, 32};
+using BfFlat = BfCfg<32, 64, 2, 2, 5, 2>;
+using BfThin = BfCfg<16, 64, 1, 4, 6, 2>;
+constexpr int kBm[kConfigs] = {256, 128, 128, 128, 64, 32, 16, 16};
+constexpr int kBn[kConfigs] = {256, 256, 128, 64, 64, 64, 64, 16};
 
 namespace {
 
@@ -1046,12 +1142,16 @@ template <bool AK, bool BK, int MODE>
 hipError_t launch_tile(BfProblem p, const BfTile& t, hipStream_t stream) {
   const unsigned units = grid_of(p, t.bm, t.bn);
   if constexpr (!AK && !BK) {
-    if (t.cfg == kFew16) return start(bf16_few_kernel<1, 1, 4, MODE>, p, units, 512, stream);
-    if (t.cfg == kFew32) return start(bf16_few_kernel<2, 2, 3, MODE>, p, units, 512, stream);
-    if (t.cfg == kFew64) return start(bf16_few_kernel<4, 2, 2, MODE>, p, units, 512, stream);
+    if (t.cfg == kFew) return start(bf16_few_kernel<1, 1, 4, MODE>, p, units, 512, stream);
+  }
+  if constexpr (!AK) {   // (k-major tiles are 64 wide at least)
+    if (t.cfg == kThin) return start(bf16_kernel<BfThin, AK, BK, MODE>, p, units, BfThin::THREADS, stream);
+    if (t.cfg == kFlat) return start(bf16_kernel<BfFlat, AK, BK, MODE>, p, units, BfFlat::THREADS, stream);
   }
   if (t.cfg == kLow) return start(bf16_kernel<BfLow, AK, BK, MODE>, p, units, BfLow::THREADS, stream);
+  if (t.cfg == kHigh) return start(bf16_kernel<BfHigh, AK, BK, MODE>, p, units, BfHigh::THREADS, stream);
   if (t.cfg == kMid) return start(bf16_kernel<BfMid, AK, BK, MODE>, p, units, BfMid::THREADS, stream);
+  if (t.cfg == kDuo) return start(bf16_kernel<BfDuo, AK, BK, MODE>, p, units, BfDuo::THREADS, stream);
   const unsigned cus = (unsigned)device_cu_count();
   p.grid = (int)(units < cus ? units : cus);
   if constexpr (MODE == kBfDense && !AK && !BK) {
@@ -1069,11 +1169,12 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
   const int64_t rows = p.mode == kBfRowRuns ? (p.M + p.groups - 1) / p.groups : p.M;
   const int64_t runs = p.mode == kBfDense ? 1 : p.groups;
   auto units = [&](int c) { return runs * ((rows + kBm[c] - 1) / kBm[c]) * (((int64_t)p.N + kBn[c] - 1) / kBn[c]); };
-  const bool few = !p.a_kmajor && !p.b_kmajor;
-  if (few && rows <= 64) t.cfg = rows <= 16 ? kFew16 : rows <= 32 ? kFew32 : kFew64;
-  else if (rows > 64 && units(kBig) * 5 >= cus * 2) t.cfg = kBig;
-  else if (rows > 64 && p.N > 64) t.cfg = kMid;
-  else t.cfg = kLow;
+  if (rows > 128 && units(kBig) * 5 >= cus * 2) t.cfg = kBig;
+  else if (p.a_kmajor) t.cfg = kMid;
+  else if (rows <= 16) t.cfg = kThin;
+  else if (rows <= 32) t.cfg = kFlat;
+  else if (rows <= 128) t.cfg = kLow;
+  else t.cfg = kHigh;
   t.bm = kBm[t.cfg];
   t.bn = kBn[t.cfg];
   t.splits = 1;
@@ -1081,7 +1182,7 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
     const int64_t u = units(t.cfg), steps = (p.K + kBK - 1) / kBK;
     if (u < cus && u <= kSplitKMaxTiles) {
       int64_t s = cus / u;
-      const int64_t least = t.cfg >= kFew16 ? 8 : 4;     // steps of a split
+      const int64_t least = 5;     // steps of a split
       if (s > steps / least) s = steps / least;
       if (s > kBfMaxSplits) s = kBfMaxSplits;
       if (s > 1) t.splits = (int)s;
