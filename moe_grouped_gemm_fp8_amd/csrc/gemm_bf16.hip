@@ -591,19 +591,6 @@ __device__ __forceinline__ bool last_of_splits(const BfProblem& p, const BfUnit&
   __syncthreads();
   return *last;
 }
-// One value's parts: all loads are issued before the first is added.
-__device__ __forceinline__ v4f sum_splits(__amdgpu_buffer_rsrc_t ws, uint32_t tile, uint32_t at, int splits) {
-  v4f part[kBfMaxSplits], sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int s = 0; s < kBfMaxSplits; ++s)
-    if (s < splits)
-      part[s] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(ws, s * tile + at, 0, kCoherent));
-#pragma unroll
-  for (int s = 0; s < kBfMaxSplits; ++s)
-    if (s < splits) sum += part[s];
-  return sum;
-}
-
 // ------------------------------------------------------------------ kernel
 template <class C, bool AK, bool BK, int MODE>
 __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
@@ -724,72 +711,58 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
 }
 
 // ------------------------------------------------------------ few rows
-// At most 16 TM rows a run, both operands k-contiguous: the time is that of
-// streaming the weights once.  The eight waves of a workgroup split k among
-// themselves, 64 at a time in turn, and each loads its fragments of both
-// operands straight into registers (16 bytes a lane, a lane's k are
-// contiguous): no LDS and no barrier stands between a wave and its loads, and
-// 2 U steps of them are in flight.  The waves' sums meet in LDS at the end.
-template <int TM, int TN, int U, int MODE>
+// A few rows a run, both operands k-contiguous, a short k: the call's latency
+// counts.  A workgroup owns 16 rows x 16 columns; its eight waves split k among
+// themselves, 64 at a time in turn, and load their fragments of both operands
+// straight into registers (16 bytes a lane, a lane's k are contiguous): no LDS
+// and no barrier stands between a wave and its loads, and eight steps of them
+// are in flight.  The waves' sums meet in LDS at the end.  (1 x 1024 x 2048:
+// 5.5 us for the 6.6 of the thin tile.  A load of this shape touches 16 lines
+// for 1 KB where a copy into LDS touches 8, so longer k go the other way:
+// 16 x 2112 x 7168 19 us for 11.)
+template <int MODE>
 __global__ __launch_bounds__(512, 2) void bf16_few_kernel(BfProblem p) {
-  constexpr int BM = 16 * TM, BN = 16 * TN, TILES = TM * TN;
-  __shared__ v4f sums[8][TILES][64];
-  __shared__ int last;
+  constexpr int U = 4;       // steps of a batch; two batches in flight
+  __shared__ v4f sums[8][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   BfUnit w;
-  if (!find_unit<BM, BN, MODE>(p, lane, w)) return;
+  if (!find_unit<16, 16, MODE>(p, lane, w)) return;
   const int i = lane & 15, g = lane >> 4;
 
-  v4f acc[TM][TN];
-#pragma unroll
-  for (int a = 0; a < TILES; ++a) (&acc[0][0])[a] = v4f{0.f, 0.f, 0.f, 0.f};
-  const int steps = (w.ks + kBK - 1) / kBK;
-  // Offsets of a lane's row in the run's (column's) tile; rows and columns past
-  // the end read the last one and are not stored.  k goes into the scalar
-  // offset, and a lane whose k lies past the end of the run loads zeros.
-  const uint16_t* xp = p.a + w.m0 * p.lda + w.k0;
-  const uint16_t* wp = p.b + (MODE == kBfRowRuns ? max(w.g, 0) * p.b_stride : 0) + (int64_t)w.n0 * p.ldb + w.k0;
+  // Offsets of a lane's row in either tile; rows and columns past the end read
+  // the last one and are not stored.  k goes into the scalar offset, and a
+  // lane whose k lies past the end loads zeros.
+  const uint16_t* xp = p.a + w.m0 * p.lda;
+  const uint16_t* wp = p.b + (MODE == kBfRowRuns ? max(w.g, 0) * p.b_stride : 0) + (int64_t)w.n0 * p.ldb;
   const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(uniform((const void*)xp), 0x7fffffff);
   const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(uniform((const void*)wp), 0x7fffffff);
-  uint32_t xo[TM], wo[TN];
-#pragma unroll
-  for (int t = 0; t < TM; ++t) xo[t] = (uint32_t)(min(16 * t + i, w.rows - 1) * (int)p.lda + 8 * g) * 2;
-#pragma unroll
-  for (int t = 0; t < TN; ++t) wo[t] = (uint32_t)(min(16 * t + i, p.N - 1 - w.n0) * (int)p.ldb + 8 * g) * 2;
+  const uint32_t xo = (uint32_t)(min(i, w.rows - 1) * (int)p.lda + 8 * g) * 2;
+  const uint32_t wo = (uint32_t)(min(i, p.N - 1 - w.n0) * (int)p.ldb + 8 * g) * 2;
   struct Batch {
-    v4i x[U][2][TM], w[U][2][TN];
+    v4i x[U][2], w[U][2];
   };
-  // steps s0, s0 + 8, .. of this wave
-  auto fetch = [&](Batch& f, int s0) {
+  auto fetch = [&](Batch& f, int s0) {     // steps s0, s0 + 8, ..
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         const int k = uniform((s0 + 8 * u) * kBK + 32 * kk);
         const bool in = 8 * g < w.ks - k;
-#pragma unroll
-        for (int t = 0; t < TN; ++t)
-          f.w[u][kk][t] = __builtin_bit_cast(
-              v4i, __builtin_amdgcn_raw_buffer_load_b128(wr, in ? wo[t] : kNowhere, k * 2, kStream));
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-          f.x[u][kk][t] = __builtin_bit_cast(
-              v4i, __builtin_amdgcn_raw_buffer_load_b128(xr, in ? xo[t] : kNowhere, k * 2, 0));
+        f.w[u][kk] = __builtin_bit_cast(
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(wr, in ? wo : kNowhere, k * 2, kStream));
+        f.x[u][kk] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(xr, in ? xo : kNowhere, k * 2, 0));
       }
   };
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
   auto multiply = [&](const Batch& f) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-        for (int b = 0; b < TN; ++b)
-#pragma unroll
-          for (int a = 0; a < TM; ++a)
-            acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, f.w[u][kk][b]),
-                                                                __builtin_bit_cast(v8bf, f.x[u][kk][a]),
-                                                                acc[a][b], 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, f.w[u][kk]),
+                                                      __builtin_bit_cast(v8bf, f.x[u][kk]), acc, 0, 0, 0);
   };
+  const int steps = (w.ks + kBK - 1) / kBK;
   if (wave < steps) {
     Batch f0, f1;
     fetch(f0, wave);
@@ -801,39 +774,13 @@ __global__ __launch_bounds__(512, 2) void bf16_few_kernel(BfProblem p) {
       multiply(f1);
     }
   }
-#pragma unroll
-  for (int t = 0; t < TILES; ++t) sums[wave][t][lane] = (&acc[0][0])[t];
+  sums[wave][lane] = acc;
   __syncthreads();
-  // tile t's sum goes to wave t mod 8
-  constexpr int MINE = (TILES + 7) / 8;
-  v4f mine[MINE];
+  if (wave == 0 && i < w.rows) {
+    v4f sum = sums[0][lane];
 #pragma unroll
-  for (int j = 0; j < MINE; ++j) {
-    const int t = wave + 8 * j;
-    mine[j] = v4f{0.f, 0.f, 0.f, 0.f};
-    if (t < TILES)
-#pragma unroll
-      for (int v = 0; v < 8; ++v) mine[j] += sums[v][t][lane];
-  }
-  if (MODE == kBfDense && p.splits > 1) {
-    constexpr uint32_t kTile = BM * BN * 4;
-    const __amdgpu_buffer_rsrc_t ws =
-        buffer_rsrc(p.partial + (int64_t)w.tile * p.splits * (BM * BN), kTile * p.splits);
-#pragma unroll
-    for (int j = 0; j < MINE; ++j)
-      if (wave + 8 * j < TILES)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, mine[j]), ws,
-                                               w.split * kTile + ((wave + 8 * j) * 64 + lane) * 16, 0, kCoherent);
-    if (!last_of_splits(p, w, tid, &last)) return;
-#pragma unroll
-    for (int j = 0; j < MINE; ++j)
-      if (wave + 8 * j < TILES) mine[j] = sum_splits(ws, kTile, ((wave + 8 * j) * 64 + lane) * 16, p.splits);
-  }
-  const BfOut out(p, w.g);
-#pragma unroll
-  for (int j = 0; j < MINE; ++j) {
-    const int t = wave + 8 * j, r = 16 * (t / TN) + i;
-    if (t < TILES && r < w.rows) out.four(w.m0 + r, w.n0 + 16 * (t % TN) + 4 * g, mine[j]);
+    for (int v = 1; v < 8; ++v) sum += sums[v][lane];
+    BfOut(p, w.g).four(w.m0 + i, w.n0 + 4 * g, sum);
   }
 }
 
@@ -1142,16 +1089,18 @@ template <bool AK, bool BK, int MODE>
 hipError_t launch_tile(BfProblem p, const BfTile& t, hipStream_t stream) {
   const unsigned units = grid_of(p, t.bm, t.bn);
   if constexpr (!AK && !BK) {
-    if (t.cfg == kFew) return start(bf16_few_kernel<1, 1, 4, MODE>, p, units, 512, stream);
+    if (t.cfg == kFew) return start(bf16_few_kernel<MODE>, p, units, 512, stream);
   }
-  if constexpr (!AK) {   // (k-major tiles are 64 wide at least)
+  if constexpr (!AK) {
     if (t.cfg == kThin) return start(bf16_kernel<BfThin, AK, BK, MODE>, p, units, BfThin::THREADS, stream);
     if (t.cfg == kFlat) return start(bf16_kernel<BfFlat, AK, BK, MODE>, p, units, BfFlat::THREADS, stream);
+    if (t.cfg == kLow) return start(bf16_kernel<BfLow, AK, BK, MODE>, p, units, BfLow::THREADS, stream);
+    if (t.cfg == kHigh) return start(bf16_kernel<BfHigh, AK, BK, MODE>, p, units, BfHigh::THREADS, stream);
   }
-  if (t.cfg == kLow) return start(bf16_kernel<BfLow, AK, BK, MODE>, p, units, BfLow::THREADS, stream);
-  if (t.cfg == kHigh) return start(bf16_kernel<BfHigh, AK, BK, MODE>, p, units, BfHigh::THREADS, stream);
+  if constexpr (MODE == kBfKRuns) {
+    if (t.cfg == kDuo) return start(bf16_kernel<BfDuo, AK, BK, MODE>, p, units, BfDuo::THREADS, stream);
+  }
   if (t.cfg == kMid) return start(bf16_kernel<BfMid, AK, BK, MODE>, p, units, BfMid::THREADS, stream);
-  if (t.cfg == kDuo) return start(bf16_kernel<BfDuo, AK, BK, MODE>, p, units, BfDuo::THREADS, stream);
   const unsigned cus = (unsigned)device_cu_count();
   p.grid = (int)(units < cus ? units : cus);
   if constexpr (MODE == kBfDense && !AK && !BK) {
@@ -1169,16 +1118,35 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
   const int64_t rows = p.mode == kBfRowRuns ? (p.M + p.groups - 1) / p.groups : p.M;
   const int64_t runs = p.mode == kBfDense ? 1 : p.groups;
   auto units = [&](int c) { return runs * ((rows + kBm[c] - 1) / kBm[c]) * (((int64_t)p.N + kBn[c] - 1) / kBn[c]); };
-  if (rows > 128 && units(kBig) * 5 >= cus * 2) t.cfg = kBig;
-  else if (p.a_kmajor) t.cfg = kMid;
-  else if (rows <= 16) t.cfg = kThin;
-  else if (rows <= 32) t.cfg = kFlat;
-  else if (rows <= 128) t.cfg = kLow;
-  else t.cfg = kHigh;
+  // (times in us, the choice first; 256 CUs)
+  if (p.a_kmajor) {
+    // Long runs or one product: the big tile.  Many tiles of short runs are
+    // bound by their stores, which two workgroups a CU interleave with sums
+    // (32 runs of 64 rows, 7168 x 2048: 288 for 312).  Few tiles: small ones
+    // (16 runs of 250 rows, 2048 x 1024: 39 for 43 and 47).
+    const bool dense = p.mode == kBfDense;
+    if (dense ? 2 * units(kBig) >= cus : p.K >= 512 * runs && units(kBig) >= 16 * cus) t.cfg = kBig;
+    else t.cfg = !dense && units(kBig) >= 6 * cus ? kDuo : kMid;
+  } else if (rows > 128 && 2 * units(kBig) >= cus) {
+    // 128 big tiles on as many CUs: 4096 x 2048 x 7168, B k-major, 152 alone
+    // for 120, but 258 for 284 within its backward pass
+    t.cfg = kBig;
+  } else if (rows <= 8 && !p.b_kmajor && p.K <= 4096 && units(kFew) <= 2 * cus) {
+    t.cfg = kFew;      // 1 x 1024 x 2048 5.5 for 6.6; 1 x 2112 x 7168 12.8 for 11.2
+  } else if (rows <= (p.mode == kBfDense ? 16 : 8)) {
+    t.cfg = kThin;     // 16 x 2112 x 7168 11.3 for 12.2; 32 runs of 16 rows on average 366 for 345
+  } else if (rows <= 32) {
+    t.cfg = kFlat;     // 32 x 2112 x 7168 12.3 for 13.7
+  } else if (units(kMid) >= (p.mode == kBfDense ? 3 * cus / 2 : cus)) {
+    t.cfg = kMid;      // 1024 x 7168 x 2048 36 for 47; 512 x 7168 x 2048 35 for 29
+  } else {
+    // 128 x 2112 x 7168 18.9 for 19.5; 512 x 2112 x 7168 37 for over 45
+    t.cfg = rows <= 128 ? kLow : kHigh;
+  }
   t.bm = kBm[t.cfg];
   t.bn = kBn[t.cfg];
   t.splits = 1;
-  if (p.mode == kBfDense && t.cfg != kBig) {
+  if (p.mode == kBfDense && t.cfg != kBig && t.cfg != kFew) {
     const int64_t u = units(t.cfg), steps = (p.K + kBK - 1) / kBK;
     if (u < cus && u <= kSplitKMaxTiles) {
       int64_t s = cus / u;
