@@ -1140,18 +1140,20 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
   } else if (units(kMid) >= (p.mode == kBfDense ? 3 * cus / 2 : cus)) {
     t.cfg = kMid;      // 1024 x 7168 x 2048 36 for 47; 512 x 7168 x 2048 35 for 29
   } else {
-    // 128 x 2112 x 7168 18.9 for 19.5; 512 x 2112 x 7168 37 for over 45
-    t.cfg = rows <= 128 ? kLow : kHigh;
+    // 192 x 2112 x 7168 20.8 for 24.2; 384 x 2112 x 7168 28.9 for 33.9
+    t.cfg = rows <= 256 ? kLow : kHigh;
   }
   t.bm = kBm[t.cfg];
   t.bn = kBn[t.cfg];
   t.splits = 1;
   if (p.mode == kBfDense && t.cfg != kBig && t.cfg != kFew) {
+    // One workgroup a CU; two where several row tiles read the same weights
+    // (64 x 2112 x 7168 14.1 in 6 splits, 16.2 in 12; 128 x 2112 x 7168 18.9
+    // in 6, 19.8 in 3), and five steps a split at least.
     const int64_t u = units(t.cfg), steps = (p.K + kBK - 1) / kBK;
-    if (u < cus && u <= kSplitKMaxTiles) {
-      int64_t s = cus / u;
-      const int64_t least = 5;     // steps of a split
-      if (s > steps / least) s = steps / least;
+    if (4 * u < 3 * cus && u <= kSplitKMaxTiles) {
+      int64_t s = (rows > t.bm ? 2 * cus : cus) / u;
+      if (s > steps / 5) s = steps / 5;
       if (s > kBfMaxSplits) s = kBfMaxSplits;
       if (s > 1) t.splits = (int)s;
     }

@@ -317,6 +317,53 @@ def test_dense_in_a_graph(dev):
         assert torch.equal(out, want), f"replay {i}"
 
 
+# ------------------------------------------------- every tile, at its sizes
+def _check_on_gpu(got, want, s, k, what):
+    err = _sum_error(k, s)
+    if got.dtype == BF16:
+        err = err + 2.0 ** -8 * (want.abs() + err)
+    bad = ~((got.double() - want).abs() <= err + 1e-38)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off"
+
+
+# rows a run on average, n, k: thin, flat, low, mid and big tiles (and the
+# few-rows kernel) of the forward pass and of the input gradient
+@pytest.mark.parametrize("experts,rows,n,k", [(8, 40, 1024, 520), (5, 33, 200, 4360), (6, 150, 1000, 136),
+                                              (9, 500, 136, 200), (16, 700, 1032, 1096), (16, 2100, 1096, 1032),
+                                              (4, 3000, 4104, 264)])
+def test_grouped_tiles(dev, experts, rows, n, k):
+    """Float64 products on the GPU as the reference: one product an expert."""
+    print(f"grouped tiles {experts} experts {rows} rows {n}x{k}", flush=True)
+    g = _gen(14, rows, n)
+    cut = torch.sort(torch.randint(0, rows + 1, (experts - 1,), generator=g)).values.tolist()
+    off = [0] + cut + [rows]
+    x, dy, w = _bf16(g, rows, k).to(dev), _bf16(g, rows, n).to(dev), _bf16(g, experts, n, k).to(dev)
+    o = torch.tensor(off, dtype=torch.int32, device=dev)
+    y, dx = _fg8().grouped_gemm_bf16(x, w, o), _fg8().grouped_gemm_bf16_dgrad(dy, w, o, out_dtype=F32)
+    for e in range(experts):
+        a, b = off[e], off[e + 1]
+        we = w[e].double()
+        _check_on_gpu(y[a:b], x[a:b].double() @ we.T, x[a:b].double().abs() @ we.abs().T, k, f"y of expert {e}")
+        _check_on_gpu(dx[a:b], dy[a:b].double() @ we, dy[a:b].double().abs() @ we.abs(), n, f"dx of expert {e}")
+
+
+# the weight gradient's tiles: 128 x 128; 128 x 256 with 32-deep steps (many
+# tiles of short runs); 256 x 256 (long runs)
+@pytest.mark.parametrize("experts,rows,n,k", [(5, 700, 520, 264), (40, 900, 1800, 1544), (64, 33000, 2048, 2040)])
+def test_grouped_wgrad_tiles(dev, experts, rows, n, k):
+    print(f"grouped wgrad tiles {experts} experts {rows} rows {n}x{k}", flush=True)
+    g = torch.Generator(device=dev).manual_seed(rows)
+    share = torch.sort(torch.randint(0, rows + 1, (experts - 1,), generator=g, device=dev)).values.tolist()
+    off = [0] + share + [rows]
+    x = torch.randn(rows, k, generator=g, device=dev).to(BF16)
+    dy = torch.randn(rows, n, generator=g, device=dev).to(BF16)
+    dw = _fg8().grouped_gemm_bf16_wgrad(dy, x, torch.tensor(off, dtype=torch.int32, device=dev))
+    for e in range(experts):
+        a, b = off[e], off[e + 1]
+        p, q = dy[a:b].double().T, x[a:b].double()
+        _check_on_gpu(dw[e], p @ q, p.abs() @ q.abs(), b - a, f"dw of expert {e}")
+
+
 # ---------------------------------------------------------------- refusals
 def test_refusals(dev):
     fg8 = _fg8()
