@@ -122,12 +122,12 @@ struct RowVec<uint16_t> {   // BF16 bits widen exactly to FP32
 __device__ __forceinline__ float normal_cdf(float z, float* bell) {
   const float x = fabsf(z) * 0.70710678118654752f;
   const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
-  const float e = __builtin_amdgcn_exp2f(x * x * -1.4426950408889634f);
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  const float n = 0.5f * p * t * e;
+  const float e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);   // -z^2 / 2 log2 e
+  float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);            // (half of erfc)
+  p = fmaf(p, t, 0.5f * 1.421413741f);
+  p = fmaf(p, t, 0.5f * -0.284496736f);
+  p = fmaf(p, t, 0.5f * 0.254829592f);
+  const float n = p * t * e;
   *bell = e;
   return z < 0.f ? n : 1.f - n;
 }

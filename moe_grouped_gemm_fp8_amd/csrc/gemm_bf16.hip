@@ -333,15 +333,27 @@ __device__ __forceinline__ bool find_unit(const BfProblem& p, int lane, BfUnit& 
 }
 
 // ---------------------------------------------------------------- epilogue
-__device__ __forceinline__ float act_of(int act, float z) {
-  if (act == kActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
-  if (act == kActSilu)   // (-0 for very negative z: exp2 gives inf, its reciprocal 0)
-    return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
-  if (act == kActGelu) {
-    float bell;
-    return z * normal_cdf(z, &bell);
+template <class F, int N>
+__device__ __forceinline__ void each(v4f (&v)[N], F f) {
+#pragma unroll
+  for (int e = 0; e < 4 * N; ++e) v[e / 4][e % 4] = f(v[e / 4][e % 4]);
+}
+// act(v) in place; the branch is taken once for all the values
+template <int N>
+__device__ __forceinline__ void activate(int act, v4f (&v)[N]) {
+  if (act == kActRelu) {
+    each(v, [](float z) { return z < 0.f ? 0.f : z; });      // (NaN stays)
+  } else if (act == kActSilu) {
+    // -0 for very negative z: exp2 gives inf, its reciprocal 0
+    each(v, [](float z) {
+      return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+    });
+  } else if (act == kActGelu) {
+    each(v, [](float z) {
+      float bell;
+      return z * normal_cdf(z, &bell);
+    });
   }
-  return z;
 }
 
 // bias[n .. n + 3] (0 past N, or without a bias)
@@ -378,10 +390,9 @@ struct BfOut {
   __device__ void four(int64_t m, int n, v4f v) const {
     if (p.bias) v += bias4(p, n);
     if (p.z) store(p.z, p.ldz, true, m, n, v);
-    if (p.act != kActNone) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = act_of(p.act, v[i]);
-    }
+    v4f t[1] = {v};
+    activate(p.act, t);
+    v = t[0];
     if (p.residual) {
       const uint2 w = residual4(p, m, n);
       v += v4f{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
@@ -485,8 +496,7 @@ __device__ __forceinline__ void store_f32_rows(uint8_t* turn, v4f a, v4f b, floa
 }
 // Sixteen rows x 64 columns staged as FP32 (4 KB), the residual's piece (res)
 // added on the way out.
-__device__ __forceinline__ void store_rows_plus(uint8_t* turn, const v4f (&v)[4], const uint4 (&res)[2], bool has_res,
-                                                void* to, int64_t ld, bool bf16, int rows, int n, int N, int lane,
+__device__ __forceinline__ void store_rows_plus(uint8_t* turn, const v4f (&v)[4], const uint4 (&res)[2], void* to, int64_t ld, bool bf16, int rows, int n, int N, int lane,
                                                 bool full) {
   const int i = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -496,12 +506,10 @@ __device__ __forceinline__ void store_rows_plus(uint8_t* turn, const v4f (&v)[4]
     const int r = 8 * h + (lane >> 3), c = lane & 7;
     v4f a = *reinterpret_cast<const v4f*>(turn + r * 256 + (((2 * c) ^ r) << 4));
     v4f b = *reinterpret_cast<const v4f*>(turn + r * 256 + (((2 * c + 1) ^ r) << 4));
-    if (has_res) {
-      float f[8];
-      RowVec<uint16_t>::widen(res[h], f);
-      a += v4f{f[0], f[1], f[2], f[3]};
-      b += v4f{f[4], f[5], f[6], f[7]};
-    }
+    float f[8];
+    RowVec<uint16_t>::widen(res[h], f);
+    a += v4f{f[0], f[1], f[2], f[3]};
+    b += v4f{f[4], f[5], f[6], f[7]};
     if (full || r < rows) {
       if (bf16) {
         store_eight((uint16_t*)to + r * ld, ld, n + 8 * c, N, full,
@@ -515,12 +523,12 @@ __device__ __forceinline__ void store_rows_plus(uint8_t* turn, const v4f (&v)[4]
 }
 // residual[m][c .. c + 7] (0 past N)
 __device__ __forceinline__ uint4 residual8(const BfProblem& p, int64_t m, int c) {
-  const uint16_t* r = p.residual + m * p.ldr + c;
-  if (p.ldr % 8 == 0 && c + 8 <= p.N) return *reinterpret_cast<const uint4*>(r);
+  const uint16_t* r = p.residual + m * p.ldr;
+  if (p.ldr % 8 == 0 && c + 8 <= p.N) return *reinterpret_cast<const uint4*>(r + c);
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (c + i < p.N) w[i / 2] |= (uint32_t)r[i] << (16 * (i & 1));
+    if (c + i < p.N) w[i / 2] |= (uint32_t)r[c + i] << (16 * (i & 1));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -561,13 +569,13 @@ struct TileOut {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] += bias[i];
       if (p.z) store_bf16_rows(turn, v, p.z + m * p.ldz, p.ldz, left, n, p.N, lane, whole && p.ldz % 8 == 0);
-      if (p.act != kActNone) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e / 4][e % 4] = act_of(p.act, v[e / 4][e % 4]);
+      activate(p.act, v);
+      if (p.residual) {
+        store_rows_plus(turn, v, res, d + m * p.ldd * (p.out_bf16 ? 2 : 4), p.ldd, p.out_bf16, left, n, p.N, lane, full);
+        return;
       }
-      store_rows_plus(turn, v, res, p.residual != nullptr, d + m * p.ldd * (p.out_bf16 ? 2 : 4), p.ldd, p.out_bf16,
-                      left, n, p.N, lane, full);
-    } else if (p.out_bf16) {
+    }
+    if (p.out_bf16) {
       store_bf16_rows(turn, v, (uint16_t*)d + m * p.ldd, p.ldd, left, n, p.N, lane, full);
     } else {
       store_f32_rows(turn, v[0], v[1], (float*)d + m * p.ldd, p.ldd, left, n, p.N, lane, full);
@@ -1024,6 +1032,12 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
       __syncthreads();              // every wave's, and its reads
     }
 
+    const int here = opaque(lane);
+    TileOut<EPI> out(p, w, 256, 256, q * 64, smem + 8 * kHalf + wave * TileOut<EPI>::kTurn, here);
+    if constexpr (EPI) {       // the bias has arrived before the copies below queue up
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(out.bias[i]));
+    }
     // the next unit's first copies, under this one's epilogue
     BfUnit next{};
     u += G;
@@ -1032,20 +1046,21 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
       if (next.ks > 0) start(next);
     }
 
-    const int here = opaque(lane);
-    const TileOut<EPI> out(p, w, 256, 256, q * 64, smem + 8 * kHalf + wave * TileOut<EPI>::kTurn, here);
+    // (the residual one group of sixteen rows ahead: before the stores, which
+    // its loads would have to wait for)
+    uint4 res[2], ahead[2];
+    if constexpr (EPI) out.residual(grp * 128, res);
 #pragma unroll
-    for (int ha = 0; ha < 2; ++ha) {
-      const int r0 = grp * 128 + ha * 64;
-      uint4 res[4][2];
-      if constexpr (EPI) {      // all of a half's loads before its stores
-#pragma unroll
-        for (int i = 0; i < 4; ++i) out.residual(r0 + 16 * i, res[i]);
+    for (int g = 0; g < 8; ++g) {
+      if constexpr (EPI) {
+        if (g < 7) out.residual(grp * 128 + 16 * (g + 1), ahead);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v4f v[4] = {acc[ha][i][0][0], acc[ha][i][0][1], acc[ha][i][1][0], acc[ha][i][1][1]};
-        out.rows16(r0 + 16 * i, v, res[i]);
+      const int ha = g / 4, i = g % 4;
+      v4f v[4] = {acc[ha][i][0][0], acc[ha][i][0][1], acc[ha][i][1][0], acc[ha][i][1][1]};
+      out.rows16(grp * 128 + 16 * g, v, res);
+      if constexpr (EPI) {
+        res[0] = ahead[0];
+        res[1] = ahead[1];
       }
     }
     if (u >= total) return;
