@@ -1140,7 +1140,7 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
     // (32 runs of 64 rows, 7168 x 2048: 288 for 312).  Few tiles: small ones
     // (16 runs of 250 rows, 2048 x 1024: 39 for 43 and 47).
     const bool dense = p.mode == kBfDense;
-    if (dense ? 2 * units(kBig) >= cus : p.K >= 512 * runs && units(kBig) >= 16 * cus) t.cfg = kBig;
+    if (dense ? 2 * units(kBig) >= cus : p.K >= 400 * runs && units(kBig) >= 16 * cus) t.cfg = kBig;
     else t.cfg = !dense && units(kBig) >= 6 * cus ? kDuo : kMid;
   } else if (rows > 128 && 2 * units(kBig) >= cus) {
     // 128 big tiles on as many CUs: 4096 x 2048 x 7168, B k-major, 152 alone

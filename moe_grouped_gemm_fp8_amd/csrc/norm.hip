@@ -7,7 +7,10 @@
 //   dweight = sum over rows of dy h,   dbias = sum over rows of dy
 //
 // All arithmetic is FP32.  HBM bounds these: a row is read once (x, and dy)
-// and written once.  A team of WAVES waves owns a row at a time and holds it
+// and written once.  Measured: forward 32768 x 7168 BF16 0.170 ms (5.5 TB/s)
+// and 16383 x 7168 FP32 0.178 ms, backward 0.300 (4.7 TB/s) and 0.265 ms; a
+// plain copy moves 4.9 TB/s here.  Rows of odd length cost nothing extra:
+// 20000 x 2051 FP32 0.059 and 0.100 ms, 5.5 and 4.9 TB/s.  A team of WAVES waves owns a row at a time and holds it
 // in registers, so the variance is taken around the mean (two passes over
 // registers, not the sum of squares); a thread owns the same columns of every
 // row its team takes, which keeps the weight and, backward, both parameters'
@@ -22,17 +25,13 @@ namespace fg8 {
 
 namespace {
 
-// Sixteen bytes of a row at element `c` as FP32: the elements at or past
-// `cols` are zeros.  Rows need no alignment beyond their element's.
+// Sixteen bytes of a row: rows need no alignment beyond their element's.
 template <class T>
 struct Piece {
   static constexpr int N = 16 / sizeof(T);
+  // elements c .. c + N - 1, those at or past `cols` zeros
   __device__ static uint4 load(const T* row, int64_t c, int64_t cols) {
-    if (c + N <= cols) {
-      uint4 v;   // (one 16-byte load at any element's address)
-      __builtin_memcpy(&v, row + c, 16);
-      return v;
-    }
+    if (c + N <= cols) return whole(row + c);
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -42,41 +41,32 @@ struct Piece {
       }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ static void store(T* row, int64_t c, int64_t cols, const float* f) {
+  __device__ static uint4 whole(const T* p) {
+    uint4 v;   // (one 16-byte load at any element's address)
+    __builtin_memcpy(&v, p, 16);
+    return v;
+  }
+  __device__ static void store(T* row, int64_t c, int64_t cols, const float* f) { store(row, c, c, cols, f); }
+  // elements max(c, from) .. of c .. c + N - 1 that lie before `cols`
+  __device__ static void store(T* row, int64_t c, int64_t from, int64_t cols, const float* f) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
       else w[i] = bf16x2(f[2 * i], f[2 * i + 1]);
     }
-    if (c + N <= cols) {
+    if (c + N <= cols && from <= c) {
       __builtin_memcpy(row + c, w, 16);
       return;
     }
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (c + i < cols) {
+      if (c + i < cols && c + i >= from) {
         if constexpr (sizeof(T) == 4) row[c + i] = f[i];
         else row[c + i] = (T)(w[i / 2] >> (16 * (i & 1)));
       }
   }
 };
-
-// N parameter values from element c on (0 past cols), FP32 or BF16, in
-// 16-byte loads where all of them exist
-template <int N>
-__device__ __forceinline__ void params(const void* p, bool bf16, int64_t c, int64_t cols, float* f) {
-  if (bf16) {
-    float w[8];
-    RowVec<uint16_t>::widen(c < cols ? Piece<uint16_t>::load((const uint16_t*)p, c, cols) : make_uint4(0, 0, 0, 0), w);
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = w[i];
-  } else {
-#pragma unroll
-    for (int h = 0; h < N; h += 4)
-      RowVec<float>::widen(c + h < cols ? Piece<float>::load((const float*)p, c + h, cols) : make_uint4(0, 0, 0, 0), f + h);
-  }
-}
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -112,13 +102,18 @@ constexpr int threads_of() { return WAVES == 1 ? 256 : 64 * WAVES; }
 template <int WAVES>
 constexpr int teams_of() { return WAVES == 1 ? 4 : 1; }
 
-// What a thread of a team holds: NV pieces of N columns each.  LEAN (the
-// longest rows, sixteen waves of 128 registers a lane): no row ahead in
-// registers, and the weight is read again for every row.
-template <class T, int WAVES, int NV, bool BACKWARD>
+// What a thread of a team holds: NV pieces of N columns each.  A row is loaded
+// without branches, so that all its loads are in flight together: a piece that
+// would cross the row's end starts at the row's last N elements instead, and
+// what lies before its own first column (another thread's) is masked to zero.
+// (Rows shorter than a piece are loaded by element: TINY.)  LEAN, where a
+// lane's registers do not suffice (more than 16 columns a thread; backward,
+// teams of sixteen waves, which have 128 a lane): no row ahead in flight, and
+// the parameters are read again for every row.
+template <class T, int WAVES, int NV, bool TINY, bool BACKWARD>
 struct Team {
   static constexpr int N = Piece<T>::N;
-  static constexpr bool LEAN = NV * N > 16 || (BACKWARD && WAVES == 16);
+  static constexpr bool LEAN = NV * N > 16 || (BACKWARD && WAVES > 8);
   int lane, wave, me, cols;
   int64_t team, teams;
   __device__ Team(int cols_) : cols(cols_) {
@@ -128,20 +123,56 @@ struct Team {
     team = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
     teams = (int64_t)gridDim.x * teams_of<WAVES>();
   }
-  __device__ int column(int i) const { return (i * 64 * WAVES + me) * N; }
+  __device__ int own(int i) const { return (i * 64 * WAVES + me) * N; }              // its own first column
+  __device__ int column(int i) const { return TINY ? own(i) : min(own(i), cols - N); }   // where its piece starts
+  __device__ bool mine(int i, int j) const { return TINY ? own(i) + j < cols : column(i) + j >= own(i); }
+  // are all lanes' pieces i whole?  (the same answer in every lane)
+  __device__ bool whole(int i) const { return (i + 1) * 64 * WAVES * N <= cols; }
+  __device__ uint4 masked(int i, uint4 v) const {
+    if (TINY || whole(i)) return v;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (N == 4) w[k] = mine(i, k) ? w[k] : 0u;
+      else w[k] &= (mine(i, 2 * k) ? 0xffffu : 0u) | (mine(i, 2 * k + 1) ? 0xffff0000u : 0u);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  template <class U>
+  __device__ uint4 fetch(const U* row, int c) const {
+    return TINY ? Piece<U>::load(row, c, cols) : Piece<U>::whole(row + c);
+  }
   __device__ void load(const T* row, uint4 (&raw)[NV]) const {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      raw[i] = column(i) < cols ? Piece<T>::load(row, column(i), cols) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < NV; ++i) raw[i] = fetch(row, column(i));
+  }
+  // N parameter values of piece i, FP32 or BF16
+  __device__ void parameters(const void* p, bool bf16, int i, float* f) const {
+    if (bf16) {
+      const uint16_t* q = (const uint16_t*)p;
+      if constexpr (N == 8) {
+        RowVec<uint16_t>::widen(fetch(q, column(i)), f);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          f[j] = !TINY || column(i) + j < cols ? __uint_as_float((uint32_t)q[column(i) + j] << 16) : 0.f;
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < N; h += 4) {
+        if (TINY && own(i) + h >= cols) f[h] = f[h + 1] = f[h + 2] = f[h + 3] = 0.f;
+        else RowVec<float>::widen(fetch((const float*)p, column(i) + h), f + h);
+      }
+    }
   }
 };
 
-template <class T, int WAVES, int NV>
+template <class T, int WAVES, int NV, bool TINY>
 __global__ __launch_bounds__(threads_of<WAVES>()) void norm_kernel(
     const T* __restrict__ x, int64_t ldx, const void* __restrict__ weight,
     const void* __restrict__ bias, bool w_bf16, float eps, int64_t rows, int cols,
     T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd) {
-  typedef Team<T, WAVES, NV, false> Me;
+  typedef Team<T, WAVES, NV, TINY, false> Me;
   constexpr int N = Me::N;
   __shared__ float buf[2][16][2];
   const Me t(cols);
@@ -149,10 +180,9 @@ __global__ __launch_bounds__(threads_of<WAVES>()) void norm_kernel(
   uint4 raw[NV], ahead[NV];
   float w[NV][N], b[NV][N];
   auto parameters = [&](int i) {
-    const int c = t.column(i);
-    params<N>(weight, w_bf16, c, cols, w[i]);
+    t.parameters(weight, w_bf16, i, w[i]);
     if (bias) {
-      params<N>(bias, w_bf16, c, cols, b[i]);
+      t.parameters(bias, w_bf16, i, b[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < N; ++j) b[i][j] = 0.f;
@@ -170,7 +200,7 @@ __global__ __launch_bounds__(threads_of<WAVES>()) void norm_kernel(
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float f[N];
-      RowVec<T>::widen(raw[i], f);
+      RowVec<T>::widen(t.masked(i, raw[i]), f);
 #pragma unroll
       for (int j = 0; j < N; ++j) s[0] += f[j];
     }
@@ -181,10 +211,15 @@ __global__ __launch_bounds__(threads_of<WAVES>()) void norm_kernel(
     for (int i = 0; i < NV; ++i) {
       float f[N];
       RowVec<T>::widen(raw[i], f);
+      if (t.whole(i)) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float d = t.column(i) + j < cols ? f[j] - m : 0.f;
-        q[0] = fmaf(d, d, q[0]);
+        for (int j = 0; j < N; ++j) q[0] = fmaf(f[j] - m, f[j] - m, q[0]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float d = t.mine(i, j) ? f[j] - m : 0.f;
+          q[0] = fmaf(d, d, q[0]);
+        }
       }
     }
     team_sum<WAVES, 1>(q, buf, at, t.wave, t.lane);
@@ -196,7 +231,7 @@ __global__ __launch_bounds__(threads_of<WAVES>()) void norm_kernel(
       RowVec<T>::widen(raw[i], f);
 #pragma unroll
       for (int j = 0; j < N; ++j) o[j] = fmaf((f[j] - m) * rs, w[i][j], b[i][j]);
-      if (t.column(i) < cols) Piece<T>::store(y + r * cols, t.column(i), cols, o);
+      if (t.own(i) < cols) Piece<T>::store(y + r * cols, t.column(i), t.own(i), cols, o);
     }
     if (t.me == 0) {
       mean[r] = m;
@@ -210,13 +245,13 @@ __global__ __launch_bounds__(threads_of<WAVES>()) void norm_kernel(
   }
 }
 
-template <class T, int WAVES, int NV>
+template <class T, int WAVES, int NV, bool TINY>
 __global__ __launch_bounds__(threads_of<WAVES>()) void norm_backward_kernel(
     const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
     const void* __restrict__ weight, bool w_bf16, const float* __restrict__ mean,
     const float* __restrict__ rstd, int64_t rows, int cols, T* __restrict__ dx,
     float* __restrict__ partial) {
-  typedef Team<T, WAVES, NV, true> Me;
+  typedef Team<T, WAVES, NV, TINY, true> Me;
   constexpr int N = Me::N;
   __shared__ float buf[2][16][2];
   const Me t(cols);
@@ -233,42 +268,53 @@ __global__ __launch_bounds__(threads_of<WAVES>()) void norm_backward_kernel(
   if (t.team < rows) fetch(t.team, rx, rd, m, rs);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if constexpr (!Me::LEAN) params<N>(weight, w_bf16, t.column(i), cols, w[i]);
+    if constexpr (!Me::LEAN) t.parameters(weight, w_bf16, i, w[i]);
 #pragma unroll
     for (int j = 0; j < N; ++j) dw[i][j] = db[i][j] = 0.f;
   }
+  // h, and g times the weight, of piece i; what is not this thread's is zero
+  // in g (and may be anything in h, whose columns nobody stores from here)
+  float h[NV][N], g[NV][N];
+  auto widen = [&](int i) {
+    RowVec<T>::widen(rx[i], h[i]);
+    RowVec<T>::widen(t.masked(i, rd[i]), g[i]);
+    if constexpr (Me::LEAN) t.parameters(weight, w_bf16, i, w[i]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) h[i][j] = (h[i][j] - m) * rs;
+  };
   for (int64_t r = t.team; r < rows; r += t.teams) {
     const bool more = r + t.teams < rows;
     if (!Me::LEAN && more) fetch(r + t.teams, nx, nd, nm, nrs);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float h[N], g[N];
-      RowVec<T>::widen(rx[i], h);
-      RowVec<T>::widen(rd[i], g);
-      if constexpr (Me::LEAN) params<N>(weight, w_bf16, t.column(i), cols, w[i]);
+      widen(i);
+      if (!t.whole(i)) {     // (another thread's column may hold NaN: it must not meet these sums)
+#pragma unroll
+        for (int j = 0; j < N; ++j) h[i][j] = t.mine(i, j) ? h[i][j] : 0.f;
+      }
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        // past the last column dy and the weight are zeros: h adds nothing
-        h[j] = (h[j] - m) * rs;
-        dw[i][j] = fmaf(g[j], h[j], dw[i][j]);
-        db[i][j] += g[j];
-        g[j] *= w[i][j];
-        s[0] += g[j];
-        s[1] = fmaf(g[j], h[j], s[1]);
+        dw[i][j] = fmaf(g[i][j], h[i][j], dw[i][j]);
+        db[i][j] += g[i][j];
+        g[i][j] *= w[i][j];
+        s[0] += g[i][j];
+        s[1] = fmaf(g[i][j], h[i][j], s[1]);
       }
     }
     team_sum<WAVES, 2>(s, buf, at, t.wave, t.lane);
     const float c1 = s[0] * inv, c2 = s[1] * inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float h[N], g[N], o[N];
-      RowVec<T>::widen(rx[i], h);
-      RowVec<T>::widen(rd[i], g);
-      if constexpr (Me::LEAN) params<N>(weight, w_bf16, t.column(i), cols, w[i]);
+      float o[N];
+      if constexpr (Me::LEAN) {          // again from the packed row: half the registers
+        widen(i);
 #pragma unroll
-      for (int j = 0; j < N; ++j) o[j] = rs * (g[j] * w[i][j] - c1 - (h[j] - m) * rs * c2);
-      if (t.column(i) < cols) Piece<T>::store(dx + r * cols, t.column(i), cols, o);
+        for (int j = 0; j < N; ++j) g[i][j] *= w[i][j];
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[j] = rs * (g[i][j] - c1 - h[i][j] * c2);
+      if (t.own(i) < cols) Piece<T>::store(dx + r * cols, t.column(i), t.own(i), cols, o);
     }
     if (Me::LEAN && more) fetch(r + t.teams, rx, rd, m, rs);
     if constexpr (!Me::LEAN) {
@@ -281,15 +327,15 @@ __global__ __launch_bounds__(threads_of<WAVES>()) void norm_backward_kernel(
       rs = nrs;
     }
   }
-  float* mine = partial + t.team * 2 * cols;
+  float* sums = partial + t.team * 2 * cols;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < N; j += 4) {
       const int c = t.column(i) + j;
-      if (c < cols) {
-        Piece<float>::store(mine, c, cols, dw[i] + j);
-        Piece<float>::store(mine + cols, c, cols, db[i] + j);
+      if (t.own(i) < cols) {
+        Piece<float>::store(sums, c, t.own(i), cols, dw[i] + j);
+        Piece<float>::store(sums + cols, c, t.own(i), cols, db[i] + j);
       }
     }
 }
@@ -321,9 +367,10 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
 
 // The team shape for a row length: waves a row and 16-byte pieces a thread.
 // Sixteen columns a thread are the rule (registers for a row ahead and,
-// backward, both running sums); the longest rows have no more waves to spread
-// over.
-template <class T, class F>
+// backward, both running sums); the longest rows take 32.  (Backward, 16000 x
+// 12000 BF16: 0.48 ms in eight waves of 32 columns, 0.76 in sixteen of 16; FP32
+// 8000 x 16384 0.79 and 0.62.)
+template <class T, bool BACKWARD, class F>
 hipError_t with_shape(int64_t cols, F f) {
   constexpr int P = sizeof(T) == 4 ? 2 : 1;        // pieces of eight columns
   constexpr std::integral_constant<int, P> p1{};
@@ -333,13 +380,17 @@ hipError_t with_shape(int64_t cols, F f) {
   constexpr std::integral_constant<int, 4> w4{};
   constexpr std::integral_constant<int, 8> w8{};
   constexpr std::integral_constant<int, 16> w16{};
-  if (cols <= 512) return f(w1, p1);
-  if (cols <= 1024) return f(w1, p2);
-  if (cols <= 2048) return f(w4, p1);
-  if (cols <= 4096) return f(w4, p2);
-  if (cols <= 8192) return f(w8, p2);
-  if (cols <= 16384) return f(w16, p2);
-  return f(w16, p4);
+  if (cols < Piece<T>::N) return f(w1, p1, std::true_type{});
+  if (cols <= 512) return f(w1, p1, std::false_type{});
+  if (cols <= 1024) return f(w1, p2, std::false_type{});
+  if (cols <= 2048) return f(w4, p1, std::false_type{});
+  if (cols <= 4096) return f(w4, p2, std::false_type{});
+  if (cols <= 8192) return f(w8, p2, std::false_type{});
+  if constexpr (BACKWARD && sizeof(T) == 2) {
+    if (cols <= 16384) return f(w8, p4, std::false_type{});
+  }
+  if (cols <= 16384) return f(w16, p2, std::false_type{});
+  return f(w16, p4, std::false_type{});
 }
 
 // Workgroups: enough for two or more a SIMD, and no more than there are rows.
@@ -356,7 +407,7 @@ namespace {
 template <class T>
 int64_t teams_as(int64_t rows, int64_t cols, int cus) {
   int64_t teams = 0;
-  (void)with_shape<T>(cols, [&](auto waves, auto) {
+  (void)with_shape<T, true>(cols, [&](auto waves, auto, auto) {
     teams = groups_of(waves, rows, cus) * teams_of<decltype(waves)::value>();
     return hipSuccess;
   });
@@ -367,9 +418,9 @@ template <class T>
 hipError_t norm_as(const void* x, int64_t ldx, const void* weight, const void* bias, bool w_bf16,
                    float eps, int64_t rows, int64_t cols, void* y, float* mean, float* rstd, int cus,
                    hipStream_t stream) {
-  return with_shape<T>(cols, [&](auto waves, auto nv) {
+  return with_shape<T, false>(cols, [&](auto waves, auto nv, auto tiny) {
     constexpr int W = decltype(waves)::value, NV = decltype(nv)::value;
-    hipLaunchKernelGGL((norm_kernel<T, W, NV>), dim3((unsigned)groups_of(W, rows, cus)),
+    hipLaunchKernelGGL((norm_kernel<T, W, NV, decltype(tiny)::value>), dim3((unsigned)groups_of(W, rows, cus)),
                        dim3(threads_of<W>()), 0, stream, (const T*)x, ldx, weight, bias, w_bf16, eps,
                        rows, (int)cols, (T*)y, mean, rstd);
     return hipGetLastError();
@@ -381,9 +432,9 @@ hipError_t norm_backward_as(const void* dy, int64_t lddy, const void* x, int64_t
                             const void* weight, bool w_bf16, const float* mean, const float* rstd,
                             int64_t rows, int64_t cols, void* dx, float* partial, int cus,
                             hipStream_t stream) {
-  return with_shape<T>(cols, [&](auto waves, auto nv) {
+  return with_shape<T, true>(cols, [&](auto waves, auto nv, auto tiny) {
     constexpr int W = decltype(waves)::value, NV = decltype(nv)::value;
-    hipLaunchKernelGGL((norm_backward_kernel<T, W, NV>), dim3((unsigned)groups_of(W, rows, cus)),
+    hipLaunchKernelGGL((norm_backward_kernel<T, W, NV, decltype(tiny)::value>), dim3((unsigned)groups_of(W, rows, cus)),
                        dim3(threads_of<W>()), 0, stream, (const T*)dy, lddy, (const T*)x, ldx, weight,
                        w_bf16, mean, rstd, rows, (int)cols, (T*)dx, partial);
     return hipGetLastError();
