@@ -345,7 +345,8 @@ int64_t fg8_moe_capacity(int64_t tokens, int32_t topk, int32_t num_experts);
  * bit patterns.  ld arguments count elements between rows and let a row be
  * part of a wider one; pointers are 16-byte aligned as everywhere, and ld of
  * an operand that a product reads is a multiple of 8 and at most 2^22 (a
- * larger one is FG8_EUNSUPPORTED).  All sums are FP32, rounded once where the
+ * larger one is FG8_EUNSUPPORTED); the products take 2^31 - 1024 rows at most
+ * (more: FG8_EUNSUPPORTED).  All sums are FP32, rounded once where the
  * output is BF16.  Sums run in a fixed order: the same call gives the same
  * bits.  m, rows or tokens of 0 are valid where a call takes them: nothing is
  * read, and gradients summed over them are zeros.
@@ -362,7 +363,7 @@ int64_t fg8_moe_capacity(int64_t tokens, int32_t topk, int32_t num_experts);
  *                [0, rows]; the kernels clamp each to that range
  *   y            [rows][ldy] float or bf16; rows before the first and after
  *                the last run are written as zeros
- *   k % 8 == 0 (else FG8_EUNSUPPORTED), any n, 0 <= rows < 2^31,
+ *   k % 8 == 0 (else FG8_EUNSUPPORTED), any n, rows >= 0,
  *   1 <= num_experts <= 1024.
  */
 fg8_status grouped_gemm_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w,
@@ -407,7 +408,7 @@ typedef enum {
  *   z         NULL, or bf16 [m][n] (output): x w^T + bias, what the backward
  *             pass takes the activation's slope at
  *   y         [m][ldy] float or bf16; it may be the residual's memory
- *   k % 8 == 0 (else FG8_EUNSUPPORTED), any n >= 1, 0 <= m < 2^31.
+ *   k % 8 == 0 (else FG8_EUNSUPPORTED), any n >= 1, m >= 0.
  *   workspace: fg8_gemm_bf16_workspace_bytes(m, n, k) bytes (NULL allowed when
  *   that is 0), under gemm_fp8_blockscaled's rules: zero-filled before its
  *   first use, not shared by calls that can overlap; one workspace serves both.
@@ -427,7 +428,8 @@ size_t fg8_gemm_bf16_workspace_bytes(int64_t m, int64_t n, int64_t k);
  *   dx bf16 [m][k], dw [n][k] float or bf16, dbias float [n]: each may be NULL
  *   and is then not computed (w is needed for dx, x for dw).
  *   dz is rounded to BF16 for the two products (the matrix units' operand
- *   type); dbias sums it before that rounding.  relu' (0) = 0.
+ *   type); dbias sums it before that rounding.  relu' (0) = 0, and where z <= 0 an
+ *   infinite dy does not pass either.
  *   k % 8 == 0 (else FG8_EUNSUPPORTED), any n, m >= 1.
  *   workspace: fg8_gemm_bf16_backward_workspace_bytes(m, n, k) bytes, under
  *   gemm_bf16_epilogue's rules (it holds dz and partial sums besides).

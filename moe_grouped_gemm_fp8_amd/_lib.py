@@ -439,14 +439,21 @@ def _stream_of(t):
 
 
 def _workspace_of(nbytes, t, stream):
-    """_workspace for a stream given as a number."""
+    """_workspace for a stream given as a number, as (tensor, pointer, bytes).
+    A call recorded in a graph gets one of its own, with its arrival counters
+    cleared by the graph: the cached one may be replaced while the graph
+    lives."""
     if nbytes == 0:
-        return None, 0
+        return None, None, 0
+    if torch.cuda.is_current_stream_capturing():
+        ws = t.new_empty(nbytes, dtype=torch.uint8)
+        ws[:4096].zero_()
+        return ws, ws.data_ptr(), nbytes
     key = (t.device, stream)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = _ws_cache[key] = torch.zeros(nbytes, dtype=torch.uint8, device=t.device)
-    return ws.data_ptr(), ws.numel()
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def _rows(t, dtype, name):
@@ -580,7 +587,7 @@ def gemm_bf16_epilogue(x, w, bias=None, residual=None, activation="none", save_z
     L = lib()
     stream = _stream_of(x)
     if workspace is None:
-        ws, ws_bytes = _workspace_of(L.fg8_gemm_bf16_workspace_bytes(m, n, k), x, stream)
+        workspace, ws, ws_bytes = _workspace_of(L.fg8_gemm_bf16_workspace_bytes(m, n, k), x, stream)
     else:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(L.gemm_bf16_epilogue(x.data_ptr(), ldx, w.data_ptr(), bias_ptr, bias_bf16, act, res_ptr,
@@ -611,10 +618,12 @@ def gemm_bf16_epilogue_backward(dy, x, w, z=None, activation="none", dw_dtype=to
     dx = x.new_empty((m, k)) if needs[0] else None
     dw = x.new_empty((n, k), dtype=dw_dtype) if needs[1] else None
     db = x.new_empty(n, dtype=torch.float32) if needs[2] else None
+    if m == 0:     # sums over no rows
+        return dx, dw if dw is None else dw.zero_(), db if db is None else db.zero_()
     L = lib()
     stream = _stream_of(x)
     if workspace is None:
-        ws, ws_bytes = _workspace_of(L.fg8_gemm_bf16_backward_workspace_bytes(m, n, k), x, stream)
+        workspace, ws, ws_bytes = _workspace_of(L.fg8_gemm_bf16_backward_workspace_bytes(m, n, k), x, stream)
     else:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(L.gemm_bf16_epilogue_backward(

@@ -496,6 +496,7 @@ fg8_status moe_contiguous_layout_fp8(const void* x, int32_t x_is_bf16, int64_t t
 namespace {
 
 constexpr int64_t kMaxLd = (int64_t)1 << 22;   // 256 rows of a tile in 31-bit byte offsets
+constexpr int64_t kMaxRows = kMaxDim - 1024;   // rows rounded up to a tile still fit int32
 
 #define FG8_CHECK_LD(ld, least, of)                                                              \
   do {                                                                                           \
@@ -524,6 +525,7 @@ fg8_status check_nk(const char* fn, int64_t n, bool n8, int64_t k) {
 
 fg8_status check_runs(const char* fn, int64_t rows, int32_t num_experts) {
   if (rows < 0 || rows >= kMaxDim) return fail(FG8_EINVAL, "%s: rows=%lld", fn, (long long)rows);
+  if (rows > kMaxRows) return fail(FG8_EUNSUPPORTED, "%s: rows=%lld exceeds %lld", fn, (long long)rows, (long long)kMaxRows);
   if (num_experts < 1 || num_experts > 1024)
     return fail(FG8_EINVAL, "%s: num_experts=%d must be in [1, 1024]", fn, (int)num_experts);
   return FG8_OK;
@@ -673,6 +675,7 @@ fg8_status gemm_bf16_epilogue(const uint16_t* x, int64_t ldx, const uint16_t* w,
                               void* workspace, size_t workspace_bytes, hipStream_t stream) {
   const char* fn = "gemm_bf16_epilogue";
   if (m < 0 || m >= kMaxDim) return fail(FG8_EINVAL, "%s: m=%lld", fn, (long long)m);
+  if (m > kMaxRows) return fail(FG8_EUNSUPPORTED, "%s: m=%lld exceeds %lld", fn, (long long)m, (long long)kMaxRows);
   if (fg8_status s = check_nk(fn, n, false, k)) return s;
   if (fg8_status s = check_out(fn, out)) return s;
   if ((int)activation < FG8_ACT_NONE || (int)activation > FG8_ACT_GELU)
@@ -715,6 +718,7 @@ fg8_status gemm_bf16_epilogue_backward(const uint16_t* dy, int64_t lddy, const u
                                        hipStream_t stream) {
   const char* fn = "gemm_bf16_epilogue_backward";
   if (m < 1 || m >= kMaxDim) return fail(FG8_EINVAL, "%s: m=%lld", fn, (long long)m);
+  if (m > kMaxRows) return fail(FG8_EUNSUPPORTED, "%s: m=%lld exceeds %lld", fn, (long long)m, (long long)kMaxRows);
   if (fg8_status s = check_nk(fn, n, false, k)) return s;
   if (fg8_status s = check_out(fn, dw_out)) return s;
   if ((int)activation < FG8_ACT_NONE || (int)activation > FG8_ACT_GELU)

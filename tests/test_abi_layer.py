@@ -61,6 +61,17 @@ def test_dense(L):
     assert back(k=60) == EUNSUPPORTED
 
 
+def test_row_limit(L):
+    # rows rounded up to a tile have to fit 32 bits
+    most = (1 << 31) - 1024
+    for rows, status in ((most + 1, EUNSUPPORTED), ((1 << 31) - 1, EUNSUPPORTED)):
+        assert L.grouped_gemm_bf16(ok, 64, ok, ok, ok, 64, 1, rows, 64, 64, 4, None) == status
+        assert L.grouped_gemm_bf16_dgrad(ok, 64, ok, ok, ok, 64, 1, rows, 64, 64, 4, None) == status
+        assert L.grouped_gemm_bf16_wgrad(ok, 64, ok, 64, ok, ok, 1, rows, 64, 64, 4, None) == status
+        assert L.gemm_bf16_epilogue(ok, 64, ok, None, 0, 0, None, 64, None, ok, 64, 1, rows, 64, 64, None, 0, None) == status
+        assert L.gemm_bf16_epilogue_backward(ok, 64, ok, 64, ok, ok, 3, ok, ok, 1, ok, rows, 64, 64, ok, 1 << 40, None) == status
+
+
 def test_workspace_sizes(L):
     # counters and whole FP32 tiles; none where one workgroup a tile fills the device
     assert L.fg8_gemm_bf16_workspace_bytes(8192, 8192, 8192) == 0

@@ -317,6 +317,56 @@ def test_dense_in_a_graph(dev):
         assert torch.equal(out, want), f"replay {i}"
 
 
+def test_dense_backward_of_no_rows(dev):
+    x, w, dy = (torch.zeros(0, 64, dtype=BF16, device=dev), torch.ones(40, 64, dtype=BF16, device=dev),
+                torch.zeros(0, 40, dtype=BF16, device=dev))
+    dx, dw, db = _fg8().gemm_bf16_epilogue_backward(dy, x, w, z=dy, activation="relu")
+    assert dx.shape == (0, 64) and not dw.any() and dw.shape == (40, 64) and not db.any() and db.shape == (40,)
+
+
+def test_dense_backward_relu_stops_infinities(dev):
+    """Where z <= 0 nothing passes, whatever dy holds."""
+    z = torch.tensor([[-1.0, 0.0, 2.0, -0.0, 3.0]] * 3, dtype=BF16)
+    dy = torch.tensor([[float("inf"), float("nan"), 1.0, float("-inf"), -4.0]] * 3, dtype=BF16)
+    w = torch.eye(5, 8, dtype=BF16)
+    dx, dw, db = _fg8().gemm_bf16_epilogue_backward(dy.to(dev), torch.ones(3, 8, dtype=BF16, device=dev), w.to(dev),
+                                                    z=z.to(dev), activation="relu")
+    want = np.array([0.0, 0.0, 1.0, 0.0, -4.0])
+    assert (_np(dx)[:, :5] == want).all() and (_np(dx)[:, 5:] == 0).all()
+    assert (_np(db) == 3 * want).all() and (_np(dw) == 3 * want[:, None]).all()
+
+
+def test_dense_in_a_graph_with_its_own_workspace(dev):
+    """A graph that leaves the workspace to the library stays right when a
+    later call of the same stream needs a larger one, and the pass behind it
+    (dz and both products) too."""
+    fg8 = _fg8()
+    g = _gen(14)
+    x, w, dy = _bf16(g, 48, 2048).to(dev), _bf16(g, 200, 2048).to(dev), _bf16(g, 48, 200).to(dev)
+    assert fg8._lib.lib().fg8_gemm_bf16_workspace_bytes(48, 200, 2048) > 0
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        fg8.gemm_bf16_epilogue(x, w, activation="silu", save_z=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        y, z = fg8.gemm_bf16_epilogue(x, w, activation="silu", save_z=True)
+        grads = fg8.gemm_bf16_epilogue_backward(dy, x, w, z=z, activation="silu")
+    for i in range(4):
+        x.copy_(_bf16(g, 48, 2048).to(dev))
+        want, want_z = fg8.gemm_bf16_epilogue(x, w, activation="silu", save_z=True)
+        want_grads = fg8.gemm_bf16_epilogue_backward(dy, x, w, z=want_z, activation="silu")
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            big = [_bf16(g, 64, 4096 * (i + 1)).to(dev) for _ in range(2)]
+            fg8.gemm_bf16_epilogue(*big)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(z, want_z), f"replay {i}"
+        assert all(torch.equal(a, b) for a, b in zip(grads, want_grads)), f"replay {i}"
+
+
 # ------------------------------------------------- every tile, at its sizes
 def _check_on_gpu(got, want, s, k, what):
     err = _sum_error(k, s)
