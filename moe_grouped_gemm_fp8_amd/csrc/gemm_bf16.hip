@@ -29,9 +29,9 @@
 // as the first operand, so a lane holds four consecutive columns n of one row.
 //
 // What bounds them (one MI355X; a library product of 8192^3 in BF16 runs at
-// 1570-1620 TFLOP/s there, 1.4 to 1.6 GHz under that load):
+// 1480-1620 TFLOP/s there, 1.4 to 1.6 GHz under that load):
 //   compute: 8192^3 0.72-0.75 ms, 1470-1530 TFLOP/s, with B k-major 0.75-0.78,
-//     with both 0.78-0.80 (the library 0.79 and 0.91); MFMA busy 73% on ragged
+//     with both 0.78-0.80 (the library 0.79-0.80 and 0.91-0.93); MFMA busy 73% on ragged
 //     runs of 1563 rows, K = 7168.  Short runs and few tiles lose to tiles that
 //     a run ends in and to the last round of the CUs.
 //   stores: the weight gradient of short runs, whose FP32 tiles take as long as
@@ -505,8 +505,9 @@ __device__ __forceinline__ void store_f32_rows(uint8_t* turn, v4f a, v4f b, floa
 }
 // Sixteen rows x 64 columns staged as FP32 (4 KB), the residual's piece (res)
 // added on the way out.
-__device__ __forceinline__ void store_rows_plus(uint8_t* turn, const v4f (&v)[4], const uint4 (&res)[2], void* to, int64_t ld, bool bf16, int rows, int n, int N, int lane,
-                                                bool full) {
+__device__ __forceinline__ void store_rows_plus(uint8_t* turn, const v4f (&v)[4], const uint4 (&res)[2],
+                                                void* to, int64_t ld, bool bf16, int rows, int n, int N,
+                                                int lane, bool full) {
   const int i = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int t = 0; t < 4; ++t) *reinterpret_cast<v4f*>(turn + i * 256 + (((4 * t + g) ^ i) << 4)) = v[t];
@@ -905,14 +906,13 @@ __device__ __forceinline__ void phase_barrier() {
 // The grid is one workgroup a CU, each walking the units; a unit's first
 // copies are issued before the last unit's epilogue, which they run under.
 //
-// What a unit costs beside its steps (1.45-1.6 us each with both waves' parts):
-// finding the next one and its first copies 1.3 us, the epilogue 2-5 us, a
-// slower first step.  The weight gradient of 32 runs, 16383 rows, 7168 x 2048,
-// takes 0.72 ms, 0.43 without its 1.88 GB of stores, which alone take 0.31:
-// the two add up whatever the order of the tiles (experts mixed over the XCDs
-// or within one, starts staggered by up to 16 us, and two workgroups a CU
-// measured the same or slower): loads of the next unit queue behind the stores
-// in a CU's one memory path.
+// What a unit costs beside its steps (1.4-1.6 us each at full load): finding
+// the next one and its first copies 1.3 us, and an epilogue of 4 to 9 us where
+// every CU stores FP32 tiles.  The weight gradient of 32 runs, 16383 rows,
+// 7168 x 2048, takes 0.72 ms, 0.43 without its 1.88 GB of stores, which alone
+// take 0.31: the two add up whatever the order of the tiles (experts mixed over
+// the XCDs, other numbers of tiles together on one, staggered starts and two
+// workgroups a CU measured within 2% or slower).
 template <bool AK, bool BK, int MODE, bool EPI>
 __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
   typedef HalfTile<AK, 64> HalfA;
