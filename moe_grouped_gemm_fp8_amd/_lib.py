@@ -658,9 +658,9 @@ def layer_norm(x, weight, bias=None, eps=1e-5):
     b, b_bf16 = _param(bias, cols, "bias")
     if b is not None and b_bf16 != w_bf16:
         raise TypeError("weight and bias must have one type")
-    y = x.new_empty(x.shape)
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
     mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
-    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    rstd = torch.empty_like(mean)
     _check(lib().layer_norm(x.data_ptr(), ldx, int(dtype == torch.bfloat16), w, b, w_bf16, eps, rows,
                             cols, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _stream_of(x)))
     return y, mean, rstd
@@ -678,9 +678,9 @@ def layer_norm_backward(dy, x, weight, mean, rstd):
     _dev(rstd, torch.float32, "rstd")
     if dy.shape != x.shape or mean.shape != x.shape[:-1] or rstd.shape != x.shape[:-1]:
         raise ValueError("operand shapes disagree")
-    dx = x.new_empty(x.shape)
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     dw = x.new_empty(cols, dtype=torch.float32)
-    db = x.new_empty(cols, dtype=torch.float32)
+    db = torch.empty_like(dw)
     L = lib()
     bf16 = int(dtype == torch.bfloat16)
     need = L.fg8_layer_norm_backward_workspace_bytes(rows, cols, bf16)

@@ -181,19 +181,16 @@ struct BfUnit {
 
 __device__ __forceinline__ int clamp_off(int v, int most) { return min(max(v, 0), most); }
 
-// The `row tile` of index u over the runs of `groups` experts: tiles of a run
-// are its rows in pieces of BM; the rows before the first run and after the
-// last one are two more runs (g = -1), whose output is zeros.  Every wave
-// scans the offsets by itself, 64 at a time.  Returns the number of row tiles;
-// looks u up where u >= 0.
+// The row tiles of the runs of `groups` experts: tiles of a run are its rows in
+// pieces of BM; the rows before the first run and after the last one are two
+// more runs (g = -1), whose output is zeros.  A wave looks at 64 runs at a
+// time, one a lane; `incl` counts the tiles of the 64 up to and with this one.
 template <int BM>
-__device__ __forceinline__ int find_rows(const int32_t* off, int groups, int rows, int u, int lane,
-                                         int& g, int& m0, int& end) {
-  int base = 0;
-  g = -2;
-  for (int c = 0; c < groups + 2; c += 64) {
+struct Runs {
+  int a, b, tiles, incl;
+  __device__ Runs(const int32_t* off, int groups, int rows, int c, int lane) {
     const int e = c + lane;
-    int a = 0, b = 0;
+    a = b = 0;
     if (e < groups) {
       a = clamp_off(off[e], rows);
       b = clamp_off(off[e + 1], rows);
@@ -203,26 +200,24 @@ __device__ __forceinline__ int find_rows(const int32_t* off, int groups, int row
     } else if (e == groups + 1) {
       b = clamp_off(off[0], rows);
     }
-    const int t = b > a ? (b - a + BM - 1) / BM : 0;
-    int incl = t;
+    tiles = b > a ? (b - a + BM - 1) / BM : 0;
+    incl = tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int v = __shfl_up(incl, o, 64);
       if (lane >= o) incl += v;
     }
-    const uint64_t hit = __ballot(base + incl > u);
-    if (g == -2 && u >= 0 && hit) {
-      const int l = __builtin_ctzll(hit);
-      const int first = base + __builtin_amdgcn_readlane(incl - t, l);
-      const int start = __builtin_amdgcn_readlane(a, l);
-      g = c + l < groups ? c + l : -1;
-      m0 = start + (u - first) * BM;
-      end = __builtin_amdgcn_readlane(b, l);
-    }
-    base += __builtin_amdgcn_readlane(incl, 63);
   }
-  return base;
-}
+  __device__ int all() const { return __builtin_amdgcn_readlane(incl, 63); }
+  // looks row tile u of these 64 runs up (u < all()); c: the first run
+  __device__ void find(int u, int c, int groups, int& g, int& m0, int& end) const {
+    const int l = __builtin_ctzll(__ballot(incl > u));
+    const int first = __builtin_amdgcn_readlane(incl - tiles, l);
+    g = c + l < groups ? c + l : -1;
+    m0 = __builtin_amdgcn_readlane(a, l) + (u - first) * BM;
+    end = __builtin_amdgcn_readlane(b, l);
+  }
+};
 
 // The same for a persistent workgroup that looks up many units: the runs'
 // tile counts as a running sum in LDS, with each run's start and end.
@@ -236,29 +231,13 @@ template <int BM, class Table>
 __device__ __forceinline__ void fill_runs(Table& t, const int32_t* off, int groups, int rows, int lane) {
   int base = 0;
   for (int c = 0; c < groups + 2; c += 64) {
-    const int e = c + lane;
-    int a = 0, b = 0;
-    if (e < groups) {
-      a = clamp_off(off[e], rows);
-      b = clamp_off(off[e + 1], rows);
-    } else if (e == groups) {
-      a = clamp_off(off[groups], rows);
-      b = rows;
-    } else if (e == groups + 1) {
-      b = clamp_off(off[0], rows);
+    const Runs<BM> r(off, groups, rows, c, lane);
+    if (c + lane < groups + 2) {
+      t.sum[c + lane] = base + r.incl;
+      t.start[c + lane] = r.a;
+      t.end[c + lane] = r.b;
     }
-    int incl = b > a ? (b - a + BM - 1) / BM : 0;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += v;
-    }
-    if (e < groups + 2) {
-      t.sum[e] = base + incl;
-      t.start[e] = a;
-      t.end[e] = b;
-    }
-    base += __builtin_amdgcn_readlane(incl, 63);
+    base += r.all();
   }
 }
 template <int BM, class Table>
@@ -300,13 +279,27 @@ __device__ __forceinline__ bool find_unit(const BfProblem& p, int lane, BfUnit& 
   const int nt = (p.N + BN - 1) / BN;
   w = BfUnit{};
   if constexpr (MODE == kBfRowRuns) {
-    int g, m0, end;
-    const int mt = find_rows<BM>(p.offsets, p.groups, p.M, -1, lane, g, m0, end);
+    // (every wave for itself; up to 62 experts are one look at the offsets)
+    const Runs<BM> head(p.offsets, p.groups, p.M, 0, lane);
+    int mt = head.all();
+    for (int c = 64; c < p.groups + 2; c += 64) mt += Runs<BM>(p.offsets, p.groups, p.M, c, lane).all();
     if ((int)blockIdx.x >= mt * nt) return false;
     const int id = xcd_round(blockIdx.x, mt * nt, kCus);
-    int m, n;
+    int m, n, g, m0, end;
     raster(id, mt, nt, m, n);
-    find_rows<BM>(p.offsets, p.groups, p.M, m, lane, g, m0, end);
+    if (m < head.all()) {
+      head.find(m, 0, p.groups, g, m0, end);
+    } else {
+      int before = head.all();
+      for (int c = 64;; c += 64) {     // (m < mt, so one of the pieces holds it)
+        const Runs<BM> r(p.offsets, p.groups, p.M, c, lane);
+        if (m < before + r.all()) {
+          r.find(m - before, c, p.groups, g, m0, end);
+          break;
+        }
+        before += r.all();
+      }
+    }
     w.g = uniform(g);
     w.m0 = uniform(m0);
     w.n0 = uniform(n) * BN;
