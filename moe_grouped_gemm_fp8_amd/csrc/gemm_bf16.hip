@@ -201,12 +201,19 @@ struct Runs {
       b = clamp_off(off[0], rows);
     }
     tiles = b > a ? (b - a + BM - 1) / BM : 0;
-    incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += v;
-    }
+    incl = scan(tiles);
+  }
+  // Running sum over the lanes: within rows of sixteen (row_shr by 1, 2, 4, 8),
+  // then each row's last lane into the row after it (rows 1 and 3, then the
+  // upper two).  Register moves, where shuffles go through LDS.
+  __device__ static int scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+    return v;
   }
   __device__ int all() const { return __builtin_amdgcn_readlane(incl, 63); }
   // looks row tile u of these 64 runs up (u < all()); c: the first run
