@@ -285,9 +285,15 @@ def main(argv=None):
         x = cp[r % len(cp)]
         return lambda: fg8.fp8_quantize(x["A"], "1x128", q=x["qa"], scales=x["sa"])
 
+    # one split-K workspace for the stream all of this runs on, its counters
+    # cleared once: a graph that leaves it to the library clears one per call
+    ws = torch.zeros(max(fg8.gemm_workspace_bytes(c.M, c.N, c.K) for c in shapes) or 1,
+                     dtype=torch.uint8, device=dev)
+
     def gemm_fn(cp, r):
         x = cp[r % len(cp)]
-        return lambda: fg8.gemm_fp8_blockscaled(x["qa"], x["sa"], x["qb"], x["sb"], out=x["d"])
+        return lambda: fg8.gemm_fp8_blockscaled(x["qa"], x["sa"], x["qb"], x["sb"], out=x["d"],
+                                                workspace=ws)
 
     def step_fn(r):
         parts = [f(cp, r) for _, cp in sets for f in (quant_fn, gemm_fn)]

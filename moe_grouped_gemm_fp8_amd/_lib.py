@@ -200,21 +200,36 @@ def gemm_workspace_bytes(m, n, k) -> int:
 _ws_cache = {}
 
 
-def _workspace(nbytes, device):
-    """A zero-initialised workspace per (device, stream); the kernels leave its
-    counters at zero, so it is reused as is."""
+def _stream_of(t):
+    """The current stream of t's device, as a number."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _workspace_of(nbytes, t, stream):
+    """A zero-initialised workspace per (t's device, stream), as (tensor,
+    pointer, bytes); the kernels leave its counters at zero, so it is reused as
+    is.  A call recorded in a graph gets one of its own, with its arrival
+    counters cleared by the graph, and leaves nothing here: a cached one may be
+    replaced while the graph lives, and one that a graph allocated belongs to
+    the graph, whose clearing has only been recorded."""
     if nbytes == 0:
-        return None
-    key = (device, torch.cuda.current_stream(device).cuda_stream)
+        return None, None, 0
+    if torch.cuda.is_current_stream_capturing():
+        ws = t.new_empty(nbytes, dtype=torch.uint8)
+        ws[:4096].zero_()
+        return ws, ws.data_ptr(), nbytes
+    key = (t.device, stream)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
-    return ws
+        ws = _ws_cache[key] = torch.zeros(nbytes, dtype=torch.uint8, device=t.device)
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def gemm_fp8_blockscaled(a, sa, b, sb, out_dtype=torch.bfloat16, out=None, workspace=None):
-    """D [m, n] = A B^T with a [m, k] e4m3, sa [k/128, m], b [n, k], sb [ceil(n/128), k/128]."""
+    """D [m, n] = A B^T with a [m, k] e4m3, sa [k/128, m], b [n, k], sb [ceil(n/128), k/128].
+    Recorded in a graph without a workspace, a split product clears the counters
+    of one of its own on every replay; a zero-filled `workspace` (see
+    gemm_workspace_bytes) that the caller keeps for the graph saves that."""
     _fp8(a, "a"); _fp8(b, "b")
     _dev(sa, torch.float32, "sa"); _dev(sb, torch.float32, "sb")
     m, k = a.shape
@@ -224,12 +239,13 @@ def gemm_fp8_blockscaled(a, sa, b, sb, out_dtype=torch.bfloat16, out=None, works
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype, device=a.device)
     _dev(out, out.dtype, "out")
-    need = gemm_workspace_bytes(m, n, k)
-    ws = workspace if workspace is not None else _workspace(need, a.device)
+    stream = _stream_of(a)
+    if workspace is None:
+        workspace, ws, ws_bytes = _workspace_of(gemm_workspace_bytes(m, n, k), a, stream)
+    else:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(lib().gemm_fp8_blockscaled(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(out),
-                                      _out_code(out.dtype), m, n, k, _ptr(ws),
-                                      0 if ws is None else ws.numel() * ws.element_size(),
-                                      _stream()))
+                                      _out_code(out.dtype), m, n, k, ws, ws_bytes, stream))
     return out
 
 
@@ -433,29 +449,6 @@ def moe_contiguous_layout_fp8(x, topk_ids, num_experts, m_cap=None, out=None):
 # These calls are made many times a layer and some run for a few microseconds,
 # so their host side is kept short: the stream as a plain number, outputs from
 # an operand's new_empty.
-def _stream_of(t):
-    """The current stream of t's device, as a number."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
-
-
-def _workspace_of(nbytes, t, stream):
-    """_workspace for a stream given as a number, as (tensor, pointer, bytes).
-    A call recorded in a graph gets one of its own, with its arrival counters
-    cleared by the graph: the cached one may be replaced while the graph
-    lives."""
-    if nbytes == 0:
-        return None, None, 0
-    if torch.cuda.is_current_stream_capturing():
-        ws = t.new_empty(nbytes, dtype=torch.uint8)
-        ws[:4096].zero_()
-        return ws, ws.data_ptr(), nbytes
-    key = (t.device, stream)
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = _ws_cache[key] = torch.zeros(nbytes, dtype=torch.uint8, device=t.device)
-    return ws, ws.data_ptr(), ws.numel()
-
-
 def _rows(t, dtype, name):
     """Row stride of a 2-D tensor whose rows are contiguous but may be part of
     wider ones."""
