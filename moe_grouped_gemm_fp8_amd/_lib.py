@@ -197,6 +197,14 @@ def gemm_workspace_bytes(m, n, k) -> int:
     return int(lib().fg8_gemm_workspace_bytes(m, n, k))
 
 
+#: The arrival counters at a workspace's front (kSplitKCounterBytes of the
+#: kernels): all of it that has to be zero before its first use.
+WS_COUNTER_BYTES = 4096
+#: The largest workspace that is kept.  Counters and partial tiles of a split
+#: product take 34 MB at most (two 128 x 128 FP32 tiles a CU); what goes beyond
+#: is a backward pass's dz, which grows with the call and is its alone.
+WS_KEEP_BYTES = 64 << 20
+
 _ws_cache = {}
 
 
@@ -205,23 +213,31 @@ def _stream_of(t):
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _new_workspace(nbytes, t):
+    ws = t.new_empty(nbytes, dtype=torch.uint8)
+    ws[:WS_COUNTER_BYTES].zero_()
+    return ws
+
+
 def _workspace_of(nbytes, t, stream):
-    """A zero-initialised workspace per (t's device, stream), as (tensor,
-    pointer, bytes); the kernels leave its counters at zero, so it is reused as
-    is.  A call recorded in a graph gets one of its own, with its arrival
-    counters cleared by the graph, and leaves nothing here: a cached one may be
-    replaced while the graph lives, and one that a graph allocated belongs to
-    the graph, whose clearing has only been recorded."""
+    """A workspace per (t's device, stream) with its counters at zero, as
+    (tensor, pointer, bytes); the kernels leave them so, and it is reused as
+    is.  One above WS_KEEP_BYTES goes back with the call.  A call recorded in a
+    graph gets one of its own, with its arrival counters cleared by the graph,
+    and leaves nothing here: a cached one may be replaced while the graph
+    lives, and one that a graph allocated belongs to the graph, whose clearing
+    has only been recorded."""
     if nbytes == 0:
         return None, None, 0
-    if torch.cuda.is_current_stream_capturing():
-        ws = t.new_empty(nbytes, dtype=torch.uint8)
-        ws[:4096].zero_()
-        return ws, ws.data_ptr(), nbytes
-    key = (t.device, stream)
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = _ws_cache[key] = torch.zeros(nbytes, dtype=torch.uint8, device=t.device)
+    if nbytes > WS_KEEP_BYTES or torch.cuda.is_current_stream_capturing():
+        ws = _new_workspace(nbytes, t)
+    else:
+        key = (t.device, stream)
+        ws = _ws_cache.get(key)
+        if ws is None or ws.numel() < nbytes:
+            ws = None
+            _ws_cache.pop(key, None)     # (its memory serves the larger one)
+            ws = _ws_cache[key] = _new_workspace(nbytes, t)
     return ws, ws.data_ptr(), ws.numel()
 
 

@@ -78,3 +78,52 @@ def test_a_recorded_call_does_not_take_the_cached_workspace(on_host, name):
     CALLS[name]()
     eager, first, _, again = [p for p, _ in library.given]
     assert eager == again and first != eager
+
+
+# ------------------------------------------------------------- what is kept
+class Operand:
+    """Allocates like a tensor and notes what the cache held meanwhile."""
+
+    def __init__(self):
+        self.device, self.held = torch.device("cpu"), []
+
+    def new_empty(self, nbytes, dtype):
+        self.held.append(sum(w.numel() for w in _lib._ws_cache.values()))
+        return torch.full((nbytes,), 7, dtype=dtype)
+
+
+def test_a_large_workspace_is_not_kept(on_host):
+    """16384 x 16384: dz alone is half a gigabyte."""
+    t, most = Operand(), _lib.WS_KEEP_BYTES
+    small = _lib._workspace_of(1 << 20, t, 7)[0]
+    big, ptr, size = _lib._workspace_of(most + 16, t, 7)
+    assert size == most + 16 and ptr == big.data_ptr() and not big[:_lib.WS_COUNTER_BYTES].any()
+    assert _lib._workspace_of(1 << 20, t, 7)[0] is small
+    assert sum(w.numel() for w in _lib._ws_cache.values()) == 1 << 20
+
+
+def test_a_growing_workspace_clears_its_counters_and_frees_the_old_one(on_host):
+    t = Operand()
+    first = _lib._workspace_of(1 << 16, t, 7)[0]
+    assert not first[:_lib.WS_COUNTER_BYTES].any()
+    del first
+    second = _lib._workspace_of(1 << 18, t, 7)[0]
+    assert t.held == [0, 0], "the old buffer was held while the new one was allocated"
+    assert not second[:_lib.WS_COUNTER_BYTES].any() and bool((second[_lib.WS_COUNTER_BYTES:] == 7).all())
+
+
+def test_the_counters_are_the_kernels():
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "moe_grouped_gemm_fp8_amd", "csrc", "fg8_internal.h")).read()
+    tiles = int(re.search(r"kSplitKMaxTiles = (\d+);", text).group(1))
+    assert "kSplitKCounterBytes = kSplitKMaxTiles * sizeof(int32_t);" in text
+    assert _lib.WS_COUNTER_BYTES == 4 * tiles
+    # the kept size holds every split product of the device
+    L = _lib.lib()
+    most = 0
+    for m in (1, 16, 33, 64, 128, 200, 256, 300, 384, 512, 700, 1024):
+        for n in (64, 512, 1024, 2112, 4096, 7168):
+            most = max(most, L.fg8_gemm_bf16_workspace_bytes(m, n, 8192), L.fg8_gemm_workspace_bytes(m, n, 8192))
+    assert most <= _lib.WS_KEEP_BYTES
