@@ -241,6 +241,12 @@ def _workspace_of(nbytes, t, stream):
     return ws, ws.data_ptr(), ws.numel()
 
 
+def _workspace_given(ws):
+    """A caller's workspace as (pointer, bytes)."""
+    _dev(ws, ws.dtype, "workspace")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def gemm_fp8_blockscaled(a, sa, b, sb, out_dtype=torch.bfloat16, out=None, workspace=None):
     """D [m, n] = A B^T with a [m, k] e4m3, sa [k/128, m], b [n, k], sb [ceil(n/128), k/128].
     Recorded in a graph without a workspace, a split product clears the counters
@@ -259,7 +265,7 @@ def gemm_fp8_blockscaled(a, sa, b, sb, out_dtype=torch.bfloat16, out=None, works
     if workspace is None:
         workspace, ws, ws_bytes = _workspace_of(gemm_workspace_bytes(m, n, k), a, stream)
     else:
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, ws_bytes = _workspace_given(workspace)
     _check(lib().gemm_fp8_blockscaled(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(out),
                                       _out_code(out.dtype), m, n, k, ws, ws_bytes, stream))
     return out
@@ -598,7 +604,7 @@ def gemm_bf16_epilogue(x, w, bias=None, residual=None, activation="none", save_z
     if workspace is None:
         workspace, ws, ws_bytes = _workspace_of(L.fg8_gemm_bf16_workspace_bytes(m, n, k), x, stream)
     else:
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, ws_bytes = _workspace_given(workspace)
     _check(L.gemm_bf16_epilogue(x.data_ptr(), ldx, w.data_ptr(), bias_ptr, bias_bf16, act, res_ptr,
                                 ldr, z.data_ptr() if save_z else None, out.data_ptr(), ldy, code, m,
                                 n, k, ws, ws_bytes, stream))
@@ -634,7 +640,7 @@ def gemm_bf16_epilogue_backward(dy, x, w, z=None, activation="none", dw_dtype=to
     if workspace is None:
         workspace, ws, ws_bytes = _workspace_of(L.fg8_gemm_bf16_backward_workspace_bytes(m, n, k), x, stream)
     else:
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, ws_bytes = _workspace_given(workspace)
     _check(L.gemm_bf16_epilogue_backward(
         dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), _ptr(z), act, _ptr(dx), _ptr(dw),
         _out_code(dw_dtype), _ptr(db), m, n, k, ws, ws_bytes, stream))
