@@ -123,9 +123,18 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _dev(t, dtype, name):
+def _here(t, name):
+    """The library launches on the current device and goes by its size: every
+    operand has to lie there."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
+                         f"cuda:{torch._C._cuda_getDevice()}")
+
+
+def _dev(t, dtype, name):
+    _here(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
@@ -474,8 +483,7 @@ def moe_contiguous_layout_fp8(x, topk_ids, num_experts, m_cap=None, out=None):
 def _rows(t, dtype, name):
     """Row stride of a 2-D tensor whose rows are contiguous but may be part of
     wider ones."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    _here(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 2:
