@@ -345,8 +345,9 @@ int64_t fg8_moe_capacity(int64_t tokens, int32_t topk, int32_t num_experts);
  * bit patterns.  ld arguments count elements between rows and let a row be
  * part of a wider one; pointers are 16-byte aligned as everywhere, and ld of
  * an operand that a product reads is a multiple of 8 and at most 2^22 (a
- * larger one is FG8_EUNSUPPORTED); the products take 2^31 - 1024 rows at most
- * (more: FG8_EUNSUPPORTED).  All sums are FP32, rounded once where the
+ * larger one is FG8_EUNSUPPORTED); the products take 2^31 - 1024 rows at most,
+ * and no more tiles than a launch of fewer than 2^32 threads holds (more:
+ * FG8_EUNSUPPORTED).  All sums are FP32, rounded once where the
  * output is BF16.  Sums run in a fixed order: the same call gives the same
  * bits.  m, rows or tokens of 0 are valid where a call takes them: nothing is
  * read, and gradients summed over them are zeros.
@@ -481,6 +482,8 @@ size_t fg8_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols, int32
  *   residual   NULL, or [tokens][hidden] of y's type; out [tokens][hidden] of
  *              y's type
  *   hidden % 8 == 0 (else FG8_EUNSUPPORTED), rows >= 1, 1 <= topk <= 256.
+ *   One launch holds tokens * ceil(hidden / C) <= 4 (2^24 - 1), C = 512 columns
+ *   in bf16 and 256 in float (more is FG8_EUNSUPPORTED).
  */
 fg8_status moe_combine(const void* y, int32_t is_bf16, int64_t rows, const int32_t* token_row,
                        const float* weights, const void* residual, int64_t tokens, int32_t topk,
@@ -494,7 +497,8 @@ fg8_status moe_combine(const void* y, int32_t is_bf16, int64_t rows, const int32
  *              gives it: a row whose value lies outside [0, tokens) holds no
  *              token, and its dy is written as zeros
  *   dout, dy   of y's type; dy [rows][hidden]; dweights float [tokens][topk].
- *   A row belongs to one position at most.
+ *   A row belongs to one position at most.  One launch holds tokens +
+ *   ceil(rows / 4) <= 2^24 - 1 (more is FG8_EUNSUPPORTED).
  */
 fg8_status moe_combine_backward(const void* dout, const void* y, int32_t is_bf16, int64_t rows,
                                 const int32_t* token_row, const int32_t* row_token,

@@ -495,6 +495,9 @@ fg8_status moe_contiguous_layout_fp8(const void* x, int32_t x_is_bf16, int64_t t
 // BF16 products, layer norm, MoE combine.
 namespace {
 
+// HIP takes launches of fewer than 2^32 threads in all.
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;
+
 constexpr int64_t kMaxLd = (int64_t)1 << 22;   // 256 rows of a tile in 31-bit byte offsets
 constexpr int64_t kMaxRows = kMaxDim - 1024;   // rows rounded up to a tile still fit int32
 
@@ -535,8 +538,12 @@ fg8_status run_bf16(const fg8::BfProblem& p, const char* fn, hipStream_t stream)
   const fg8::BfTile t = fg8::bf16_tile(p, fg8::device_cu_count());
   const int64_t runs = p.mode == fg8::kBfKRuns ? p.groups : t.splits;
   const int64_t mt = ((int64_t)p.M + t.bm - 1) / t.bm + (p.mode == fg8::kBfRowRuns ? p.groups + 1 : 0);
-  if (mt * (((int64_t)p.N + t.bn - 1) / t.bn) * runs >= INT32_MAX - 8)
-    return fail(FG8_EUNSUPPORTED, "%s: too many tiles for a 32-bit count", fn);
+  const int64_t tiles = mt * (((int64_t)p.N + t.bn - 1) / t.bn) * runs;
+  if (tiles >= INT32_MAX - 8) return fail(FG8_EUNSUPPORTED, "%s: too many tiles for a 32-bit count", fn);
+  // (a persistent launch has a workgroup a CU; the others one a tile, rounded
+  // up to the eight XCDs)
+  if (!t.persistent && (tiles + 7) / 8 * 8 * t.threads > kMaxThreads)
+    return fail(FG8_EUNSUPPORTED, "%s: %lld tiles of %d threads exceed a launch", fn, (long long)tiles, t.threads);
   const hipError_t e = fg8::launch_bf16(p, t, stream);
   if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
   g_err[0] = 0;
@@ -854,8 +861,14 @@ fg8_status check_combine(const char* fn, int32_t is_bf16, int64_t rows, int64_t 
                 (long long)tokens, (long long)hidden);
   if (topk < 1 || topk > 256) return fail(FG8_EINVAL, "%s: topk=%d must be in [1, 256]", fn, (int)topk);
   if (hidden % 8) return fail(FG8_EUNSUPPORTED, "%s: hidden=%lld is not a multiple of 8", fn, (long long)hidden);
-  if (tokens * ((hidden + 255) / 256) >= kMaxDim || tokens + rows >= kMaxDim)
-    return fail(FG8_EUNSUPPORTED, "%s: too many tokens", fn);
+  if (tokens >= kMaxDim) return fail(FG8_EUNSUPPORTED, "%s: too many tokens", fn);
+  return FG8_OK;
+}
+
+fg8_status check_combine_launch(const char* fn, int64_t workgroups) {
+  if (workgroups > kMaxThreads / fg8::kCombineThreads)
+    return fail(FG8_EUNSUPPORTED, "%s: %lld workgroups of %d threads exceed a launch", fn, (long long)workgroups,
+                fg8::kCombineThreads);
   return FG8_OK;
 }
 
@@ -866,6 +879,7 @@ fg8_status moe_combine(const void* y, int32_t is_bf16, int64_t rows, const int32
                        int64_t hidden, void* out, hipStream_t stream) {
   const char* fn = "moe_combine";
   if (fg8_status s = check_combine(fn, is_bf16, rows, tokens, topk, hidden)) return s;
+  if (fg8_status s = check_combine_launch(fn, fg8::combine_workgroups(is_bf16 == 1, tokens, hidden))) return s;
   if (tokens == 0) return FG8_OK;
   FG8_CHECK_PTR(y);
   FG8_CHECK_PTR(token_row);
@@ -885,6 +899,7 @@ fg8_status moe_combine_backward(const void* dout, const void* y, int32_t is_bf16
                                 void* dy, float* dweights, hipStream_t stream) {
   const char* fn = "moe_combine_backward";
   if (fg8_status s = check_combine(fn, is_bf16, rows, tokens, topk, hidden)) return s;
+  if (fg8_status s = check_combine_launch(fn, fg8::combine_backward_workgroups(rows, tokens))) return s;
   if (tokens > 0) {   // (without tokens every row's gradient is zeros)
     FG8_CHECK_PTR(dout);
     FG8_CHECK_PTR(token_row);

@@ -36,7 +36,7 @@ __device__ __forceinline__ void store16(T* p, const float* f) {
 
 // A wave's item: one span of 64 pieces of one token.
 template <class T>
-__global__ __launch_bounds__(256) void combine_kernel(
+__global__ __launch_bounds__(kCombineThreads) void combine_kernel(
     const T* __restrict__ y, int64_t rows, const int32_t* __restrict__ token_row,
     const float* __restrict__ weights, const T* __restrict__ residual, int64_t tokens, int topk,
     int64_t hidden, int spans, T* __restrict__ out) {
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(256) void combine_kernel(
 // Workgroups [0, tokens): one token each, its pieces dealt to four waves; the
 // others clear the rows that hold no token, four rows each.
 template <class T>
-__global__ __launch_bounds__(256) void combine_backward_kernel(
+__global__ __launch_bounds__(kCombineThreads) void combine_backward_kernel(
     const T* __restrict__ dout, const T* __restrict__ y, int64_t rows,
     const int32_t* __restrict__ token_row, const int32_t* __restrict__ row_token,
     const float* __restrict__ weights, int64_t tokens, int topk, int64_t hidden,
@@ -164,20 +164,29 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
   }
 }
 
+int combine_spans(bool bf16, int64_t hidden) {
+  const int64_t span = 64 * (bf16 ? 8 : 4);
+  return (int)((hidden + span - 1) / span);
+}
+
 }  // namespace
+
+int64_t combine_workgroups(bool bf16, int64_t tokens, int64_t hidden) {
+  return (tokens * combine_spans(bf16, hidden) + 3) / 4;
+}
+int64_t combine_backward_workgroups(int64_t rows, int64_t tokens) { return tokens + (rows + 3) / 4; }
 
 hipError_t launch_combine(const void* y, bool bf16, int64_t rows, const int32_t* token_row,
                           const float* weights, const void* residual, int64_t tokens, int topk,
                           int64_t hidden, void* out, hipStream_t stream) {
-  const int64_t span = 64 * (bf16 ? 8 : 4);
-  const int spans = (int)((hidden + span - 1) / span);
-  const dim3 grid((unsigned)((tokens * spans + 3) / 4));
+  const int spans = combine_spans(bf16, hidden);
+  const dim3 grid((unsigned)combine_workgroups(bf16, tokens, hidden));
   if (bf16)
-    hipLaunchKernelGGL(combine_kernel<uint16_t>, grid, dim3(256), 0, stream, (const uint16_t*)y, rows,
+    hipLaunchKernelGGL(combine_kernel<uint16_t>, grid, dim3(kCombineThreads), 0, stream, (const uint16_t*)y, rows,
                        token_row, weights, (const uint16_t*)residual, tokens, topk, hidden, spans,
                        (uint16_t*)out);
   else
-    hipLaunchKernelGGL(combine_kernel<float>, grid, dim3(256), 0, stream, (const float*)y, rows,
+    hipLaunchKernelGGL(combine_kernel<float>, grid, dim3(kCombineThreads), 0, stream, (const float*)y, rows,
                        token_row, weights, (const float*)residual, tokens, topk, hidden, spans,
                        (float*)out);
   return hipGetLastError();
@@ -187,13 +196,13 @@ hipError_t launch_combine_backward(const void* dout, const void* y, bool bf16, i
                                    const int32_t* token_row, const int32_t* row_token,
                                    const float* weights, int64_t tokens, int topk, int64_t hidden,
                                    void* dy, float* dweights, hipStream_t stream) {
-  const dim3 grid((unsigned)(tokens + (rows + 3) / 4));
+  const dim3 grid((unsigned)combine_backward_workgroups(rows, tokens));
   if (bf16)
-    hipLaunchKernelGGL(combine_backward_kernel<uint16_t>, grid, dim3(256), 0, stream,
+    hipLaunchKernelGGL(combine_backward_kernel<uint16_t>, grid, dim3(kCombineThreads), 0, stream,
                        (const uint16_t*)dout, (const uint16_t*)y, rows, token_row, row_token, weights,
                        tokens, topk, hidden, (uint16_t*)dy, dweights);
   else
-    hipLaunchKernelGGL(combine_backward_kernel<float>, grid, dim3(256), 0, stream, (const float*)dout,
+    hipLaunchKernelGGL(combine_backward_kernel<float>, grid, dim3(kCombineThreads), 0, stream, (const float*)dout,
                        (const float*)y, rows, token_row, row_token, weights, tokens, topk, hidden,
                        (float*)dy, dweights);
   return hipGetLastError();

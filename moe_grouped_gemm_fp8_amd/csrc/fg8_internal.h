@@ -114,6 +114,8 @@ struct BfProblem {
 };
 struct BfTile {
   int cfg, bm, bn, splits;
+  int threads;        // of a workgroup
+  bool persistent;    // a workgroup a CU; otherwise one a tile and split
 };
 constexpr int kBfMaxSplits = 16;
 BfTile bf16_tile(const BfProblem& p, int num_cus);
@@ -140,6 +142,11 @@ hipError_t launch_layer_norm_backward(const void* dy, int64_t lddy, const void* 
                                       float* partial, int num_cus, hipStream_t stream);
 
 // -------------------------------------------------------------- MoE combine
+// Workgroups of the launches (fewer than 2^32 threads in all, the caller
+// checks).
+constexpr int kCombineThreads = 256;
+int64_t combine_workgroups(bool bf16, int64_t tokens, int64_t hidden);
+int64_t combine_backward_workgroups(int64_t rows, int64_t tokens);
 hipError_t launch_combine(const void* y, bool bf16, int64_t rows, const int32_t* token_row,
                           const float* weights, const void* residual, int64_t tokens, int topk,
                           int64_t hidden, void* out, hipStream_t stream);

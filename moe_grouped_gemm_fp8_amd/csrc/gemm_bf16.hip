@@ -1098,6 +1098,8 @@ using BfFlat = BfCfg<32, 64, 2, 2, 5, 2>;
 using BfThin = BfCfg<16, 64, 1, 4, 6, 2>;
 constexpr int kBm[kConfigs] = {256, 128, 128, 128, 64, 32, 16, 16};
 constexpr int kBn[kConfigs] = {256, 256, 128, 64, 64, 64, 64, 16};
+constexpr int kThreads[kConfigs] = {512, BfDuo::THREADS, BfMid::THREADS, BfHigh::THREADS,
+                                    BfLow::THREADS, BfFlat::THREADS, BfThin::THREADS, 512};
 
 namespace {
 
@@ -1178,6 +1180,8 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
   }
   t.bm = kBm[t.cfg];
   t.bn = kBn[t.cfg];
+  t.threads = kThreads[t.cfg];
+  t.persistent = t.cfg == kBig;
   t.splits = 1;
   if (p.mode == kBfDense && t.cfg != kBig && t.cfg != kFew) {
     // One workgroup a CU; two where several row tiles read the same weights
