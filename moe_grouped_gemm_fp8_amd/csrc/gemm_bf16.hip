@@ -48,6 +48,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
+constexpr int kLdsBytes = 160 * 1024;          // of a CU
 constexpr int kBK = 64;                       // k depth of one step
 constexpr uint32_t kNowhere = 0x80000000u;    // an offset past every buffer resource
 
@@ -61,7 +62,8 @@ struct BfCfg {
   static constexpr int A_BYTES = BM * DEPTH * 2, B_BYTES = BN * DEPTH * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static_assert(WM % 16 == 0 && WN % 16 == 0 && STAGES >= 2, "whole MFMA tiles, two stages");
-  static_assert(STAGES * STAGE_BYTES <= 160 * 1024, "LDS of a CU");
+  // (the stages, and bf16_kernel's flag beside them)
+  static_assert(OCC * (STAGES * STAGE_BYTES + 16) <= kLdsBytes, "OCC workgroups share the LDS of a CU");
 };
 
 // A copy of 16 bytes a lane into LDS at `lds` + 16 * lane.  The instruction
@@ -229,13 +231,12 @@ struct Runs {
 // The same for a persistent workgroup that looks up many units: the runs'
 // tile counts as a running sum in LDS, with each run's start and end.
 constexpr int kMaxRuns = 1024 + 2;
-template <int CAP>
 struct RunTable {
-  int sum[CAP], start[CAP], end[CAP];   // sum: tiles of the runs up to and with this one
+  int sum[kMaxRuns], start[kMaxRuns], end[kMaxRuns];   // sum: tiles of the runs up to and with this one
 };
 // Filled by one wave (the caller's barrier makes it visible).
-template <int BM, class Table>
-__device__ __forceinline__ void fill_runs(Table& t, const int32_t* off, int groups, int rows, int lane) {
+template <int BM>
+__device__ __forceinline__ void fill_runs(RunTable& t, const int32_t* off, int groups, int rows, int lane) {
   int base = 0;
   for (int c = 0; c < groups + 2; c += 64) {
     const Runs<BM> r(off, groups, rows, c, lane);
@@ -247,8 +248,8 @@ __device__ __forceinline__ void fill_runs(Table& t, const int32_t* off, int grou
     base += r.all();
   }
 }
-template <int BM, class Table>
-__device__ __forceinline__ void look_up_run(const Table& t, int groups, int m, int& g, int& m0, int& rows) {
+template <int BM>
+__device__ __forceinline__ void look_up_run(const RunTable& t, int groups, int m, int& g, int& m0, int& rows) {
   int lo = 0, hi = groups + 1;      // the first run whose sum exceeds m
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -918,13 +919,15 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
   typedef HalfTile<AK, 64> HalfA;
   typedef HalfTile<BK, 32> HalfB;
   constexpr uint32_t kHalf = HalfA::BYTES;         // LDS: per stage A0, A1, B0, B1
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[8 * kHalf + 8 * TileOut<EPI>::kTurn];
-  __shared__ RunTable<MODE == kBfRowRuns ? kMaxRuns : 1> runs;
+  constexpr uint32_t kTurns = 8 * kHalf, kTable = kTurns + 8 * TileOut<EPI>::kTurn;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kTable + (MODE == kBfRowRuns ? sizeof(RunTable) : 0)];
+  static_assert(sizeof(smem) <= kLdsBytes, "all the LDS of the kernel: the stages, the waves' turns, the runs");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int grp = wave >> 2, q = wave & 3;
   const int nt = (p.N + 255) / 256;
   int mt = (p.M + 255) / 256;
   if constexpr (MODE == kBfRowRuns) {
+    RunTable& runs = *reinterpret_cast<RunTable*>(smem + kTable);
     if (wave == 0) fill_runs<256>(runs, p.offsets, p.groups, p.M, lane);
     __syncthreads();
     mt = uniform(runs.sum[p.groups + 1]);
@@ -937,7 +940,7 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
     if constexpr (MODE == kBfRowRuns) {
       raster(id, mt, nt, m, n);
       int m0;
-      look_up_run<256>(runs, p.groups, m, w.g, m0, w.rows);
+      look_up_run<256>(*reinterpret_cast<const RunTable*>(smem + kTable), p.groups, m, w.g, m0, w.rows);
       w.m0 = m0;
       w.ks = w.g < 0 ? 0 : p.K;
     } else {
@@ -1051,7 +1054,7 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
     }
 
     const int here = opaque(lane);
-    TileOut<EPI> out(p, w, 256, 256, q * 64, smem + 8 * kHalf + wave * TileOut<EPI>::kTurn, here);
+    TileOut<EPI> out(p, w, 256, 256, q * 64, smem + kTurns + wave * TileOut<EPI>::kTurn, here);
     if constexpr (EPI) {       // the bias has arrived before the copies below queue up
 #pragma unroll
       for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(out.bias[i]));
