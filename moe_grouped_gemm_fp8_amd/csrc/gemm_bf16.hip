@@ -811,13 +811,14 @@ __global__ __launch_bounds__(512, 2) void bf16_few_kernel(BfProblem p) {
 template <bool KMAJOR, int RUN>
 struct HalfTile {
   static constexpr int ROWS = 128, BYTES = ROWS * kBK * 2;
+  static constexpr int COPIES = BYTES / 1024 / 8;     // a wave's
   static constexpr int PITCH = KMAJOR ? ROWS * 2 : kBK * 2;
   typedef Operand<KMAJOR, ROWS, 8> Frag;    // the layout inside a half
 
   const char* base;
   int64_t ld;
   int64_t left;
-  uint32_t off[2][2];     // [half][copy]
+  uint32_t off[2][COPIES];     // [half][copy]
   int rem_k;
 
   __device__ static int tile_row(int x, int h) { return x / RUN * (2 * RUN) + h * RUN + x % RUN; }
@@ -831,8 +832,8 @@ struct HalfTile {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at = (wave * 2 + i) * 1024 + lane * 16;
+      for (int i = 0; i < COPIES; ++i) {
+        const int at = (wave * COPIES + i) * 1024 + lane * 16;
         if constexpr (KMAJOR) {
           const int k = at / PITCH, c = tile_row(((at % PITCH / 16) ^ (Frag::gran(k) << 1)) * 8, h);
           off[h][i] = c < xs ? (uint32_t)(k * ld) + c * 2 : kNowhere;
@@ -843,7 +844,7 @@ struct HalfTile {
       }
   }
 
-  // this wave's two copies of half h of k step kt into LDS; past the last step
+  // this wave's copies of half h of k step kt into LDS; past the last step
   // they copy zeros, so the count of copies in flight stays what the waits
   // assume
   __device__ void issue(int kt, int h, uint32_t lds, int wave, int lane) const {
@@ -851,13 +852,13 @@ struct HalfTile {
     const int64_t bytes = KMAJOR ? (int64_t)(rem - 1) * ld + left : left + (int64_t)((rem + 7) & ~7) * 2;
     const v4i rs = resource(base + (int64_t)kt * (KMAJOR ? kBK * ld : kBK * 2), rem > 0 ? bytes : 0);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < COPIES; ++i) {
       uint32_t o = off[h][i];
       if constexpr (!KMAJOR) {
         const int c = (lane & 7) ^ (4 * i + (lane >> 4));     // the chunk of k, swz(row) undone
         o = c * 8 < rem ? o : kNowhere;
       }
-      copy16(rs, o, uniform(lds + (uint32_t)(wave * 2 + i) * 1024));
+      copy16(rs, o, uniform(lds + (uint32_t)(wave * COPIES + i) * 1024));
     }
   }
 };
@@ -964,7 +965,10 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
   const uint32_t lds0 = lds_addr(smem);
   auto copy_a = [&](int t, int h) { a.issue(t, h, lds0 + ((t & 1) * 4 + h) * kHalf, wave, lane); };
   auto copy_b = [&](int t, int h) { b.issue(t, h, lds0 + ((t & 1) * 4 + 2 + h) * kHalf, wave, lane); };
-  auto start = [&](const BfUnit& w) {     // the first twelve copies of a unit
+  // Copies of two halves may be in flight wherever a wave waits for its own.
+  static_assert(HalfA::COPIES == HalfB::COPIES);
+  constexpr int kTwoHalves = 2 * HalfA::COPIES;
+  auto start = [&](const BfUnit& w) {     // a unit's first five halves
     const int here = opaque(lane);
     a.init(p.a, p.lda, w.m0, w.rows, w.k0, w.ks, wave, here);
     b.init(p.b + (MODE == kBfRowRuns ? w.g * p.b_stride : 0), p.ldb, w.n0, p.N - w.n0, w.k0, w.ks, wave, here);
@@ -1024,7 +1028,7 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
       };
       constexpr std::integral_constant<int, 0> c0{};
       constexpr std::integral_constant<int, 1> c1{};
-      wait_vmcnt<4>();              // step 0 but for A1
+      wait_vmcnt<kTwoHalves>();     // step 0 but for A1 (the last of start()'s five is B0 of step 1)
       phase_barrier();
       read_b(fb[0], 0, 0);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -1035,13 +1039,13 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
         read_a(P, 0);
         copy_a(t + 1, 0);
         copy_b(t + 1, 1);
-        wait_vmcnt<4>();            // A1 of step t, B0 of step t + 1
+        wait_vmcnt<kTwoHalves>();   // A1 of step t, B0 of step t + 1
         multiply(c0, fb[P], c0, fb1);
         read_b(fb[P ^ 1], P ^ 1, 0);
         read_a(P, 1);
         copy_a(t + 1, 1);
         copy_b(t + 2, 0);
-        wait_vmcnt<4>();            // A0 and B1 of step t + 1
+        wait_vmcnt<kTwoHalves>();   // A0 and B1 of step t + 1
         multiply(c1, fb1, c1, fb[P]);
       };
       for (int t = 0; t < steps; t += 2) {
