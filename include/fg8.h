@@ -516,6 +516,16 @@ fg8_status moe_combine_backward(const void* dout, const void* y, int32_t is_bf16
 fg8_status fg8_tile_choice(int32_t mode, int64_t m, int64_t n, int64_t k, int32_t groups,
                            int32_t num_cus, int32_t* out);
 
+/* The same for the BF16 products: product 0 gemm_bf16_epilogue, 1 and 2 its
+ * gradients dx and dw, 3 grouped_gemm_bf16, 4 its dgrad, 5 its wgrad; m (rows),
+ * n, k and groups (num_experts; 1 for products 0 to 2) as those take them.
+ * Writes out[0..3] = tile rows, tile columns, splits of the summed axis, and 1
+ * for one workgroup a compute unit (0: one a tile and split).  FG8_EINVAL for a
+ * NULL out, an unknown product, sizes < 1 or past 2^31 - 1024, groups > 1024 or
+ * num_cus < 1. */
+fg8_status fg8_bf16_tile_choice(int32_t product, int64_t m, int64_t n, int64_t k, int32_t groups,
+                                int32_t num_cus, int32_t* out);
+
 /* Text of the calling thread's last non-OK status ("" if none). */
 const char* fg8_last_error(void);
 

@@ -6,6 +6,7 @@ has not been built.
 """
 from ._lib import (  # noqa: F401
     Fg8Error,
+    bf16_tile_choice,
     fp8_quantize,
     gemm_bf16_epilogue,
     gemm_bf16_epilogue_backward,

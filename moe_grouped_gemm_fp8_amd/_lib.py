@@ -72,6 +72,7 @@ _SIGNATURES = {
                              _c_i64, _c_ptr, _c_ptr, _c_ptr],
     "fg8_gemm_workspace_bytes": [_c_i64, _c_i64, _c_i64],
     "fg8_tile_choice": [_c_i32, _c_i64, _c_i64, _c_i64, _c_i32, _c_i32, _c_ptr],
+    "fg8_bf16_tile_choice": [_c_i32, _c_i64, _c_i64, _c_i64, _c_i32, _c_i32, _c_ptr],
     "fg8_last_error": [],
     "fg8_version": [],
 }
@@ -169,6 +170,22 @@ def tile_choice(mode, m, n, k, groups=1, num_cus=None):
     out = (ctypes.c_int32 * 5)()
     _check(lib().fg8_tile_choice(mode, m, n, k, groups, num_cus, ctypes.cast(out, ctypes.c_void_p)))
     return dict(zip(("bm", "bn", "splits", "grid", "raster"), list(out)))
+
+
+BF16_PRODUCTS = ("gemm_bf16_epilogue", "dx", "dw", "grouped_gemm_bf16", "grouped_gemm_bf16_dgrad", "grouped_gemm_bf16_wgrad")
+
+
+def bf16_tile_choice(product, m, n, k, groups=1, num_cus=None):
+    """The tiling the library picks for a BF16 product (fg8_bf16_tile_choice):
+    one of BF16_PRODUCTS ("dx" and "dw" of gemm_bf16_epilogue_backward) with m
+    rows, n, k and experts as that call takes them; dict of bm, bn, splits,
+    persistent.  num_cus defaults to the current device's."""
+    if num_cus is None:
+        num_cus = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    out = (ctypes.c_int32 * 4)()
+    _check(lib().fg8_bf16_tile_choice(BF16_PRODUCTS.index(product), m, n, k, groups, num_cus,
+                                      ctypes.cast(out, ctypes.c_void_p)))
+    return dict(zip(("bm", "bn", "splits", "persistent"), list(out)))
 
 
 # --------------------------------------------------------------- quantize

@@ -775,6 +775,29 @@ fg8_status gemm_bf16_epilogue_backward(const uint16_t* dy, int64_t lddy, const u
   return FG8_OK;
 }
 
+fg8_status fg8_bf16_tile_choice(int32_t product, int64_t m, int64_t n, int64_t k, int32_t groups,
+                                int32_t num_cus, int32_t* out) {
+  const char* fn = "fg8_bf16_tile_choice";
+  if (!out) return fail(FG8_EINVAL, "%s: out is NULL", fn);
+  if (product < 0 || product > 5 || m < 1 || n < 1 || k < 1 || m > kMaxRows || n > kMaxRows || k > kMaxRows ||
+      groups < 1 || groups > (product < 3 ? 1 : 1024) || num_cus < 1)
+    return fail(FG8_EINVAL, "%s: bad arguments (product=%d m=%lld n=%lld k=%lld groups=%d num_cus=%d)", fn,
+                (int)product, (long long)m, (long long)n, (long long)k, (int)groups, (int)num_cus);
+  const int form = product % 3;    // forward, input gradient, weight gradient
+  fg8::BfProblem p = form == 0   ? dense_bf16(m, n, k, false, false)
+                     : form == 1 ? dense_bf16(m, k, n, false, true)
+                                 : dense_bf16(n, k, m, true, true);
+  if (product >= 3) {
+    p.mode = form == 2 ? fg8::kBfKRuns : fg8::kBfRowRuns;
+    p.groups = groups;
+  }
+  const fg8::BfTile t = fg8::bf16_tile(p, num_cus);
+  out[0] = t.bm; out[1] = t.bn; out[2] = t.splits; out[3] = t.persistent;
+  return FG8_OK;
+}
+
+}  // extern "C"
+
 namespace {
 
 constexpr int64_t kMaxNormCols = 32768;
@@ -790,6 +813,8 @@ fg8_status check_norm(const char* fn, int64_t rows, int64_t cols, int32_t x_is_b
 }
 
 }  // namespace
+
+extern "C" {
 
 fg8_status layer_norm(const void* x, int64_t ldx, int32_t x_is_bf16, const void* weight,
                       const void* bias, int32_t w_is_bf16, float eps, int64_t rows, int64_t cols,
