@@ -1161,25 +1161,42 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
   const int64_t runs = p.mode == kBfDense ? 1 : p.groups;
   auto units = [&](int c) { return runs * ((rows + kBm[c] - 1) / kBm[c]) * (((int64_t)p.N + kBn[c] - 1) / kBn[c]); };
   // (times in us, the choice first; 256 CUs)
+  //
+  // One product: 128 x 128 tiles while all of them run at once, two a CU, and
+  // the big tile beyond, where they would take a second round.  At 512 of them
+  // (128 big ones): 2048 x 4096 x 7168 111 for 118, with GELU, residual and z
+  // 122 for 135, dx of 4096 x 7168 x 2048 148 for 159 alone and 250 for 266
+  // within its backward pass, dW of 4096 x 4096 x 2048 169 for 182 within its.
+  // At 560 to 640: 1280 x 7168 x 2048 42 for 56, 4096 x 2560 x 7168 129 for 182,
+  // dW of 4000 x 5000 x 2048 207 for 239.
+  const bool dense = p.mode == kBfDense;
+  const bool second_round = units(kMid) > 2 * cus;
   if (p.a_kmajor) {
-    // Long runs or one product: the big tile.  Many tiles of short runs are
-    // bound by their stores, which two workgroups a CU interleave with sums
-    // (32 runs of 64 rows, 7168 x 2048: 288 for 312).  Few tiles: small ones
-    // (16 runs of 250 rows, 2048 x 1024: 39 for 43 and 47).
-    const bool dense = p.mode == kBfDense;
-    if (dense ? 2 * units(kBig) >= cus : p.K >= 400 * runs && units(kBig) >= 16 * cus) t.cfg = kBig;
+    // Weight gradients of runs: the big tile from two tiles and 64 of its steps
+    // a CU on (8 runs of 4096 rows, 4096 x 2048: 461-482 for 520-529 and
+    // 562-578; 8 of 1024 144-152 for 149-155 and 158-165; 16 of 512 175-200 for
+    // 178-187 and 200-209; below: 8 of 512 96-98 for 90-92, 16 of 1024,
+    // 2048 x 1024, 129 for 106).  Short runs of many tiles are bound by their
+    // stores, which two workgroups a CU interleave with sums (32 runs of 64
+    // rows, 7168 x 2048: 288 for 312).  Few tiles: small ones (16 runs of 250
+    // rows, 2048 x 1024: 39 for 43 and 47).
+    const bool deep = units(kBig) >= 2 * cus && units(kBig) * (p.K / runs) >= (int64_t)4096 * cus;
+    if (dense ? second_round : deep) t.cfg = kBig;
     else t.cfg = !dense && units(kBig) >= 6 * cus ? kDuo : kMid;
-  } else if (rows > 128 && 2 * units(kBig) >= cus) {
-    // 128 big tiles on as many CUs: 4096 x 2048 x 7168, B k-major, 152 alone
-    // for 120, but 258 for 284 within its backward pass
+  } else if (rows > 128 && (dense ? second_round : 2 * units(kBig) >= cus)) {
+    // Row runs, whose ends inside tiles are not known here: the big tile from
+    // half the CUs on, by the runs' average.  8 ragged runs of 512 rows on
+    // average, 2048 x 2048 (128 big tiles by it, 168 in fact): 43 for 54, of
+    // 1024 rows (256, 296) 89 for 82, of 1024 rows, 4096 x 2048 (512, 592) 136
+    // for 145.  Runs of whole tiles: 41 for 34, 56 for 65, 104 for 137.
     t.cfg = kBig;
   } else if (rows <= 8 && !p.b_kmajor && p.K <= 4096 && units(kFew) <= 2 * cus) {
     t.cfg = kFew;      // 1 x 1024 x 2048 5.5 for 6.6; 1 x 2112 x 7168 12.8 for 11.2
-  } else if (rows <= (p.mode == kBfDense ? 16 : 8)) {
+  } else if (rows <= (dense ? 16 : 8)) {
     t.cfg = kThin;     // 16 x 2112 x 7168 11.3 for 12.2; 32 runs of 16 rows on average 366 for 345
   } else if (rows <= 32) {
     t.cfg = kFlat;     // 32 x 2112 x 7168 12.3 for 13.7
-  } else if (units(kMid) >= (p.mode == kBfDense ? 3 * cus / 2 : cus)) {
+  } else if (units(kMid) >= (dense ? 3 * cus / 2 : cus)) {
     t.cfg = kMid;      // 1024 x 7168 x 2048 36 for 47; 512 x 7168 x 2048 35 for 29
   } else {
     // 192 x 2112 x 7168 20.8 for 24.2; 384 x 2112 x 7168 28.9 for 33.9
@@ -1190,7 +1207,7 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
   t.threads = kThreads[t.cfg];
   t.persistent = t.cfg == kBig;
   t.splits = 1;
-  if (p.mode == kBfDense && t.cfg != kBig && t.cfg != kFew) {
+  if (dense && t.cfg != kBig && t.cfg != kFew) {
     // One workgroup a CU; two where several row tiles read the same weights
     // (64 x 2112 x 7168 14.1 in 6 splits, 16.2 in 12; 128 x 2112 x 7168 18.9
     // in 6, 19.8 in 3), and five steps a split at least.

@@ -42,3 +42,41 @@ def test_refusals(args):
     out = (ctypes.c_int32 * 4)()
     assert _lib.lib().fg8_bf16_tile_choice(*args, ctypes.cast(out, ctypes.c_void_p)) == 1
     assert _lib.lib().fg8_bf16_tile_choice(0, 8, 8, 8, 1, 256, None) == 1
+
+
+BIG, DUO, MID = (256, 256, 1, 1), (128, 256, 1, 0), (128, 128, 1, 0)
+
+
+@pytest.mark.parametrize("m,n,k", [(2048, 4096, 7168), (4096, 2048, 7168), (1024, 7168, 2048)])
+def test_dense_small_tiles_while_one_round_holds_them(m, n, k):
+    """Up to two 128 x 128 tiles a CU, for y and for gradients of that size:
+    the big tile measured 6 to 17% slower there."""
+    assert choice(FORWARD, m, n, k) == MID
+    assert choice(DX, m, k, n) == MID               # dx [m][n], summed over k
+    assert choice(DW, k, m, n) == MID               # dw [m][n], summed over k
+
+
+@pytest.mark.parametrize("m,n,k", [(1280, 7168, 2048), (4096, 2560, 7168), (4000, 5000, 2048), (8192, 8192, 8192)])
+def test_dense_big_tiles_from_a_second_round_on(m, n, k):
+    assert choice(FORWARD, m, n, k) == BIG
+    assert choice(DX, m, k, n) == BIG
+    assert choice(DW, k, m, n) == BIG
+
+
+def test_the_backward_pass_of_4096x7168x2048():
+    assert choice(DX, 4096, 7168, 2048) == MID and choice(DW, 4096, 7168, 2048) == BIG
+
+
+@pytest.mark.parametrize("runs,rows,n,k,tile", [
+    (8, 4096, 4096, 2048, BIG), (2, 8192, 4096, 4096, BIG), (8, 1024, 4096, 2048, BIG), (16, 1024, 7168, 2048, BIG),
+    (32, 512, 7168, 2048, BIG),                                              # long runs, two tiles a CU and more
+    (16, 250, 4096, 2048, DUO), (32, 64, 7168, 2048, DUO),                   # short runs of many tiles
+    (8, 512, 4096, 2048, MID), (4, 1024, 4096, 2048, MID), (16, 1024, 2048, 1024, MID), (2, 4096, 2048, 2048, MID)])
+def test_weight_gradients_of_runs(runs, rows, n, k, tile):
+    assert choice(WGRAD, runs * rows, n, k, runs) == tile
+
+
+def test_row_runs_from_half_the_device_on():
+    for product, n, k in ((GROUPED, 2048, 1024), (DGRAD, 1024, 2048)):
+        assert choice(product, 8 * 512, n, k, 8) == BIG                     # 128 by the average
+        assert choice(product, 8 * 256, n, k, 8) != BIG                     # 64
