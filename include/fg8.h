@@ -428,9 +428,12 @@ size_t fg8_gemm_bf16_workspace_bytes(int64_t m, int64_t n, int64_t k);
  *   dy bf16 [m][lddy] (any lddy >= n)   z bf16 [m][n] (NULL without activation)
  *   dx bf16 [m][k], dw [n][k] float or bf16, dbias float [n]: each may be NULL
  *   and is then not computed (w is needed for dx, x for dw).
- *   dz is rounded to BF16 for the two products (the matrix units' operand
- *   type); dbias sums it before that rounding.  relu' (0) = 0, and where z <= 0 an
- *   infinite dy does not pass either.
+ *   Behind SiLU and GELU dz is rounded to BF16 for dx and for a bf16 dw (the
+ *   matrix units' operand type; that and the outputs' own rounding make 0.0023
+ *   of relative error for 0.0017).  A float dw takes dz in two BF16 parts, to
+ *   2^-16 of each value, in a second pass and product (where an infinite x makes
+ *   its dw NaN); dbias sums dz in float.
+ *   relu' (0) = 0, and where z <= 0 an infinite dy does not pass either.
  *   k % 8 == 0 (else FG8_EUNSUPPORTED), any n, m >= 1.
  *   workspace: fg8_gemm_bf16_backward_workspace_bytes(m, n, k) bytes, under
  *   gemm_bf16_epilogue's rules (it holds dz and partial sums besides).

@@ -641,7 +641,8 @@ def gemm_bf16_epilogue_backward(dy, x, w, z=None, activation="none", dw_dtype=to
     """Gradients of act(x w^T + bias) (the residual's is dy itself): dy bf16
     [m, n], x bf16 [m, k], w bf16 [n, k], z bf16 [m, n] as saved -> (dx bf16
     [m, k], dw dw_dtype [n, k], dbias float32 [n]); `needs` leaves out (None)
-    what is not wanted."""
+    what is not wanted.  Behind "silu" and "gelu" dx and a bfloat16 dw take dz
+    rounded to bfloat16, a float32 dw to 2^-16 (a second product)."""
     act = ACTIVATIONS[activation]
     _dev(w, torch.bfloat16, "w")
     lddy, ldx = _rows(dy, torch.bfloat16, "dy"), _rows(x, torch.bfloat16, "x")

@@ -106,6 +106,7 @@ struct BfProblem {
   int64_t ldr;
   uint16_t* z;                  // the value before the activation, BF16
   int64_t ldz;
+  int add;                      // dense, both operands k-major, FP32: D += the product
   int grid;                     // workgroups of a persistent launch (set by the launcher)
   // split k (dense)
   int splits;
@@ -124,10 +125,11 @@ hipError_t launch_bf16(BfProblem p, const BfTile& t, hipStream_t stream);
 
 // dz = dy * act'(z) in BF16 (row stride ldz, zeros from column n up to it) and
 // its column sums, by `chunks` row ranges in partial [chunks][n], then in
-// dbias [n]; either result may be left out (NULL).
+// dbias [n]; either result may be left out (NULL).  rest: what that rounding of
+// dz left, in BF16 again (0 beside an infinity or NaN), in its place.
 int act_backward_chunks(int64_t m, int64_t n);
 hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldzin,
-                               int act, int64_t m, int64_t n, uint16_t* dz, int64_t ldz,
+                               int act, int64_t m, int64_t n, bool rest, uint16_t* dz, int64_t ldz,
                                float* partial, float* dbias, hipStream_t stream);
 
 // --------------------------------------------------------------- layer norm

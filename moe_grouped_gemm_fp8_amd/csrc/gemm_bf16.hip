@@ -475,6 +475,16 @@ __device__ __forceinline__ void store_four(float* q, int64_t ld, int c, int N, b
   }
 }
 
+// The four columns from c on of the row at q as they lie there (0 past N).
+__device__ __forceinline__ v4f load_four(const float* q, int64_t ld, int c, int N) {
+  if (ld % 4 == 0 && c + 4 <= N) return *reinterpret_cast<const v4f*>(q + c);
+  v4f v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (c + i < N) v[i] = q[c + i];
+  return v;
+}
+
 // Sixteen rows x 64 columns as BF16 (2 KB of LDS) -> rows m + l / 8 (+ 8),
 // columns n + 8 (l % 8) ..: eight lanes a row, 128 bytes.
 __device__ __forceinline__ void store_bf16_rows(uint8_t* turn, const v4f (&v)[4], uint16_t* to, int64_t ld,
@@ -491,7 +501,9 @@ __device__ __forceinline__ void store_bf16_rows(uint8_t* turn, const v4f (&v)[4]
     if (full || r < rows) store_eight(to + r * ld, ld, n + 8 * c, N, full, u);
   }
 }
-// Sixteen rows x 32 columns as FP32 (2 KB): eight lanes a row, 128 bytes.
+// Sixteen rows x 32 columns as FP32 (2 KB): eight lanes a row, 128 bytes.  ADD:
+// on top of what lies there.
+template <bool ADD>
 __device__ __forceinline__ void store_f32_rows(uint8_t* turn, v4f a, v4f b, float* to, int64_t ld, int rows,
                                                int n, int N, int lane, bool full) {
   const int i = lane & 15, g = lane >> 4;
@@ -500,8 +512,11 @@ __device__ __forceinline__ void store_f32_rows(uint8_t* turn, v4f a, v4f b, floa
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r = 8 * h + (lane >> 3), c = lane & 7;
-    const v4f u = *reinterpret_cast<const v4f*>(turn + r * 128 + ((c ^ swz(r)) << 4));
-    if (full || r < rows) store_four(to + r * ld, ld, n + 4 * c, N, full, u);
+    v4f u = *reinterpret_cast<const v4f*>(turn + r * 128 + ((c ^ swz(r)) << 4));
+    if (full || r < rows) {
+      if constexpr (ADD) u += load_four(to + r * ld, ld, n + 4 * c, N);
+      store_four(to + r * ld, ld, n + 4 * c, N, full, u);
+    }
   }
 }
 // Sixteen rows x 64 columns staged as FP32 (4 KB), the residual's piece (res)
@@ -543,8 +558,9 @@ __device__ __forceinline__ uint4 residual8(const BfProblem& p, int64_t m, int c)
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One unit's output: what rows16() needs beside the values.
-template <bool EPI>
+// One unit's output: what rows16() needs beside the values.  ADD: on top of an
+// FP32 output that is there (instances of their own, the others stay as they are).
+template <bool EPI, bool ADD>
 struct TileOut {
   static constexpr int kTurn = EPI ? 4096 : 2048;    // LDS of a wave
   const BfProblem& p;
@@ -589,8 +605,8 @@ struct TileOut {
     if (p.out_bf16) {
       store_bf16_rows(turn, v, (uint16_t*)d + m * p.ldd, p.ldd, left, n, p.N, lane, full);
     } else {
-      store_f32_rows(turn, v[0], v[1], (float*)d + m * p.ldd, p.ldd, left, n, p.N, lane, full);
-      store_f32_rows(turn, v[2], v[3], (float*)d + m * p.ldd, p.ldd, left, n + 32, p.N, lane, full);
+      store_f32_rows<ADD>(turn, v[0], v[1], (float*)d + m * p.ldd, p.ldd, left, n, p.N, lane, full);
+      store_f32_rows<ADD>(turn, v[2], v[3], (float*)d + m * p.ldd, p.ldd, left, n + 32, p.N, lane, full);
     }
   }
 };
@@ -611,7 +627,7 @@ __device__ __forceinline__ bool last_of_splits(const BfProblem& p, const BfUnit&
   return *last;
 }
 // ------------------------------------------------------------------ kernel
-template <class C, bool AK, bool BK, int MODE>
+template <class C, bool AK, bool BK, int MODE, bool ADD = false>
 __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::STAGES * C::STAGE_BYTES];
   __shared__ int last;
@@ -706,9 +722,10 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
 
   if constexpr (C::WN == 64) {
     constexpr bool EPI = MODE == kBfDense && !AK && !BK;
-    static_assert(C::WAVES * TileOut<EPI>::kTurn <= C::STAGES * C::STAGE_BYTES, "rows turn in the stages");
+    typedef TileOut<EPI, ADD> Out;
+    static_assert(C::WAVES * Out::kTurn <= C::STAGES * C::STAGE_BYTES, "rows turn in the stages");
     __syncthreads();      // every wave is done with the stages
-    const TileOut<EPI> out(p, w, C::BM, C::BN, wn0, smem + wave * TileOut<EPI>::kTurn, lane);
+    const Out out(p, w, C::BM, C::BN, wn0, smem + wave * Out::kTurn, lane);
 #pragma unroll
     for (int i = 0; i < C::TM; ++i) {
       uint4 res[2];
@@ -915,12 +932,13 @@ __device__ __forceinline__ void phase_barrier() {
 // take 0.31: the two add up whatever the order of the tiles (experts mixed over
 // the XCDs, other numbers of tiles together on one, staggered starts and two
 // workgroups a CU measured within 2% or slower).
-template <bool AK, bool BK, int MODE, bool EPI>
+template <bool AK, bool BK, int MODE, bool EPI, bool ADD = false>
 __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
   typedef HalfTile<AK, 64> HalfA;
   typedef HalfTile<BK, 32> HalfB;
+  typedef TileOut<EPI, ADD> Out;
   constexpr uint32_t kHalf = HalfA::BYTES;         // LDS: per stage A0, A1, B0, B1
-  constexpr uint32_t kTurns = 8 * kHalf, kTable = kTurns + 8 * TileOut<EPI>::kTurn;
+  constexpr uint32_t kTurns = 8 * kHalf, kTable = kTurns + 8 * Out::kTurn;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kTable + (MODE == kBfRowRuns ? sizeof(RunTable) : 0)];
   static_assert(sizeof(smem) <= kLdsBytes, "all the LDS of the kernel: the stages, the waves' turns, the runs");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1058,7 +1076,7 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
     }
 
     const int here = opaque(lane);
-    TileOut<EPI> out(p, w, 256, 256, q * 64, smem + kTurns + wave * TileOut<EPI>::kTurn, here);
+    Out out(p, w, 256, 256, q * 64, smem + kTurns + wave * Out::kTurn, here);
     if constexpr (EPI) {       // the bias has arrived before the copies below queue up
 #pragma unroll
       for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(out.bias[i]));
@@ -1142,9 +1160,14 @@ hipError_t launch_tile(BfProblem p, const BfTile& t, hipStream_t stream) {
   if constexpr (MODE == kBfKRuns) {
     if (t.cfg == kDuo) return start(bf16_kernel<BfDuo, AK, BK, MODE>, p, units, BfDuo::THREADS, stream);
   }
-  if (t.cfg == kMid) return start(bf16_kernel<BfMid, AK, BK, MODE>, p, units, BfMid::THREADS, stream);
   const unsigned cus = (unsigned)device_cu_count();
   p.grid = (int)(units < cus ? units : cus);
+  if constexpr (MODE == kBfDense && AK && BK) {
+    if (p.add)
+      return t.cfg == kMid ? start(bf16_kernel<BfMid, AK, BK, MODE, true>, p, units, BfMid::THREADS, stream)
+                           : start(bf16_big_kernel<AK, BK, MODE, false, true>, p, p.grid, 512, stream);
+  }
+  if (t.cfg == kMid) return start(bf16_kernel<BfMid, AK, BK, MODE>, p, units, BfMid::THREADS, stream);
   if constexpr (MODE == kBfDense && !AK && !BK) {
     if (p.bias || p.act != kActNone || p.residual || p.z)
       return start(bf16_big_kernel<AK, BK, MODE, true>, p, p.grid, 512, stream);

@@ -491,11 +491,20 @@ __device__ __forceinline__ float act_gradient(int act, float z, float dy) {
   return dy;
 }
 
+// What rounding d to BF16 leaves (exact in FP32); 0 beside an infinity or NaN.
+__device__ __forceinline__ float bf16_rest(float d) {
+  const uint32_t hi = bf16x2(d, 0.f) << 16;
+  return (hi & 0x7f800000u) == 0x7f800000u ? 0.f : d - __uint_as_float(hi);
+}
+
 constexpr int kActCols = 512;   // columns of a workgroup: eight a lane
 
 // Bound by HBM: dy and z read, dz written once (4096 x 7168 0.036 ms, 4.9 TB/s).
 // Workgroup (column block, row chunk): its four waves take the chunk's rows in
-// turn and meet in LDS for the column sums, taken before dz is rounded.
+// turn and meet in LDS for the column sums, taken before dz is rounded.  REST:
+// what that rounding left, in dz's place (an instance of its own: as a run-time
+// choice it cost every dz 20 us of these 36).
+template <bool REST>
 __global__ __launch_bounds__(256) void act_backward_kernel(
     const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ z, int64_t ldzin,
     int act, int64_t m, int64_t n, int64_t per, uint16_t* __restrict__ dz, int64_t ldz,
@@ -521,6 +530,7 @@ __global__ __launch_bounds__(256) void act_backward_kernel(
         // (a slope of NaN past the last column would not reach dz's padding)
         if (c + i >= n) d[i] = 0.f;
         s[i] += d[i];
+        if constexpr (REST) d[i] = bf16_rest(d[i]);
       }
       if (dz) Piece<uint16_t>::store(dz + r * ldz, c, ldz, d);
     }
@@ -546,13 +556,13 @@ int act_backward_chunks(int64_t m, int64_t n) {
 }
 
 hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldzin,
-                               int act, int64_t m, int64_t n, uint16_t* dz, int64_t ldz,
+                               int act, int64_t m, int64_t n, bool rest, uint16_t* dz, int64_t ldz,
                                float* partial, float* dbias, hipStream_t stream) {
   const int chunks = act_backward_chunks(m, n);
   const int64_t per = (m + chunks - 1) / chunks;
-  hipLaunchKernelGGL(act_backward_kernel, dim3((unsigned)((n + kActCols - 1) / kActCols), (unsigned)chunks),
-                     dim3(256), 0, stream, dy, lddy, z, ldzin, act, m, n, per, dz, ldz,
-                     dbias ? partial : nullptr);
+  hipLaunchKernelGGL(rest ? act_backward_kernel<true> : act_backward_kernel<false>,
+                     dim3((unsigned)((n + kActCols - 1) / kActCols), (unsigned)chunks), dim3(256), 0, stream, dy,
+                     lddy, z, ldzin, act, m, n, per, dz, ldz, dbias ? partial : nullptr);
   if (dbias)
     hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((n + 63) / 64)), dim3(1024), 0, stream,
                        partial, chunks, n, n, dbias, dbias);
