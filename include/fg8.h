@@ -344,12 +344,12 @@ int64_t fg8_moe_capacity(int64_t tokens, int32_t topk, int32_t num_experts);
  * around its FP8 products, forward and backward.  bfloat16 values are uint16_t
  * bit patterns.  ld arguments count elements between rows and let a row be
  * part of a wider one; pointers are 16-byte aligned as everywhere, and ld of
- * an operand that a product reads is a multiple of 8 and at most 2^22 (a
- * larger one is FG8_EUNSUPPORTED); the products take 2^31 - 1024 rows at most,
- * and no more tiles than a launch of fewer than 2^32 threads holds (more:
- * FG8_EUNSUPPORTED).  All sums are FP32, rounded once where the
- * output is BF16.  Sums run in a fixed order: the same call gives the same
- * bits.  m, rows or tokens of 0 are valid where a call takes them: nothing is
+ * an operand that a product reads is a multiple of 8.  No ld exceeds 2^22, and
+ * in the products neither n nor k, the row lengths of w, y and the gradients
+ * (FG8_EUNSUPPORTED); the products take 2^31 - 1024 rows at most, and no more
+ * tiles than a launch of fewer than 2^32 threads holds (more:
+ * FG8_EUNSUPPORTED).  All sums are FP32, rounded once where the output is BF16.
+ * Sums run in a fixed order: the same call gives the same bits.  m, rows or tokens of 0 are valid where a call takes them: nothing is
  * read, and gradients summed over them are zeros.
  */
 

@@ -10,7 +10,8 @@
 // pieces of a token and has the pieces of up to kAhead of its rows in flight
 // together; a token's indices and weights sit in its lanes and are handed out
 // with readlane.  8192 tokens x 7168, top-8 of 32: forward with a residual
-// 0.212 ms (5.5 TB/s), backward 0.399 ms (5.0 TB/s); a plain copy moves 4.9.
+// 0.212 ms (5.5 TB/s), backward 0.398 ms (5.0 TB/s); in FP32 0.44 and 0.83 ms
+// (5.4 and 5.0); a plain copy moves 4.8-4.9.
 #include "fg8_device.h"
 #include "fg8_internal.h"
 

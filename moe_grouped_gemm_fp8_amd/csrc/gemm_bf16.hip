@@ -30,8 +30,8 @@
 //
 // What bounds them (one MI355X; a library product of 8192^3 in BF16 runs at
 // 1480-1620 TFLOP/s there, 1.4 to 1.6 GHz under that load):
-//   compute: 8192^3 0.72-0.75 ms, 1470-1530 TFLOP/s, with B k-major 0.75-0.78,
-//     with both 0.78-0.80 (the library 0.79-0.80 and 0.91-0.93); MFMA busy 73% on ragged
+//   compute: 8192^3 0.72-0.76 ms, 1440-1530 TFLOP/s, with B k-major 0.75-0.81,
+//     with both 0.78-0.83 (the library 0.79-0.84 and 0.91-0.96); MFMA busy 73% on ragged
 //     runs of 1563 rows, K = 7168.  Short runs and few tiles lose to tiles that
 //     a run ends in and to the last round of the CUs.
 //   stores: the weight gradient of short runs, whose FP32 tiles take as long as

@@ -6,11 +6,19 @@
 //   dx = rstd * (g - mean(g) - h * mean(g h))
 //   dweight = sum over rows of dy h,   dbias = sum over rows of dy
 //
-// All arithmetic is FP32.  HBM bounds these: a row is read once (x, and dy)
-// and written once.  Measured: forward 32768 x 7168 BF16 0.170 ms (5.5 TB/s)
-// and 16383 x 7168 FP32 0.178 ms, backward 0.300 (4.7 TB/s) and 0.265 ms; a
-// plain copy moves 4.9 TB/s here.  Rows of odd length cost nothing extra:
-// 20000 x 2051 FP32 0.059 and 0.100 ms, 5.5 and 4.9 TB/s.
+// All arithmetic is FP32.  A row is read once (x, and dy) and written once.
+// HBM bounds the forward pass of many rows: 32768 x 7168 BF16 0.19-0.20 ms
+// (4.7-5.0 TB/s), 16383 x 7168 FP32 0.178 (5.3), rows of odd length the same
+// (20000 x 2051 FP32 0.060, 5.5); 16000 x 12000 and 4000 x 32768 BF16 run at 3.8.
+// A plain copy moves 4.8-4.9 TB/s here.  The backward pass by size:
+//   many rows of up to 8192 columns: HBM.  32768 x 7168 BF16 0.295-0.305 ms (4.6
+//     to 4.8 TB/s), 16383 x 7168 FP32 0.27 (5.2), 20000 x 2051 FP32 0.100 (4.9).
+//   above 8192 columns: registers.  Both parameters' running sums leave no room
+//     for a row ahead, and from there on spill: 16000 x 12000 BF16 0.45 ms and
+//     8000 x 16384 FP32 0.615 (2.6 TB/s), 4000 x 32768 BF16 1.3-1.4 (0.6).
+//   up to a few thousand rows: the partial sums, 8 bytes a column from every team
+//     and read again.  512 x 7168 BF16 22 us, 2048 x 7168 31 (2.8 TB/s), 4096 x
+//     7168 44 (4.0); 65536 x 256 38 (2.7), whose sums are added by 8 workgroups.
 //
 // A team of WAVES waves owns a row at a time and holds it in registers, so the
 // variance is taken around the mean (two passes over registers, not the sum of
@@ -370,7 +378,7 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
 // The team shape for a row length: waves a row and 16-byte pieces a thread.
 // Sixteen columns a thread are the rule (registers for a row ahead and,
 // backward, both running sums); the longest rows take 32.  (Backward, 16000 x
-// 12000 BF16: 0.48 ms in eight waves of 32 columns, 0.76 in sixteen of 16; FP32
+// 12000 BF16: 0.45 ms in eight waves of 32 columns, 0.76 in sixteen of 16; FP32
 // 8000 x 16384 0.79 and 0.62.)
 template <class T, bool BACKWARD, class F>
 hipError_t with_shape(int64_t cols, F f) {

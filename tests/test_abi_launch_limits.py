@@ -56,3 +56,15 @@ def test_products(L):
     # runs: long ones take a launch of one workgroup a CU, which has no such limit)
     assert L.grouped_gemm_bf16_wgrad(ok, n, ok, 1 << 18, ok, ok, 0, 2, n, 1 << 18, 4, None) == EUNSUPPORTED
     assert b"exceed a launch" in L.fg8_last_error()
+
+
+def test_row_strides(L):
+    """No ld past 2^22, an output's or a normed row's either."""
+    far, n = (1 << 22) + 8, 1 << 22
+    assert L.grouped_gemm_bf16(ok, 64, ok, ok, ok, far, 1, 10, 64, 64, 4, None) == EUNSUPPORTED
+    assert L.grouped_gemm_bf16_dgrad(ok, 64, ok, ok, ok, far, 1, 10, 64, 64, 4, None) == EUNSUPPORTED
+    assert L.gemm_bf16_epilogue(ok, 64, ok, None, 0, 0, ok, far, None, ok, 64, 1, 1024, 64, 64, None, 0, None) == EUNSUPPORTED
+    assert L.gemm_bf16_epilogue(ok, 64, ok, None, 0, 0, None, 0, None, ok, n + 8, 1, 1024, n + 8, 64, None, 0, None) == EUNSUPPORTED
+    assert L.gemm_bf16_epilogue_backward(ok, far, ok, 64, ok, ok, 3, ok, ok, 1, ok, 8, 64, 64, ok, 1 << 30, None) == EUNSUPPORTED
+    assert L.layer_norm(ok, far, 1, ok, None, 0, 1e-5, 4, 64, ok, ok, ok, None) == EUNSUPPORTED
+    assert L.layer_norm_backward(ok, far, ok, 64, 1, ok, 0, ok, ok, 4, 64, ok, ok, ok, ok, 1 << 20, None) == EUNSUPPORTED
