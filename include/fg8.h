@@ -447,6 +447,70 @@ fg8_status gemm_bf16_epilogue_backward(const uint16_t* dy, int64_t lddy, const u
 size_t fg8_gemm_bf16_backward_workspace_bytes(int64_t m, int64_t n, int64_t k);
 
 /*
+ * gemm_bf16_gated: both projections of a gated feed-forward block, its
+ * activation and its product in one kernel:
+ *   z = x w^T,   h[r][j] = act(z[r][j]) z[r][n + j]
+ *   x bf16 [m][ldx]   w bf16 [2 n][k]: n gate rows, then n up rows
+ *   z NULL, or bf16 [m][2 n] (output), for the backward pass; h is computed
+ *   from the unrounded sums
+ *   h [m][ldh] float or bf16
+ *   k % 8 == 0, any n >= 1, m >= 0; neither 2 n nor k above 2^22.
+ *   workspace: fg8_gemm_bf16_gated_workspace_bytes(m, n, k) bytes under
+ *   gemm_bf16_epilogue's rules.
+ */
+fg8_status gemm_bf16_gated(const uint16_t* x, int64_t ldx, const uint16_t* w,
+                           fg8_activation activation, uint16_t* z, void* h, int64_t ldh,
+                           fg8_out out, int64_t m, int64_t n, int64_t k, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+size_t fg8_gemm_bf16_gated_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/*
+ * grouped_gemm_bf16_gated: the same over ragged row runs, w bf16
+ * [num_experts][2 n][k]; row_offsets, rows and num_experts as
+ * grouped_gemm_bf16.  Rows of no run: h and z are zeros.
+ */
+fg8_status grouped_gemm_bf16_gated(const uint16_t* x, int64_t ldx, const uint16_t* w,
+                                   const int32_t* row_offsets, fg8_activation activation,
+                                   uint16_t* z, void* h, int64_t ldh, fg8_out out, int64_t rows,
+                                   int64_t n, int64_t k, int32_t num_experts, hipStream_t stream);
+
+/*
+ * gemm_bf16_gated_backward: its gradients from dh and z as saved,
+ *   dz[r][j] = dh[r][j] z[r][n + j] act'(z[r][j]),  dz[r][n + j] = dh[r][j] act(z[r][j])
+ *   dx = dz w,  dw = dz^T x
+ *   dh bf16 [m][lddh] (any lddh >= n)   z bf16 [m][2 n]
+ *   dx bf16 [m][k], dw [2 n][k] float or bf16; either may be NULL and is then
+ *   not computed (w is needed for dx, x for dw).
+ *   dz is rounded to BF16 for dx and a bf16 dw; a float dw takes it in two BF16
+ *   parts, as gemm_bf16_epilogue_backward's does.
+ *   k % 8 == 0, any n, m >= 1.  workspace:
+ *   fg8_gemm_bf16_gated_backward_workspace_bytes(m, n, k, 0) bytes under
+ *   gemm_bf16_epilogue's rules (it holds dz).
+ */
+fg8_status gemm_bf16_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* x,
+                                    int64_t ldx, const uint16_t* w, const uint16_t* z,
+                                    fg8_activation activation, uint16_t* dx, void* dw,
+                                    fg8_out dw_out, int64_t m, int64_t n, int64_t k,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * grouped_gemm_bf16_gated_backward: the same over ragged row runs, w and dw
+ * [num_experts][2 n][k].  Rows of no run: dx is zeros, and whatever they hold
+ * takes no part; an empty run's dw is zeros.  rows >= 1.  workspace:
+ * fg8_gemm_bf16_gated_backward_workspace_bytes(rows, n, k, num_experts) bytes,
+ * under the same rules.
+ */
+fg8_status grouped_gemm_bf16_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* x,
+                                            int64_t ldx, const uint16_t* w, const uint16_t* z,
+                                            const int32_t* row_offsets, fg8_activation activation,
+                                            uint16_t* dx, void* dw, fg8_out dw_out, int64_t rows,
+                                            int64_t n, int64_t k, int32_t num_experts,
+                                            void* workspace, size_t workspace_bytes,
+                                            hipStream_t stream);
+size_t fg8_gemm_bf16_gated_backward_workspace_bytes(int64_t m, int64_t n, int64_t k,
+                                                    int32_t num_experts);
+
+/*
  * layer_norm: y = (x - mean) rstd weight + bias over the last axis, with
  * rstd = 1 / sqrt(variance + eps) and the variance taken around the mean.
  *   x [rows][ldx] bf16 (x_is_bf16 = 1) or float (0), any cols and ldx

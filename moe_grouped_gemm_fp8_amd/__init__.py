@@ -10,12 +10,16 @@ from ._lib import (  # noqa: F401
     fp8_quantize,
     gemm_bf16_epilogue,
     gemm_bf16_epilogue_backward,
+    gemm_bf16_gated,
+    gemm_bf16_gated_backward,
     gemm_fp8_blockscaled,
     gemm_fp8_blockscaled_noalloc,
     gemm_mxfp8,
     gemm_workspace_bytes,
     grouped_gemm_bf16,
     grouped_gemm_bf16_dgrad,
+    grouped_gemm_bf16_gated,
+    grouped_gemm_bf16_gated_backward,
     grouped_gemm_bf16_wgrad,
     grouped_gemm_fp8_contiguous,
     grouped_gemm_fp8_contiguous_swiglu,

@@ -60,6 +60,18 @@ _SIGNATURES = {
                                     _c_ptr, ctypes.c_size_t, _c_ptr],
     "fg8_gemm_bf16_workspace_bytes": [_c_i64, _c_i64, _c_i64],
     "fg8_gemm_bf16_backward_workspace_bytes": [_c_i64, _c_i64, _c_i64],
+    "gemm_bf16_gated": [_c_ptr, _c_i64, _c_ptr, ctypes.c_int, _c_ptr, _c_ptr, _c_i64, ctypes.c_int,
+                        _c_i64, _c_i64, _c_i64, _c_ptr, ctypes.c_size_t, _c_ptr],
+    "grouped_gemm_bf16_gated": [_c_ptr, _c_i64, _c_ptr, _c_ptr, ctypes.c_int, _c_ptr, _c_ptr, _c_i64,
+                                ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i32, _c_ptr],
+    "gemm_bf16_gated_backward": [_c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_ptr, ctypes.c_int, _c_ptr,
+                                 _c_ptr, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_ptr,
+                                 ctypes.c_size_t, _c_ptr],
+    "grouped_gemm_bf16_gated_backward": [_c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_ptr, _c_ptr,
+                                         ctypes.c_int, _c_ptr, _c_ptr, ctypes.c_int, _c_i64, _c_i64,
+                                         _c_i64, _c_i32, _c_ptr, ctypes.c_size_t, _c_ptr],
+    "fg8_gemm_bf16_gated_workspace_bytes": [_c_i64, _c_i64, _c_i64],
+    "fg8_gemm_bf16_gated_backward_workspace_bytes": [_c_i64, _c_i64, _c_i64, _c_i32],
     "layer_norm": [_c_ptr, _c_i64, _c_i32, _c_ptr, _c_ptr, _c_i32, ctypes.c_float, _c_i64, _c_i64,
                    _c_ptr, _c_ptr, _c_ptr, _c_ptr],
     "layer_norm_backward": [_c_ptr, _c_i64, _c_ptr, _c_i64, _c_i32, _c_ptr, _c_i32, _c_ptr, _c_ptr,
@@ -80,6 +92,8 @@ _RESTYPES = {"fg8_gemm_workspace_bytes": ctypes.c_size_t, "fg8_last_error": ctyp
              "fg8_moe_capacity": ctypes.c_int64,
              "fg8_gemm_bf16_workspace_bytes": ctypes.c_size_t,
              "fg8_gemm_bf16_backward_workspace_bytes": ctypes.c_size_t,
+             "fg8_gemm_bf16_gated_workspace_bytes": ctypes.c_size_t,
+             "fg8_gemm_bf16_gated_backward_workspace_bytes": ctypes.c_size_t,
              "fg8_layer_norm_backward_workspace_bytes": ctypes.c_size_t}
 
 _lib = None
@@ -671,6 +685,125 @@ def gemm_bf16_epilogue_backward(dy, x, w, z=None, activation="none", dw_dtype=to
         dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), _ptr(z), act, _ptr(dx), _ptr(dw),
         _out_code(dw_dtype), _ptr(db), m, n, k, ws, ws_bytes, stream))
     return dx, dw, db
+
+
+# --------------------------------------------- gated feed-forward products
+def _gated_weights(w, k, lead):
+    _dev(w, torch.bfloat16, "w")
+    if w.dim() != 2 + lead or w.shape[-1] != k or w.shape[-2] % 2 or w.shape[-2] == 0:
+        raise ValueError("w must be " + ("[E, 2 n, k]" if lead else "[2 n, k]") + " with x's k")
+    return w.shape[-2] // 2
+
+
+def _run_offsets(w, row_offsets):
+    _dev(row_offsets, torch.int32, "row_offsets")
+    if row_offsets.shape != (w.shape[0] + 1,):
+        raise ValueError("row_offsets must be [E + 1]")
+    return w.shape[0]
+
+
+def gemm_bf16_gated(x, w, activation="silu", save_z=False, out_dtype=torch.bfloat16, out=None,
+                    workspace=None):
+    """h = act(x wg^T) * (x wu^T) in one kernel: x bf16 [m, k] (rows may be
+    strided), w bf16 [2 n, k] with wg the first n rows and wu the others,
+    activation as gemm_bf16_epilogue's.  Returns h [m, n], or (h, z) with
+    save_z, z = x w^T in bf16 [m, 2 n] for the backward pass."""
+    act = ACTIVATIONS[activation]
+    ldx = _rows(x, torch.bfloat16, "x")
+    m, k = x.shape
+    n = _gated_weights(w, k, 0)
+    out, ldh, code = _out_rows(out, (m, n), out_dtype, x)
+    z = x.new_empty((m, 2 * n)) if save_z else None
+    L = lib()
+    stream = _stream_of(x)
+    if workspace is None:
+        workspace, ws, ws_bytes = _workspace_of(L.fg8_gemm_bf16_gated_workspace_bytes(m, n, k), x, stream)
+    else:
+        ws, ws_bytes = _workspace_given(workspace)
+    _check(L.gemm_bf16_gated(x.data_ptr(), ldx, w.data_ptr(), act, z.data_ptr() if save_z else None,
+                             out.data_ptr(), ldh, code, m, n, k, ws, ws_bytes, stream))
+    return (out, z) if save_z else out
+
+
+def grouped_gemm_bf16_gated(x, w, row_offsets, activation="silu", save_z=False,
+                            out_dtype=torch.bfloat16, out=None):
+    """gemm_bf16_gated over ragged row runs, as grouped_gemm_bf16: w bf16
+    [E, 2 n, k], row_offsets int32 [E + 1] (device); rows of no run are zeros
+    (of z too)."""
+    act = ACTIVATIONS[activation]
+    ldx = _rows(x, torch.bfloat16, "x")
+    rows, k = x.shape
+    n = _gated_weights(w, k, 1)
+    E = _run_offsets(w, row_offsets)
+    out, ldh, code = _out_rows(out, (rows, n), out_dtype, x)
+    z = x.new_empty((rows, 2 * n)) if save_z else None
+    _check(lib().grouped_gemm_bf16_gated(x.data_ptr(), ldx, w.data_ptr(), row_offsets.data_ptr(), act,
+                                         z.data_ptr() if save_z else None, out.data_ptr(), ldh, code,
+                                         rows, n, k, E, _stream_of(x)))
+    return (out, z) if save_z else out
+
+
+def _gated_backward_args(dh, x, w, z, n):
+    lddh, ldx = _rows(dh, torch.bfloat16, "dh"), _rows(x, torch.bfloat16, "x")
+    _dev(z, torch.bfloat16, "z")
+    if dh.shape != (x.shape[0], n) or z.shape != (x.shape[0], 2 * n):
+        raise ValueError("dh must be [m, n] and z [m, 2 n]")
+    return lddh, ldx
+
+
+def gemm_bf16_gated_backward(dh, x, w, z, activation="silu", dw_dtype=torch.bfloat16,
+                             needs=(True, True), workspace=None):
+    """Gradients of gemm_bf16_gated: dh bf16 [m, n], x, w and z as the forward
+    pass had and saved them -> (dx bf16 [m, k], dw dw_dtype [2 n, k]); `needs`
+    leaves out (None) what is not wanted.  dx and a bfloat16 dw take dz rounded
+    to bfloat16, a float32 dw to 2^-16 (a second product)."""
+    act = ACTIVATIONS[activation]
+    m, k = x.shape
+    n = _gated_weights(w, k, 0)
+    lddh, ldx = _gated_backward_args(dh, x, w, z, n)
+    dx = x.new_empty((m, k)) if needs[0] else None
+    dw = w.new_empty(w.shape, dtype=dw_dtype) if needs[1] else None
+    if m == 0:     # sums over no rows
+        return dx, dw if dw is None else dw.zero_()
+    L = lib()
+    stream = _stream_of(x)
+    if workspace is None:
+        workspace, ws, ws_bytes = _workspace_of(
+            L.fg8_gemm_bf16_gated_backward_workspace_bytes(m, n, k, 0), x, stream)
+    else:
+        ws, ws_bytes = _workspace_given(workspace)
+    _check(L.gemm_bf16_gated_backward(dh.data_ptr(), lddh, x.data_ptr(), ldx, w.data_ptr(), z.data_ptr(),
+                                      act, _ptr(dx), _ptr(dw), _out_code(dw_dtype), m, n, k, ws, ws_bytes,
+                                      stream))
+    return dx, dw
+
+
+def grouped_gemm_bf16_gated_backward(dh, x, w, z, row_offsets, activation="silu",
+                                     dw_dtype=torch.float32, needs=(True, True), workspace=None):
+    """Gradients of grouped_gemm_bf16_gated: dh bf16 [rows, n], z bf16
+    [rows, 2 n] as saved -> (dx bf16 [rows, k], zeros in rows of no run, dw
+    dw_dtype [E, 2 n, k], zeros for an empty run).  The rest as
+    gemm_bf16_gated_backward."""
+    act = ACTIVATIONS[activation]
+    rows, k = x.shape
+    n = _gated_weights(w, k, 1)
+    E = _run_offsets(w, row_offsets)
+    lddh, ldx = _gated_backward_args(dh, x, w, z, n)
+    dx = x.new_empty((rows, k)) if needs[0] else None
+    dw = w.new_empty(w.shape, dtype=dw_dtype) if needs[1] else None
+    if rows == 0:
+        return dx, dw if dw is None else dw.zero_()
+    L = lib()
+    stream = _stream_of(x)
+    if workspace is None:
+        workspace, ws, ws_bytes = _workspace_of(
+            L.fg8_gemm_bf16_gated_backward_workspace_bytes(rows, n, k, E), x, stream)
+    else:
+        ws, ws_bytes = _workspace_given(workspace)
+    _check(L.grouped_gemm_bf16_gated_backward(
+        dh.data_ptr(), lddh, x.data_ptr(), ldx, w.data_ptr(), z.data_ptr(), row_offsets.data_ptr(), act,
+        _ptr(dx), _ptr(dw), _out_code(dw_dtype), rows, n, k, E, ws, ws_bytes, stream))
+    return dx, dw
 
 
 # --------------------------------------------------------------- layer norm

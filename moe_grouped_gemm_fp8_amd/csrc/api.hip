@@ -787,6 +787,186 @@ fg8_status gemm_bf16_epilogue_backward(const uint16_t* dy, int64_t lddy, const u
   return FG8_OK;
 }
 
+}  // extern "C"
+
+// ------------------------------------------------------- gated products
+namespace {
+
+fg8::BfProblem gated_bf16(int64_t m, int64_t n, int64_t k) {
+  fg8::BfProblem p = dense_bf16(m, 2 * n, k, false, false);
+  p.gated = 1;
+  return p;
+}
+
+// gemm_bf16_gated_backward's workspace, and that of the row runs' (whose
+// products take no splits): as backward_space's, dz of 2 n columns.
+BackwardSpace gated_space(int64_t m, int64_t n, int64_t k, bool runs) {
+  BackwardSpace s{};
+  s.products = fg8::kSplitKCounterBytes;
+  if (!runs) {
+    const int cus = fg8::device_cu_count();
+    const size_t dx = fg8::bf16_workspace_bytes(dense_bf16(m, k, 2 * n, false, true), cus);
+    const size_t dw = fg8::bf16_workspace_bytes(dense_bf16(2 * n, k, m, true, true), cus);
+    if (dx > s.products) s.products = dx;
+    if (dw > s.products) s.products = dw;
+  }
+  s.ldz = up(2 * n, 8);
+  s.dz = s.products;
+  s.total = s.dz + (size_t)m * s.ldz * 2;
+  return s;
+}
+
+// sizes and activation of a gated call
+fg8_status check_gated(const char* fn, int64_t n, int64_t k, fg8_activation activation) {
+  if (fg8_status s = check_nk(fn, n, false, k)) return s;
+  if (2 * n > kMaxLd || k > kMaxLd)
+    return fail(FG8_EUNSUPPORTED, "%s: 2 n=%lld and k=%lld must not exceed %lld", fn, (long long)(2 * n), (long long)k,
+                (long long)kMaxLd);
+  if ((int)activation < FG8_ACT_NONE || (int)activation > FG8_ACT_GELU)
+    return fail(FG8_EINVAL, "%s: unknown activation %d", fn, (int)activation);
+  return FG8_OK;
+}
+
+fg8_status gated_forward(const char* fn, const uint16_t* x, int64_t ldx, const uint16_t* w, fg8_activation activation,
+                         uint16_t* z, void* h, int64_t ldh, fg8_out out, int64_t m, int64_t n, int64_t k,
+                         const int32_t* offsets, int32_t num_experts, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream) {
+  FG8_CHECK_PTR(x);
+  FG8_CHECK_PTR(w);
+  FG8_CHECK_PTR(h);
+  if (z) FG8_CHECK_PTR(z);
+  FG8_CHECK_LD(ldx, k, 8);
+  FG8_CHECK_LD(ldh, n, 1);
+  fg8::BfProblem p = gated_bf16(m, n, k);
+  p.a = x; p.lda = ldx; p.b = w; p.ldb = k; p.d = h; p.ldd = ldh;
+  p.out_bf16 = out == FG8_OUT_BF16;
+  p.act = (int)activation; p.z = z; p.ldz = 2 * n;
+  if (num_experts) {
+    FG8_CHECK_PTR(offsets);
+    p.mode = fg8::kBfRowRuns;
+    p.b_stride = 2 * n * k;
+    p.groups = num_experts; p.offsets = offsets;
+  } else if (fg8_status s = set_workspace(p, fn, workspace, workspace_bytes,
+                                          fg8::bf16_workspace_bytes(p, fg8::device_cu_count()))) {
+    return s;
+  }
+  return run_bf16(p, fn, stream);
+}
+
+fg8_status gated_backward(const char* fn, const uint16_t* dh, int64_t lddh, const uint16_t* x, int64_t ldx,
+                          const uint16_t* w, const uint16_t* z, fg8_activation activation, uint16_t* dx, void* dw,
+                          fg8_out dw_out, int64_t m, int64_t n, int64_t k, const int32_t* offsets, int32_t num_experts,
+                          void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  FG8_CHECK_PTR(dh);
+  FG8_CHECK_PTR(z);
+  FG8_CHECK_LD(lddh, n, 1);
+  if (dx) {
+    FG8_CHECK_PTR(dx);
+    FG8_CHECK_PTR(w);
+  }
+  if (dw) {
+    FG8_CHECK_PTR(dw);
+    FG8_CHECK_PTR(x);
+    FG8_CHECK_LD(ldx, k, 8);
+  }
+  if (!dx && !dw) return fail(FG8_EINVAL, "%s: no output", fn);
+  const BackwardSpace here = gated_space(m, n, k, num_experts != 0);
+  fg8::BfProblem p = dense_bf16(m, k, 2 * n, false, true), q = dense_bf16(2 * n, k, m, true, true);
+  if (fg8_status e = set_workspace(p, fn, workspace, workspace_bytes, here.total)) return e;
+  q.counters = p.counters; q.partial = p.partial;
+  uint16_t* dz = (uint16_t*)((char*)workspace + here.dz);
+  p.a = dz; p.lda = here.ldz; p.b = w; p.ldb = k; p.d = dx; p.ldd = k; p.out_bf16 = 1;
+  q.a = dz; q.lda = here.ldz; q.b = x; q.ldb = ldx; q.d = dw; q.ldd = k; q.out_bf16 = dw_out == FG8_OUT_BF16;
+  if (num_experts) {
+    FG8_CHECK_PTR(offsets);
+    p.mode = fg8::kBfRowRuns; q.mode = fg8::kBfKRuns;
+    p.b_stride = q.d_stride = 2 * n * k;
+    p.groups = q.groups = num_experts;
+    p.offsets = q.offsets = offsets;
+  }
+  // A float dw takes dz in two BF16 parts, as gemm_bf16_epilogue_backward's does.
+  for (int part = 0; part < (dw && !q.out_bf16 ? 2 : 1); ++part) {
+    const hipError_t e = fg8::launch_gated_backward(dh, lddh, z, (int)activation, m, n, part == 1, dz, here.ldz, stream);
+    if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+    if (dx && part == 0)
+      if (fg8_status r = run_bf16(p, fn, stream)) return r;
+    if (dw) {
+      q.add = part;
+      if (fg8_status r = run_bf16(q, fn, stream)) return r;
+    }
+  }
+  g_err[0] = 0;
+  return FG8_OK;
+}
+
+fg8_status check_m(const char* fn, int64_t m, int64_t least) {
+  if (m < least || m >= kMaxDim) return fail(FG8_EINVAL, "%s: m=%lld", fn, (long long)m);
+  if (m > kMaxRows) return fail(FG8_EUNSUPPORTED, "%s: m=%lld exceeds %lld", fn, (long long)m, (long long)kMaxRows);
+  return FG8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fg8_gemm_bf16_gated_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m < 1 || n < 1 || k < 1 || m >= kMaxDim || n >= kMaxDim / 2 || k >= kMaxDim) return 0;
+  return fg8::bf16_workspace_bytes(gated_bf16(m, n, k), fg8::device_cu_count());
+}
+
+fg8_status gemm_bf16_gated(const uint16_t* x, int64_t ldx, const uint16_t* w, fg8_activation activation, uint16_t* z,
+                           void* h, int64_t ldh, fg8_out out, int64_t m, int64_t n, int64_t k, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+  const char* fn = "gemm_bf16_gated";
+  if (fg8_status s = check_m(fn, m, 0)) return s;
+  if (fg8_status s = check_gated(fn, n, k, activation)) return s;
+  if (fg8_status s = check_out(fn, out)) return s;
+  if (m == 0) return FG8_OK;
+  return gated_forward(fn, x, ldx, w, activation, z, h, ldh, out, m, n, k, nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+fg8_status grouped_gemm_bf16_gated(const uint16_t* x, int64_t ldx, const uint16_t* w, const int32_t* row_offsets,
+                                   fg8_activation activation, uint16_t* z, void* h, int64_t ldh, fg8_out out,
+                                   int64_t rows, int64_t n, int64_t k, int32_t num_experts, hipStream_t stream) {
+  const char* fn = "grouped_gemm_bf16_gated";
+  if (fg8_status s = check_runs(fn, rows, num_experts)) return s;
+  if (fg8_status s = check_gated(fn, n, k, activation)) return s;
+  if (fg8_status s = check_out(fn, out)) return s;
+  if (rows == 0) return FG8_OK;
+  return gated_forward(fn, x, ldx, w, activation, z, h, ldh, out, rows, n, k, row_offsets, num_experts, nullptr, 0, stream);
+}
+
+size_t fg8_gemm_bf16_gated_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t num_experts) {
+  if (m < 1 || n < 1 || k < 1 || m >= kMaxDim || n >= kMaxDim / 2 || k >= kMaxDim) return 0;
+  return gated_space(m, n, k, num_experts != 0).total;
+}
+
+fg8_status gemm_bf16_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* x, int64_t ldx, const uint16_t* w,
+                                    const uint16_t* z, fg8_activation activation, uint16_t* dx, void* dw, fg8_out dw_out,
+                                    int64_t m, int64_t n, int64_t k, void* workspace, size_t workspace_bytes,
+                                    hipStream_t stream) {
+  const char* fn = "gemm_bf16_gated_backward";
+  if (fg8_status s = check_m(fn, m, 1)) return s;
+  if (fg8_status s = check_gated(fn, n, k, activation)) return s;
+  if (fg8_status s = check_out(fn, dw_out)) return s;
+  return gated_backward(fn, dh, lddh, x, ldx, w, z, activation, dx, dw, dw_out, m, n, k, nullptr, 0, workspace,
+                        workspace_bytes, stream);
+}
+
+fg8_status grouped_gemm_bf16_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* x, int64_t ldx,
+                                            const uint16_t* w, const uint16_t* z, const int32_t* row_offsets,
+                                            fg8_activation activation, uint16_t* dx, void* dw, fg8_out dw_out,
+                                            int64_t rows, int64_t n, int64_t k, int32_t num_experts, void* workspace,
+                                            size_t workspace_bytes, hipStream_t stream) {
+  const char* fn = "grouped_gemm_bf16_gated_backward";
+  if (fg8_status s = check_runs(fn, rows, num_experts)) return s;
+  if (rows < 1) return fail(FG8_EINVAL, "%s: rows=%lld", fn, (long long)rows);
+  if (fg8_status s = check_gated(fn, n, k, activation)) return s;
+  if (fg8_status s = check_out(fn, dw_out)) return s;
+  return gated_backward(fn, dh, lddh, x, ldx, w, z, activation, dx, dw, dw_out, rows, n, k, row_offsets, num_experts,
+                        workspace, workspace_bytes, stream);
+}
+
 fg8_status fg8_bf16_tile_choice(int32_t product, int64_t m, int64_t n, int64_t k, int32_t groups,
                                 int32_t num_cus, int32_t* out) {
   const char* fn = "fg8_bf16_tile_choice";

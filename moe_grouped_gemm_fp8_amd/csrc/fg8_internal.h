@@ -106,7 +106,8 @@ struct BfProblem {
   int64_t ldr;
   uint16_t* z;                  // the value before the activation, BF16
   int64_t ldz;
-  int add;                      // dense, both operands k-major, FP32: D += the product
+  int add;                      // both operands k-major, FP32: D += the product
+  int gated;                    // B, both k-contiguous: N / 2 gate rows over N / 2 up rows; D and z as GatedOut
   int grid;                     // workgroups of a persistent launch (set by the launcher)
   // split k (dense)
   int splits;
@@ -131,6 +132,11 @@ int act_backward_chunks(int64_t m, int64_t n);
 hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldzin,
                                int act, int64_t m, int64_t n, bool rest, uint16_t* dz, int64_t ldz,
                                float* partial, float* dbias, hipStream_t stream);
+
+// dz [m][ldz] of h = act(z_gate) z_up, z [m][2 n] gate half first: dh z_up
+// act'(z_gate), then dh act(z_gate), then zeros up to ldz.  rest: as above.
+hipError_t launch_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* z, int act, int64_t m,
+                                 int64_t n, bool rest, uint16_t* dz, int64_t ldz, hipStream_t stream);
 
 // --------------------------------------------------------------- layer norm
 int64_t layer_norm_teams(int64_t rows, int64_t cols, bool bf16, int num_cus);

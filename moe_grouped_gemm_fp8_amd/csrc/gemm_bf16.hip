@@ -12,6 +12,10 @@
 //                   D belonging to expert e, whose B is b + e * b_stride
 //   k runs          the third, k (a token row) off[e] .. off[e + 1] - 1
 //                   belonging to expert e, whose D is d + e * d_stride
+// and the gated form of the first one, dense or over row runs: B is 2 n rows,
+// gate rows over up rows, D[m][j] = act(sum of gate row j) * (sum of up row j).
+// A tile's columns are then half gate rows, half the up rows of the same j, laid
+// so that one wave holds both sums of its columns.
 //
 // An operand tile of one 64-deep k step is copied from global memory straight
 // into LDS (16 bytes a lane, no staging registers).  The copies go through a
@@ -171,6 +175,56 @@ struct Operand {
       return *reinterpret_cast<const v8bf*>(tile + r * PITCH + (((g + 4 * kk) ^ chunk_xor(r)) << 4));
     }
   }
+};
+
+// B's tile of a gated product (k-contiguous): the columns that a wave owns, WN of
+// the tile's BX, are WN / 2 gate rows and then the up rows of the same columns of
+// h.  A copy of 1 KB lies in one of the two.
+template <int BX, int WN, int WAVES, int DEPTH>
+struct GatedOperand {
+  typedef Operand<false, BX, WAVES, DEPTH> Plain;
+  static constexpr int COPIES = Plain::COPIES, PER = Plain::PER, PITCH = Plain::PITCH, HALF = WN / 2;
+  static constexpr bool EVEN = Plain::EVEN;
+  static_assert(HALF % (1024 / PITCH) == 0, "a copy's rows are all gate or all up");
+
+  const char* base;      // gate row j0 at the first k
+  int64_t up;            // bytes from there to up row j0
+  int64_t left;          // bytes of either's rows before the last one
+  uint32_t off[PER];
+  int rem_k;
+
+  __device__ static bool is_up(int copy) { return copy * (1024 / PITCH) % WN >= HALF; }
+
+  // j0: the tile's first column of h; js: columns from there (>= 1) of n
+  __device__ void init(const uint16_t* p, int64_t ld_elems, int64_t j0, int js, int64_t n, int64_t k0, int ks,
+                       int wave, int lane) {
+    const int64_t ld = ld_elems * 2;
+    rem_k = ks;
+    base = (const char*)(p + j0 * ld_elems + k0);
+    up = n * ld;
+    left = (int64_t)((js < BX / 2 ? js : BX / 2) - 1) * ld;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int at = (wave + i * WAVES) * 1024 + lane * 16;
+      const int r = at / PITCH, c = (at % PITCH / 16) ^ Plain::chunk_xor(r);
+      off[i] = (uint32_t)((r / WN * HALF + r % HALF) * ld) + c * 16;
+    }
+  }
+  __device__ void issue(int kt, uint32_t lds, int wave, int lane) const {
+    const int rem = rem_k - kt * DEPTH;
+    const char* from = base + (int64_t)kt * (DEPTH * 2);
+    const int64_t bytes = left + (int64_t)((rem + 7) & ~7) * 2;
+    const v4i gate = resource(from, bytes), above = resource(from + up, bytes);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (EVEN || wave + i * WAVES < COPIES) {
+        const int at = (wave + i * WAVES) * 1024 + lane * 16;
+        const int c = (at % PITCH / 16) ^ Plain::chunk_xor(at / PITCH);
+        copy16(is_up(wave + i * WAVES) ? above : gate, c * 8 < rem ? off[i] : kNowhere,
+               uniform(lds + (uint32_t)(wave + i * WAVES) * 1024));
+      }
+  }
+  __device__ static v8bf frag(const uint8_t* tile, int x, int kk, int lane) { return Plain::frag(tile, x, kk, lane); }
 };
 
 // ------------------------------------------------------------ work units
@@ -611,6 +665,83 @@ struct TileOut {
   }
 };
 
+// Sixteen rows x 32 columns as BF16 (1 KB of LDS) -> four lanes a row, 64 bytes.
+// ld8: to and ld are whole 16-byte pieces.
+__device__ __forceinline__ void store_bf16_half_rows(uint8_t* turn, v4f a, v4f b, uint16_t* to, int64_t ld, bool ld8,
+                                                     int rows, int n, int N, int lane, bool whole) {
+  const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const v4f v = t ? b : a;
+    *reinterpret_cast<uint2*>(turn + i * 64 + (((2 * t + (g >> 1)) ^ (i >> 2)) << 4) + (g & 1) * 8) =
+        make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+  }
+  const int r = lane >> 2, c = lane & 3;
+  const uint4 u = *reinterpret_cast<const uint4*>(turn + r * 64 + ((c ^ (r >> 2)) << 4));
+  if (whole || r < rows) store_eight(to + r * ld, ld8 ? 8 : 1, n + 8 * c, N, whole && ld8, u);
+}
+
+// One unit's output of a gated product: a wave holds the gate and the up sums of
+// the same 16 COLS columns of h.  z is taken before the activation, h from the
+// FP32 sums.
+template <int COLS>
+struct GatedOut {
+  static constexpr int kTurn = 2048;                 // LDS of a wave
+  const BfProblem& p;
+  uint8_t* turn;
+  int64_t m0;
+  int rows, j, n, lane;      // rows of D from m0 on; the wave's first column, of n
+  bool whole, z8, h8;
+  __device__ GatedOut(const BfProblem& q, const BfUnit& w, int bm, int bn, int wave_n, uint8_t* t, int l)
+      : p(q), turn(t), m0(w.m0), rows(w.rows), j((w.n0 + wave_n) / 2), n(p.N / 2), lane(l) {
+    whole = w.rows >= bm && w.n0 + bn <= p.N;
+    z8 = n % 8 == 0 && p.ldz % 8 == 0;               // (the up half of z starts at column n)
+    h8 = p.ldd % (p.out_bf16 ? 8 : 4) == 0;
+  }
+  // rows r .. r + 15 of the tile
+  __device__ void rows16(int r, v4f (&gate)[COLS], v4f (&up)[COLS]) const {
+    const int64_t m = m0 + r;
+    if (p.z) {
+      put(true, p.z + m * p.ldz, p.ldz, z8, r, gate);
+      put(true, p.z + m * p.ldz + n, p.ldz, z8, r, up);
+    }
+    activate(p.act, gate);
+#pragma unroll
+    for (int t = 0; t < COLS; ++t) gate[t] *= up[t];
+    put(p.out_bf16, (char*)p.d + m * p.ldd * (p.out_bf16 ? 2 : 4), p.ldd, h8, r, gate);
+  }
+  __device__ void put(bool bf16, void* to, int64_t ld, bool pieces, int r, const v4f (&v)[COLS]) const {
+    if constexpr (COLS == 2) {
+      if (bf16) store_bf16_half_rows(turn, v[0], v[1], (uint16_t*)to, ld, pieces, rows - r, j, n, lane, whole);
+      else store_f32_rows<false>(turn, v[0], v[1], (float*)to, ld, rows - r, j, n, lane, whole && pieces);
+    } else if (r + (lane & 15) < rows) {
+      // (sixteen columns: four a lane, straight from the registers)
+      const int c = j + 4 * (lane >> 4), row = lane & 15;
+      const bool four = pieces && c + 4 <= n;
+      if (bf16) {
+        uint16_t* q = (uint16_t*)to + row * ld + c;
+        const uint32_t w[2] = {bf16x2(v[0][0], v[0][1]), bf16x2(v[0][2], v[0][3])};
+        if (four) {
+          *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i < n) q[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+        }
+      } else {
+        float* q = (float*)to + row * ld + c;
+        if (four) {
+          *reinterpret_cast<v4f*>(q) = v[0];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i < n) q[i] = v[0][i];
+        }
+      }
+    }
+  }
+};
+
 // ---------------------------------------------------------------- split k
 // Every split publishes its FP32 tile past the caches of its XCD and counts
 // itself in; the last one to arrive adds them up in the order of the splits
@@ -627,7 +758,7 @@ __device__ __forceinline__ bool last_of_splits(const BfProblem& p, const BfUnit&
   return *last;
 }
 // ------------------------------------------------------------------ kernel
-template <class C, bool AK, bool BK, int MODE, bool ADD = false>
+template <class C, bool AK, bool BK, int MODE, bool ADD = false, bool GATED = false>
 __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::STAGES * C::STAGE_BYTES];
   __shared__ int last;
@@ -645,11 +776,14 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
   const int steps = (w.ks + C::DEPTH - 1) / C::DEPTH;
   if (steps > 0) {
     typedef Operand<AK, C::BM, C::WAVES, C::DEPTH> OpA;
-    typedef Operand<BK, C::BN, C::WAVES, C::DEPTH> OpB;
+    typedef std::conditional_t<GATED, GatedOperand<C::BN, C::WN, C::WAVES, C::DEPTH>,
+                               Operand<BK, C::BN, C::WAVES, C::DEPTH>> OpB;
     OpA a;
     OpB b;
     a.init(p.a, p.lda, w.m0, w.rows, w.k0, w.ks, wave, lane);
-    b.init(p.b + (MODE == kBfRowRuns ? w.g * p.b_stride : 0), p.ldb, w.n0, p.N - w.n0, w.k0, w.ks, wave, lane);
+    const uint16_t* pb = p.b + (MODE == kBfRowRuns ? w.g * p.b_stride : 0);
+    if constexpr (GATED) b.init(pb, p.ldb, w.n0 / 2, (p.N - w.n0) / 2, p.N / 2, w.k0, w.ks, wave, lane);
+    else b.init(pb, p.ldb, w.n0, p.N - w.n0, w.k0, w.ks, wave, lane);
     const uint32_t lds0 = lds_addr(smem);
     auto issue = [&](int kt) {
       const uint32_t st = uniform(lds0 + (uint32_t)(kt % C::STAGES * C::STAGE_BYTES));
@@ -720,7 +854,23 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
     }
   }
 
-  if constexpr (C::WN == 64) {
+  if constexpr (GATED) {
+    constexpr int COLS = C::TN / 2;
+    typedef GatedOut<COLS> Out;
+    static_assert(C::WAVES * Out::kTurn <= C::STAGES * C::STAGE_BYTES, "rows turn in the stages");
+    __syncthreads();      // every wave is done with the stages
+    const Out out(p, w, C::BM, C::BN, wn0, smem + wave * Out::kTurn, lane);
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i) {
+      v4f gate[COLS], up[COLS];
+#pragma unroll
+      for (int t = 0; t < COLS; ++t) {
+        gate[t] = acc[i][t];
+        up[t] = acc[i][COLS + t];
+      }
+      out.rows16(wm0 + 16 * i, gate, up);
+    }
+  } else if constexpr (C::WN == 64) {
     constexpr bool EPI = MODE == kBfDense && !AK && !BK;
     typedef TileOut<EPI, ADD> Out;
     static_assert(C::WAVES * Out::kTurn <= C::STAGES * C::STAGE_BYTES, "rows turn in the stages");
@@ -756,26 +906,29 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
 // 5.5 us for the 6.6 of the thin tile.  A load of this shape touches 16 lines
 // for 1 KB where a copy into LDS touches 8, so longer k go the other way:
 // 16 x 2112 x 7168 19 us for 11.)
-template <int MODE>
+template <int MODE, bool GATED = false>
 __global__ __launch_bounds__(512, 2) void bf16_few_kernel(BfProblem p) {
-  constexpr int U = 4;       // steps of a batch; two batches in flight
-  __shared__ v4f sums[8][64];
+  constexpr int U = GATED ? 3 : 4;       // steps of a batch; two batches in flight
+  constexpr int SETS = GATED ? 2 : 1;    // rows of B for a column: gate and up
+  __shared__ v4f sums[8][SETS][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   BfUnit w;
-  if (!find_unit<16, 16, MODE>(p, lane, w)) return;
+  if (!find_unit<16, 16 * SETS, MODE>(p, lane, w)) return;
   const int i = lane & 15, g = lane >> 4;
+  const int n0 = w.n0 / SETS, N = p.N / SETS;
 
   // Offsets of a lane's row in either tile; rows and columns past the end read
   // the last one and are not stored.  k goes into the scalar offset, and a
   // lane whose k lies past the end loads zeros.
   const uint16_t* xp = p.a + w.m0 * p.lda;
-  const uint16_t* wp = p.b + (MODE == kBfRowRuns ? max(w.g, 0) * p.b_stride : 0) + (int64_t)w.n0 * p.ldb;
+  const uint16_t* wp = p.b + (MODE == kBfRowRuns ? max(w.g, 0) * p.b_stride : 0) + (int64_t)n0 * p.ldb;
   const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(uniform((const void*)xp), 0x7fffffff);
   const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(uniform((const void*)wp), 0x7fffffff);
   const uint32_t xo = (uint32_t)(min(i, w.rows - 1) * (int)p.lda + 8 * g) * 2;
-  const uint32_t wo = (uint32_t)(min(i, p.N - 1 - w.n0) * (int)p.ldb + 8 * g) * 2;
+  const __amdgpu_buffer_rsrc_t ur = buffer_rsrc(uniform((const void*)(wp + (int64_t)N * p.ldb)), 0x7fffffff);
+  const uint32_t wo = (uint32_t)(min(i, N - 1 - n0) * (int)p.ldb + 8 * g) * 2;
   struct Batch {
-    v4i x[U][2], w[U][2];
+    v4i x[U][2], w[SETS][U][2];
   };
   auto fetch = [&](Batch& f, int s0) {     // steps s0, s0 + 8, ..
 #pragma unroll
@@ -784,19 +937,25 @@ __global__ __launch_bounds__(512, 2) void bf16_few_kernel(BfProblem p) {
       for (int kk = 0; kk < 2; ++kk) {
         const int k = uniform((s0 + 8 * u) * kBK + 32 * kk);
         const bool in = 8 * g < w.ks - k;
-        f.w[u][kk] = __builtin_bit_cast(
-            v4i, __builtin_amdgcn_raw_buffer_load_b128(wr, in ? wo : kNowhere, k * 2, kStream));
+#pragma unroll
+        for (int s = 0; s < SETS; ++s)
+          f.w[s][u][kk] = __builtin_bit_cast(
+              v4i, __builtin_amdgcn_raw_buffer_load_b128(s ? ur : wr, in ? wo : kNowhere, k * 2, kStream));
         f.x[u][kk] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(xr, in ? xo : kNowhere, k * 2, 0));
       }
   };
-  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  v4f acc[SETS];
+#pragma unroll
+  for (int s = 0; s < SETS; ++s) acc[s] = v4f{0.f, 0.f, 0.f, 0.f};
   auto multiply = [&](const Batch& f) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, f.w[u][kk]),
-                                                      __builtin_bit_cast(v8bf, f.x[u][kk]), acc, 0, 0, 0);
+#pragma unroll
+        for (int s = 0; s < SETS; ++s)
+          acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, f.w[s][u][kk]),
+                                                           __builtin_bit_cast(v8bf, f.x[u][kk]), acc[s], 0, 0, 0);
   };
   const int steps = (w.ks + kBK - 1) / kBK;
   if (wave < steps) {
@@ -810,13 +969,19 @@ __global__ __launch_bounds__(512, 2) void bf16_few_kernel(BfProblem p) {
       multiply(f1);
     }
   }
-  sums[wave][lane] = acc;
-  __syncthreads();
-  if (wave == 0 && i < w.rows) {
-    v4f sum = sums[0][lane];
 #pragma unroll
-    for (int v = 1; v < 8; ++v) sum += sums[v][lane];
-    BfOut(p, w.g).four(w.m0 + i, w.n0 + 4 * g, sum);
+  for (int s = 0; s < SETS; ++s) sums[wave][s][lane] = acc[s];
+  __syncthreads();
+  if (wave == 0) {
+    v4f sum[SETS][1];
+#pragma unroll
+    for (int s = 0; s < SETS; ++s) {
+      sum[s][0] = sums[0][s][lane];
+#pragma unroll
+      for (int v = 1; v < 8; ++v) sum[s][0] += sums[v][s][lane];
+    }
+    if constexpr (GATED) GatedOut<1>(p, w, 16, 32, 0, nullptr, lane).rows16(0, sum[0], sum[1]);
+    else if (i < w.rows) BfOut(p, w.g).four(w.m0 + i, w.n0 + 4 * g, sum[0][0]);
   }
 }
 
@@ -880,6 +1045,43 @@ struct HalfTile {
   }
 };
 
+// B's halves of a gated product: half 0 is 128 gate rows, half 1 the up rows of
+// the same columns of h, so that a wave's two halves are both sums of its columns.
+struct GatedHalf {
+  typedef HalfTile<false, 32> Plain;
+  typedef Plain::Frag Frag;
+  static constexpr int BYTES = Plain::BYTES, COPIES = Plain::COPIES, PITCH = Plain::PITCH;
+
+  const char* base;            // gate row j0 at the first k
+  int64_t up, left;            // bytes to up row j0; of either's rows before the last one
+  uint32_t off[COPIES];
+  int rem_k;
+
+  __device__ void init(const uint16_t* p, int64_t ld_elems, int64_t j0, int js, int64_t n, int64_t k0, int ks,
+                       int wave, int lane) {
+    const int64_t ld = ld_elems * 2;
+    rem_k = ks;
+    base = (const char*)(p + j0 * ld_elems + k0);
+    up = n * ld;
+    left = (int64_t)((js < 128 ? js : 128) - 1) * ld;
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) {
+      const int at = (wave * COPIES + i) * 1024 + lane * 16, r = at / PITCH;
+      off[i] = (uint32_t)(r * ld) + (((at % PITCH / 16) ^ swz(r)) << 4);
+    }
+  }
+  __device__ void issue(int kt, int h, uint32_t lds, int wave, int lane) const {
+    const int rem = rem_k - kt * kBK;
+    const int64_t bytes = left + (int64_t)((rem + 7) & ~7) * 2;
+    const v4i rs = resource(base + (h ? up : 0) + (int64_t)kt * (kBK * 2), rem > 0 ? bytes : 0);
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) {
+      const int c = (lane & 7) ^ (4 * i + (lane >> 4));
+      copy16(rs, c * 8 < rem ? off[i] : kNowhere, uniform(lds + (uint32_t)(wave * COPIES + i) * 1024));
+    }
+  }
+};
+
 // A copy of a per-lane value that the compiler cannot trace: what is computed
 // from it is computed here, not before the loop over units, where it would
 // take registers through the main loop.
@@ -932,11 +1134,11 @@ __device__ __forceinline__ void phase_barrier() {
 // take 0.31: the two add up whatever the order of the tiles (experts mixed over
 // the XCDs, other numbers of tiles together on one, staggered starts and two
 // workgroups a CU measured within 2% or slower).
-template <bool AK, bool BK, int MODE, bool EPI, bool ADD = false>
+template <bool AK, bool BK, int MODE, bool EPI, bool ADD = false, bool GATED = false>
 __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
   typedef HalfTile<AK, 64> HalfA;
-  typedef HalfTile<BK, 32> HalfB;
-  typedef TileOut<EPI, ADD> Out;
+  typedef std::conditional_t<GATED, GatedHalf, HalfTile<BK, 32>> HalfB;
+  typedef std::conditional_t<GATED, GatedOut<2>, TileOut<EPI, ADD>> Out;
   constexpr uint32_t kHalf = HalfA::BYTES;         // LDS: per stage A0, A1, B0, B1
   constexpr uint32_t kTurns = 8 * kHalf, kTable = kTurns + 8 * Out::kTurn;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kTable + (MODE == kBfRowRuns ? sizeof(RunTable) : 0)];
@@ -989,7 +1191,9 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
   auto start = [&](const BfUnit& w) {     // a unit's first five halves
     const int here = opaque(lane);
     a.init(p.a, p.lda, w.m0, w.rows, w.k0, w.ks, wave, here);
-    b.init(p.b + (MODE == kBfRowRuns ? w.g * p.b_stride : 0), p.ldb, w.n0, p.N - w.n0, w.k0, w.ks, wave, here);
+    const uint16_t* pb = p.b + (MODE == kBfRowRuns ? w.g * p.b_stride : 0);
+    if constexpr (GATED) b.init(pb, p.ldb, w.n0 / 2, (p.N - w.n0) / 2, p.N / 2, w.k0, w.ks, wave, here);
+    else b.init(pb, p.ldb, w.n0, p.N - w.n0, w.k0, w.ks, wave, here);
     copy_a(0, 0);
     copy_b(0, 0);
     copy_b(0, 1);
@@ -1099,8 +1303,13 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
         if (g < 7) out.residual(grp * 128 + 16 * (g + 1), ahead);
       }
       const int ha = g / 4, i = g % 4;
-      v4f v[4] = {acc[ha][i][0][0], acc[ha][i][0][1], acc[ha][i][1][0], acc[ha][i][1][1]};
-      out.rows16(grp * 128 + 16 * g, v, res);
+      if constexpr (GATED) {
+        v4f gate[2] = {acc[ha][i][0][0], acc[ha][i][0][1]}, up[2] = {acc[ha][i][1][0], acc[ha][i][1][1]};
+        out.rows16(grp * 128 + 16 * g, gate, up);
+      } else {
+        v4f v[4] = {acc[ha][i][0][0], acc[ha][i][0][1], acc[ha][i][1][0], acc[ha][i][1][1]};
+        out.rows16(grp * 128 + 16 * g, v, res);
+      }
       if constexpr (EPI) {
         res[0] = ahead[0];
         res[1] = ahead[1];
@@ -1145,6 +1354,20 @@ hipError_t start(K kernel, const BfProblem& p, unsigned grid, int threads, hipSt
   return hipGetLastError();
 }
 
+// The gated products.
+template <int MODE>
+hipError_t launch_gated(BfProblem p, const BfTile& t, hipStream_t stream) {
+  const unsigned units = grid_of(p, t.bm, t.bn);
+  if (t.cfg == kFew) return start(bf16_few_kernel<MODE, true>, p, units, 512, stream);
+  if (t.cfg == kFlat) return start(bf16_kernel<BfFlat, false, false, MODE, false, true>, p, units, BfFlat::THREADS, stream);
+  if (t.cfg == kLow) return start(bf16_kernel<BfLow, false, false, MODE, false, true>, p, units, BfLow::THREADS, stream);
+  if (t.cfg == kHigh) return start(bf16_kernel<BfHigh, false, false, MODE, false, true>, p, units, BfHigh::THREADS, stream);
+  if (t.cfg == kMid) return start(bf16_kernel<BfMid, false, false, MODE, false, true>, p, units, BfMid::THREADS, stream);
+  const unsigned cus = (unsigned)device_cu_count();
+  p.grid = (int)(units < cus ? units : cus);
+  return start(bf16_big_kernel<false, false, MODE, false, false, true>, p, p.grid, 512, stream);
+}
+
 template <bool AK, bool BK, int MODE>
 hipError_t launch_tile(BfProblem p, const BfTile& t, hipStream_t stream) {
   const unsigned units = grid_of(p, t.bm, t.bn);
@@ -1158,10 +1381,16 @@ hipError_t launch_tile(BfProblem p, const BfTile& t, hipStream_t stream) {
     if (t.cfg == kHigh) return start(bf16_kernel<BfHigh, AK, BK, MODE>, p, units, BfHigh::THREADS, stream);
   }
   if constexpr (MODE == kBfKRuns) {
-    if (t.cfg == kDuo) return start(bf16_kernel<BfDuo, AK, BK, MODE>, p, units, BfDuo::THREADS, stream);
+    if (p.add) {
+      if (t.cfg == kDuo) return start(bf16_kernel<BfDuo, AK, BK, MODE, true>, p, units, BfDuo::THREADS, stream);
+      if (t.cfg == kMid) return start(bf16_kernel<BfMid, AK, BK, MODE, true>, p, units, BfMid::THREADS, stream);
+    } else if (t.cfg == kDuo) return start(bf16_kernel<BfDuo, AK, BK, MODE>, p, units, BfDuo::THREADS, stream);
   }
   const unsigned cus = (unsigned)device_cu_count();
   p.grid = (int)(units < cus ? units : cus);
+  if constexpr (MODE == kBfKRuns) {
+    if (p.add) return start(bf16_big_kernel<AK, BK, MODE, false, true>, p, p.grid, 512, stream);
+  }
   if constexpr (MODE == kBfDense && AK && BK) {
     if (p.add)
       return t.cfg == kMid ? start(bf16_kernel<BfMid, AK, BK, MODE, true>, p, units, BfMid::THREADS, stream)
@@ -1182,6 +1411,7 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
   // rows of one tile column: a run's average for the row runs
   const int64_t rows = p.mode == kBfRowRuns ? (p.M + p.groups - 1) / p.groups : p.M;
   const int64_t runs = p.mode == kBfDense ? 1 : p.groups;
+  // (a gated product's N counts gate and up rows)
   auto units = [&](int c) { return runs * ((rows + kBm[c] - 1) / kBm[c]) * (((int64_t)p.N + kBn[c] - 1) / kBn[c]); };
   // (times in us, the choice first; 256 CUs)
   //
@@ -1213,9 +1443,9 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
     // 1024 rows (256, 296) 89 for 82, of 1024 rows, 4096 x 2048 (512, 592) 136
     // for 145.  Runs of whole tiles: 41 for 34, 56 for 65, 104 for 137.
     t.cfg = kBig;
-  } else if (rows <= 8 && !p.b_kmajor && p.K <= 4096 && units(kFew) <= 2 * cus) {
+  } else if (rows <= 8 && !p.b_kmajor && p.K <= 4096 && units(kFew) <= (p.gated ? 4 : 2) * cus) {
     t.cfg = kFew;      // 1 x 1024 x 2048 5.5 for 6.6; 1 x 2112 x 7168 12.8 for 11.2
-  } else if (rows <= (dense ? 16 : 8)) {
+  } else if (rows <= (dense ? 16 : 8) && !p.gated) {   // (its waves own too few columns for both sums)
     t.cfg = kThin;     // 16 x 2112 x 7168 11.3 for 12.2; 32 runs of 16 rows on average 366 for 345
   } else if (rows <= 32) {
     t.cfg = kFlat;     // 32 x 2112 x 7168 12.3 for 13.7
@@ -1226,7 +1456,7 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
     t.cfg = rows <= 256 ? kLow : kHigh;
   }
   t.bm = kBm[t.cfg];
-  t.bn = kBn[t.cfg];
+  t.bn = kBn[t.cfg] * (p.gated && t.cfg == kFew ? 2 : 1);   // (16 gate and 16 up rows)
   t.threads = kThreads[t.cfg];
   t.persistent = t.cfg == kBig;
   t.splits = 1;
@@ -1254,6 +1484,7 @@ size_t bf16_workspace_bytes(const BfProblem& p, int cus) {
 
 hipError_t launch_bf16(BfProblem p, const BfTile& t, hipStream_t stream) {
   p.splits = t.splits;
+  if (p.gated) return p.mode == kBfRowRuns ? launch_gated<kBfRowRuns>(p, t, stream) : launch_gated<kBfDense>(p, t, stream);
   if (p.mode == kBfRowRuns)
     return p.b_kmajor ? launch_tile<false, true, kBfRowRuns>(p, t, stream)
                       : launch_tile<false, false, kBfRowRuns>(p, t, stream);

@@ -553,6 +553,51 @@ __global__ __launch_bounds__(256) void act_backward_kernel(
   }
 }
 
+// act(z)
+__device__ __forceinline__ float act_value(int act, float z) {
+  if (act == kActRelu) return z < 0.f ? 0.f : z;
+  if (act == kActSilu) return z / (1.f + __expf(-z));
+  if (act == kActGelu) {
+    float bell;
+    return z * normal_cdf(z, &bell);
+  }
+  return z;
+}
+
+// The same for h = act(z_gate) z_up.  Bound by HBM: dh and both halves of z
+// read, both halves of dz written.  REST as above.
+template <bool REST>
+__global__ __launch_bounds__(256) void gated_backward_kernel(
+    const uint16_t* __restrict__ dh, int64_t lddh, const uint16_t* __restrict__ z, int act, int64_t m, int64_t n,
+    int64_t per, uint16_t* __restrict__ dz, int64_t ldz) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * kActCols + lane * 8;
+  const int64_t r1 = min((int64_t)(blockIdx.y + 1) * per, m);
+  if (c >= n) return;
+#pragma unroll 2
+  for (int64_t r = blockIdx.y * per + wave; r < r1; r += 4) {
+    float d[8], gate[8], up[8];
+    RowVec<uint16_t>::widen(Piece<uint16_t>::load(dh + r * lddh, c, n), d);
+    RowVec<uint16_t>::widen(Piece<uint16_t>::load(z + r * 2 * n, c, n), gate);
+    RowVec<uint16_t>::widen(Piece<uint16_t>::load(z + r * 2 * n + n, c, n), up);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float g = gate[i];
+      gate[i] = act_gradient(act, g, d[i] * up[i]);
+      up[i] = d[i] * act_value(act, g);
+      if constexpr (REST) {
+        gate[i] = bf16_rest(gate[i]);
+        up[i] = bf16_rest(up[i]);
+      }
+    }
+    uint16_t* row = dz + r * ldz;
+    Piece<uint16_t>::store(row, c, n, gate);
+    Piece<uint16_t>::store(row + n, c, n, up);
+    if (c + 8 >= n)                 // the last columns' lane clears what follows them
+      for (int64_t i = 2 * n; i < ldz; ++i) row[i] = 0;
+  }
+}
+
 }  // namespace
 
 int act_backward_chunks(int64_t m, int64_t n) {
@@ -574,6 +619,16 @@ hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const uint16_t*
   if (dbias)
     hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((n + 63) / 64)), dim3(1024), 0, stream,
                        partial, chunks, n, n, dbias, dbias);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* z, int act, int64_t m,
+                                 int64_t n, bool rest, uint16_t* dz, int64_t ldz, hipStream_t stream) {
+  const int chunks = act_backward_chunks(m, n);
+  const int64_t per = (m + chunks - 1) / chunks;
+  hipLaunchKernelGGL(rest ? gated_backward_kernel<true> : gated_backward_kernel<false>,
+                     dim3((unsigned)((n + kActCols - 1) / kActCols), (unsigned)chunks), dim3(256), 0, stream, dh,
+                     lddh, z, act, m, n, per, dz, ldz);
   return hipGetLastError();
 }
 

@@ -1,6 +1,7 @@
 """Plain float64 forms of what an MoE layer computes around its FP8 products:
-expert products over ragged row runs, the dense product with an epilogue,
-layer norm and the combine step, each with its gradients.  Loops and textbook
+expert products over ragged row runs, the dense product with an epilogue, the
+gated feed-forward products, layer norm and the combine step, each with its
+gradients.  Loops and textbook
 formulas; no code shared with the HIP path.
 """
 import math
@@ -75,6 +76,20 @@ def dense(x, w, bias=None):
     if bias is not None:
         z, s = z + bias, s + np.abs(bias)
     return z, s
+
+
+# ------------------------------------------------- gated feed-forward block
+def gated(name, z):
+    """h = act(z_gate) z_up of z [rows, 2 n], gate half first."""
+    z = np.asarray(z, np.float64)
+    n = z.shape[1] // 2
+    return activation(name, z[:, :n]) * z[:, n:]
+
+
+def gated_dz(name, dh, z):
+    dh, z = _f64(dh, z)
+    n = z.shape[1] // 2
+    return np.concatenate([dh * z[:, n:] * slope(name, z[:, :n]), dh * activation(name, z[:, :n])], 1)
 
 
 # --------------------------------------------------------------- layer norm
