@@ -511,6 +511,56 @@ size_t fg8_gemm_bf16_gated_backward_workspace_bytes(int64_t m, int64_t n, int64_
                                                     int32_t num_experts);
 
 /*
+ * Weights in 4 bits with group scales.  A row of weights is cut into groups of
+ * `group` (32, 64 or 128) consecutive columns:
+ *   s = fl32(amax / 7) (1 where that is 0), rounded to the scales' type;
+ *   code = rne(fl32(w / s)) + 8, in 1 .. 15;   the code stands for (code - 8) s
+ *   q       uint8 [rows][cols / 2], column 2 j in the low four bits of byte j
+ *   scales  [cols / group][rows] float (scales_are_bf16 = 0) or bf16 (1)
+ * A group with a NaN or an infinity gets a NaN for its scale, and stands for NaN.
+ * A product takes any code, 0 too.  cols is a multiple of the group; rows and
+ * cols do not exceed 2^22 (FG8_EUNSUPPORTED).
+ *
+ * int4_quantize: w [batch][rows][cols] float (w_is_bf16 = 0) or bf16 (1).
+ * int4_dequantize: its inverse, w [batch][rows][cols] float or bf16, rounded once.
+ * 1 <= batch <= 65535.
+ */
+fg8_status int4_quantize(const void* w, int32_t w_is_bf16, int64_t batch, int64_t rows,
+                         int64_t cols, int32_t group, uint8_t* q, void* scales,
+                         int32_t scales_are_bf16, hipStream_t stream);
+fg8_status int4_dequantize(const uint8_t* q, const void* scales, int32_t scales_are_bf16,
+                           int64_t batch, int64_t rows, int64_t cols, int32_t group, void* w,
+                           fg8_out out, hipStream_t stream);
+
+/*
+ * gemm_bf16_int4: products of few rows with such weights.
+ *   gated = 0: y = act(x W^T + bias) + residual, W [n][k]
+ *   gated = 1: y[r][j] = act(z[r][j]) z[r][n + j], z = x W^T, W [2 n][k] (n gate
+ *              rows, then n up rows); no bias, no residual
+ *   x bf16 [m][ldx]   q, scales as above (rows n or 2 n, cols k)
+ *   bias, residual, activation, y as gemm_bf16_epilogue; m >= 0, any n
+ * Any m is right, in pieces of 64 rows that read the weights each; it is made for
+ * one to some dozens (beyond, int4_dequantize and a BF16 product are faster).
+ */
+fg8_status gemm_bf16_int4(const uint16_t* x, int64_t ldx, const uint8_t* q, const void* scales,
+                          int32_t scales_are_bf16, int32_t group, const void* bias,
+                          int32_t bias_is_bf16, fg8_activation activation, int32_t gated,
+                          const uint16_t* residual, int64_t ldr, void* y, int64_t ldy, fg8_out out,
+                          int64_t m, int64_t n, int64_t k, hipStream_t stream);
+
+/*
+ * grouped_gemm_bf16_int4: the same over ragged row runs, q [num_experts][n or
+ * 2 n][k / 2], scales [num_experts][k / group][n or 2 n], without bias and
+ * residual; row_offsets, rows and num_experts as grouped_gemm_bf16 (rows of no
+ * run are written as zeros).
+ */
+fg8_status grouped_gemm_bf16_int4(const uint16_t* x, int64_t ldx, const uint8_t* q,
+                                  const void* scales, int32_t scales_are_bf16, int32_t group,
+                                  const int32_t* row_offsets, fg8_activation activation,
+                                  int32_t gated, void* y, int64_t ldy, fg8_out out, int64_t rows,
+                                  int64_t n, int64_t k, int32_t num_experts, hipStream_t stream);
+
+/*
  * layer_norm: y = (x - mean) rstd weight + bias over the last axis, with
  * rstd = 1 / sqrt(variance + eps) and the variance taken around the mean.
  *   x [rows][ldx] bf16 (x_is_bf16 = 1) or float (0), any cols and ldx

@@ -12,6 +12,7 @@ from ._lib import (  # noqa: F401
     gemm_bf16_epilogue_backward,
     gemm_bf16_gated,
     gemm_bf16_gated_backward,
+    gemm_bf16_int4,
     gemm_fp8_blockscaled,
     gemm_fp8_blockscaled_noalloc,
     gemm_mxfp8,
@@ -20,12 +21,15 @@ from ._lib import (  # noqa: F401
     grouped_gemm_bf16_dgrad,
     grouped_gemm_bf16_gated,
     grouped_gemm_bf16_gated_backward,
+    grouped_gemm_bf16_int4,
     grouped_gemm_bf16_wgrad,
     grouped_gemm_fp8_contiguous,
     grouped_gemm_fp8_contiguous_swiglu,
     grouped_gemm_fp8_kgrouped,
     grouped_gemm_fp8_masked,
     grouped_gemm_mxfp8_contiguous,
+    int4_dequantize,
+    int4_quantize,
     layer_norm,
     layer_norm_backward,
     moe_capacity,

@@ -7,6 +7,7 @@ library has not been built this module raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -72,6 +73,15 @@ _SIGNATURES = {
                                          _c_i64, _c_i32, _c_ptr, ctypes.c_size_t, _c_ptr],
     "fg8_gemm_bf16_gated_workspace_bytes": [_c_i64, _c_i64, _c_i64],
     "fg8_gemm_bf16_gated_backward_workspace_bytes": [_c_i64, _c_i64, _c_i64, _c_i32],
+    "int4_quantize": [_c_ptr, _c_i32, _c_i64, _c_i64, _c_i64, _c_i32, _c_ptr, _c_ptr, _c_i32, _c_ptr],
+    "int4_dequantize": [_c_ptr, _c_ptr, _c_i32, _c_i64, _c_i64, _c_i64, _c_i32, _c_ptr, ctypes.c_int,
+                        _c_ptr],
+    "gemm_bf16_int4": [_c_ptr, _c_i64, _c_ptr, _c_ptr, _c_i32, _c_i32, _c_ptr, _c_i32, ctypes.c_int,
+                       _c_i32, _c_ptr, _c_i64, _c_ptr, _c_i64, ctypes.c_int, _c_i64, _c_i64, _c_i64,
+                       _c_ptr],
+    "grouped_gemm_bf16_int4": [_c_ptr, _c_i64, _c_ptr, _c_ptr, _c_i32, _c_i32, _c_ptr, ctypes.c_int,
+                               _c_i32, _c_ptr, _c_i64, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i32,
+                               _c_ptr],
     "layer_norm": [_c_ptr, _c_i64, _c_i32, _c_ptr, _c_ptr, _c_i32, ctypes.c_float, _c_i64, _c_i64,
                    _c_ptr, _c_ptr, _c_ptr, _c_ptr],
     "layer_norm_backward": [_c_ptr, _c_i64, _c_ptr, _c_i64, _c_i32, _c_ptr, _c_i32, _c_ptr, _c_ptr,
@@ -804,6 +814,99 @@ def grouped_gemm_bf16_gated_backward(dh, x, w, z, row_offsets, activation="silu"
         dh.data_ptr(), lddh, x.data_ptr(), ldx, w.data_ptr(), z.data_ptr(), row_offsets.data_ptr(), act,
         _ptr(dx), _ptr(dw), _out_code(dw_dtype), rows, n, k, E, ws, ws_bytes, stream))
     return dx, dw
+
+
+# ------------------------------------------------------- weights in 4 bits
+def int4_quantize(w, group=128, scale_dtype=torch.float32):
+    """w float32 or bfloat16 [..., n, k] -> (q uint8 [..., n, k / 2], scales
+    scale_dtype (float32 or bfloat16) [..., k / group, n]): 4-bit codes, each
+    group of 32, 64 or 128 columns with a scale of amax / 7; see fg8.h."""
+    bf16 = w.dtype == torch.bfloat16
+    _dev(w, torch.bfloat16 if bf16 else torch.float32, "w")
+    if w.dim() < 2 or group < 1:
+        raise ValueError("w must be [..., n, k], group 32, 64 or 128")
+    *lead, n, k = w.shape
+    code = _out_code(scale_dtype)
+    q = w.new_empty((*lead, n, k // 2), dtype=torch.uint8)
+    scales = w.new_empty((*lead, k // group, n), dtype=scale_dtype)
+    _check(lib().int4_quantize(w.data_ptr(), int(bf16), math.prod(lead), n, k, group, q.data_ptr(),
+                               scales.data_ptr(), code, _stream_of(w)))
+    return q, scales
+
+
+def _int4(q, scales, lead):
+    """(n, k, group, scales are bf16) of codes [..., n, k / 2] and their scales."""
+    _dev(q, torch.uint8, "q")
+    bf16 = scales.dtype == torch.bfloat16
+    _dev(scales, torch.bfloat16 if bf16 else torch.float32, "scales")
+    if q.dim() < 2 or (lead is not None and q.dim() != 2 + lead):
+        raise ValueError("q must be " + ("[..., n, k / 2]" if lead is None else "[E, n, k / 2]" if lead else "[n, k / 2]"))
+    n, k = q.shape[-2], 2 * q.shape[-1]
+    if scales.dim() != q.dim() or scales.shape[:-2] != q.shape[:-2] or scales.shape[-1] != n or scales.shape[-2] == 0 \
+            or k % scales.shape[-2]:
+        raise ValueError("scales must be [..., k / group, n] for q [..., n, k / 2]")
+    return n, k, k // scales.shape[-2], int(bf16)
+
+
+def int4_dequantize(q, scales, out_dtype=torch.bfloat16):
+    """The values [..., n, k] that codes and scales stand for, as int4_quantize
+    returned them (for the BF16 products of many rows)."""
+    n, k, group, bf16 = _int4(q, scales, None)
+    w = q.new_empty((*q.shape[:-1], k), dtype=out_dtype)
+    _check(lib().int4_dequantize(q.data_ptr(), scales.data_ptr(), bf16, math.prod(q.shape[:-2]), n, k,
+                                 group, w.data_ptr(), _out_code(out_dtype), _stream_of(q)))
+    return w
+
+
+def gemm_bf16_int4(x, q, scales, bias=None, residual=None, activation="none", gated=False,
+                   out_dtype=torch.bfloat16, out=None):
+    """y = act(x W^T + bias) + residual for few rows, W [n, k] in 4 bits as
+    int4_quantize returns it: x bf16 [m, k], the rest as gemm_bf16_epilogue.
+    gated: W [2 n, k], y = act(x Wg^T) * (x Wu^T) as gemm_bf16_gated, without bias
+    and residual."""
+    act = ACTIVATIONS[activation]
+    wide, k, group, s_bf16 = _int4(q, scales, 0)
+    ldx = _rows(x, torch.bfloat16, "x")
+    m = x.shape[0]
+    if x.shape[1] != k or (gated and wide % 2):
+        raise ValueError("operand shapes disagree")
+    n = wide // 2 if gated else wide
+    if gated and (bias is not None or residual is not None):
+        raise ValueError("a gated product takes neither bias nor residual")
+    bias_ptr, bias_bf16 = _param(bias, n, "bias")
+    res_ptr, ldr = None, n
+    if residual is not None:
+        ldr = _rows(residual, torch.bfloat16, "residual")
+        if residual.shape != (m, n):
+            raise ValueError("residual must have the output's shape")
+        res_ptr = residual.data_ptr()
+        if m == 1:
+            ldr = n
+    out, ldy, code = _out_rows(out, (m, n), out_dtype, x)
+    _check(lib().gemm_bf16_int4(x.data_ptr(), ldx, q.data_ptr(), scales.data_ptr(), s_bf16, group, bias_ptr,
+                                bias_bf16, act, int(gated), res_ptr, ldr, out.data_ptr(), ldy, code, m, n, k,
+                                _stream_of(x)))
+    return out
+
+
+def grouped_gemm_bf16_int4(x, q, scales, row_offsets, activation="none", gated=False,
+                           out_dtype=torch.bfloat16, out=None):
+    """gemm_bf16_int4 over ragged row runs, as grouped_gemm_bf16: q [E, n, k / 2]
+    (gated: 2 n), scales [E, k / group, n], row_offsets int32 [E + 1] (device);
+    rows of no run are zeros."""
+    act = ACTIVATIONS[activation]
+    wide, k, group, s_bf16 = _int4(q, scales, 1)
+    ldx = _rows(x, torch.bfloat16, "x")
+    rows = x.shape[0]
+    if x.shape[1] != k or (gated and wide % 2):
+        raise ValueError("operand shapes disagree")
+    n = wide // 2 if gated else wide
+    E = _run_offsets(q, row_offsets)
+    out, ldy, code = _out_rows(out, (rows, n), out_dtype, x)
+    _check(lib().grouped_gemm_bf16_int4(x.data_ptr(), ldx, q.data_ptr(), scales.data_ptr(), s_bf16, group,
+                                        row_offsets.data_ptr(), act, int(gated), out.data_ptr(), ldy, code,
+                                        rows, n, k, E, _stream_of(x)))
+    return out
 
 
 # --------------------------------------------------------------- layer norm

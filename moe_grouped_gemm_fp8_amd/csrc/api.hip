@@ -990,6 +990,127 @@ fg8_status fg8_bf16_tile_choice(int32_t product, int64_t m, int64_t n, int64_t k
 
 }  // extern "C"
 
+// ----------------------------------------------------- weights in 4 bits
+namespace {
+
+// the codes' and scales' sizes: [rows][cols] weights in groups of `group` columns
+fg8_status check_int4(const char* fn, int64_t rows, int64_t cols, int32_t group, int32_t scales_bf16) {
+  if (group != 32 && group != 64 && group != 128) return fail(FG8_EUNSUPPORTED, "%s: group=%d must be 32, 64 or 128", fn, (int)group);
+  if (rows < 1 || cols < 1) return fail(FG8_EINVAL, "%s: bad sizes n=%lld k=%lld", fn, (long long)rows, (long long)cols);
+  if (cols % group) return fail(FG8_EUNSUPPORTED, "%s: k=%lld is not a multiple of the group (%d)", fn, (long long)cols, (int)group);
+  if (rows > kMaxLd || cols > kMaxLd)
+    return fail(FG8_EUNSUPPORTED, "%s: weights of %lld x %lld exceed %lld a side", fn, (long long)rows, (long long)cols, (long long)kMaxLd);
+  if (scales_bf16 != 0 && scales_bf16 != 1) return fail(FG8_EINVAL, "%s: scales_are_bf16=%d", fn, (int)scales_bf16);
+  return FG8_OK;
+}
+
+fg8_status check_int4_launch(const char* fn, int64_t batch, int64_t rows, int64_t cols) {
+  if (batch < 1 || batch > 65535) return fail(FG8_EINVAL, "%s: batch=%lld must be in [1, 65535]", fn, (long long)batch);
+  if (fg8::int4_workgroups(batch, rows, cols) * 256 > kMaxThreads)
+    return fail(FG8_EUNSUPPORTED, "%s: %lld x %lld x %lld exceed a launch", fn, (long long)batch, (long long)rows, (long long)cols);
+  return FG8_OK;
+}
+
+fg8_status int4_product(const char* fn, const uint16_t* x, int64_t ldx, const uint8_t* q, const void* scales,
+                        int32_t scales_bf16, int32_t group, const void* bias, int32_t bias_bf16, fg8_activation activation,
+                        int32_t gated, const uint16_t* residual, int64_t ldr, void* y, int64_t ldy, fg8_out out, int64_t m,
+                        int64_t n, int64_t k, const int32_t* offsets, int32_t num_experts, hipStream_t stream) {
+  if (gated != 0 && gated != 1) return fail(FG8_EINVAL, "%s: gated=%d", fn, (int)gated);
+  if (n > kMaxLd) return fail(FG8_EUNSUPPORTED, "%s: n=%lld exceeds %lld", fn, (long long)n, (long long)kMaxLd);
+  if (fg8_status s = check_int4(fn, gated ? 2 * n : n, k, group, scales_bf16)) return s;
+  if (fg8_status s = check_out(fn, out)) return s;
+  if ((int)activation < FG8_ACT_NONE || (int)activation > FG8_ACT_GELU)
+    return fail(FG8_EINVAL, "%s: unknown activation %d", fn, (int)activation);
+  if (bias_bf16 != 0 && bias_bf16 != 1) return fail(FG8_EINVAL, "%s: bias_is_bf16=%d", fn, (int)bias_bf16);
+  if (gated && (bias || residual)) return fail(FG8_EINVAL, "%s: a gated product takes neither bias nor residual", fn);
+  if (m == 0) return FG8_OK;
+  FG8_CHECK_PTR(x);
+  FG8_CHECK_PTR(q);
+  FG8_CHECK_PTR(scales);
+  FG8_CHECK_PTR(y);
+  FG8_CHECK_LD(ldx, k, 8);
+  FG8_CHECK_LD(ldy, n, 1);
+  if (bias) FG8_CHECK_PTR(bias);
+  if (residual) {
+    FG8_CHECK_PTR(residual);
+    FG8_CHECK_LD(ldr, n, 1);
+  }
+  fg8::BfProblem p = dense_bf16(m, gated ? 2 * n : n, k, false, false);
+  p.a = x; p.lda = ldx; p.d = y; p.ldd = ldy;
+  p.out_bf16 = out == FG8_OUT_BF16;
+  p.bias = bias; p.bias_bf16 = bias_bf16; p.act = (int)activation; p.gated = gated;
+  p.residual = residual; p.ldr = ldr;
+  if (num_experts) {
+    FG8_CHECK_PTR(offsets);
+    p.mode = fg8::kBfRowRuns;
+    p.groups = num_experts; p.offsets = offsets;
+  }
+  const fg8::Int4Tile t = fg8::int4_tile(p, fg8::device_cu_count());
+  if ((t.units + 7) / 8 * 8 * t.threads > kMaxThreads)
+    return fail(FG8_EUNSUPPORTED, "%s: %lld tiles of %d threads exceed a launch", fn, (long long)t.units, t.threads);
+  const hipError_t e = fg8::launch_int4(p, t, q, scales, scales_bf16 != 0, group, stream);
+  if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  g_err[0] = 0;
+  return FG8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fg8_status int4_quantize(const void* w, int32_t w_is_bf16, int64_t batch, int64_t rows, int64_t cols, int32_t group,
+                         uint8_t* q, void* scales, int32_t scales_are_bf16, hipStream_t stream) {
+  const char* fn = "int4_quantize";
+  if (fg8_status s = check_int4(fn, rows, cols, group, scales_are_bf16)) return s;
+  if (fg8_status s = check_int4_launch(fn, batch, rows, cols)) return s;
+  if (w_is_bf16 != 0 && w_is_bf16 != 1) return fail(FG8_EINVAL, "%s: w_is_bf16=%d", fn, (int)w_is_bf16);
+  FG8_CHECK_PTR(w);
+  FG8_CHECK_PTR(q);
+  FG8_CHECK_PTR(scales);
+  const hipError_t e = fg8::launch_int4_quantize(w, w_is_bf16 != 0, batch, rows, cols, group, q, scales, scales_are_bf16 != 0, stream);
+  if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  g_err[0] = 0;
+  return FG8_OK;
+}
+
+fg8_status int4_dequantize(const uint8_t* q, const void* scales, int32_t scales_are_bf16, int64_t batch, int64_t rows,
+                           int64_t cols, int32_t group, void* w, fg8_out out, hipStream_t stream) {
+  const char* fn = "int4_dequantize";
+  if (fg8_status s = check_int4(fn, rows, cols, group, scales_are_bf16)) return s;
+  if (fg8_status s = check_int4_launch(fn, batch, rows, cols)) return s;
+  if (fg8_status s = check_out(fn, out)) return s;
+  FG8_CHECK_PTR(q);
+  FG8_CHECK_PTR(scales);
+  FG8_CHECK_PTR(w);
+  const hipError_t e =
+      fg8::launch_int4_dequantize(q, scales, scales_are_bf16 != 0, batch, rows, cols, group, w, out == FG8_OUT_BF16, stream);
+  if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  g_err[0] = 0;
+  return FG8_OK;
+}
+
+fg8_status gemm_bf16_int4(const uint16_t* x, int64_t ldx, const uint8_t* q, const void* scales, int32_t scales_are_bf16,
+                          int32_t group, const void* bias, int32_t bias_is_bf16, fg8_activation activation, int32_t gated,
+                          const uint16_t* residual, int64_t ldr, void* y, int64_t ldy, fg8_out out, int64_t m, int64_t n,
+                          int64_t k, hipStream_t stream) {
+  const char* fn = "gemm_bf16_int4";
+  if (fg8_status s = check_m(fn, m, 0)) return s;
+  return int4_product(fn, x, ldx, q, scales, scales_are_bf16, group, bias, bias_is_bf16, activation, gated, residual, ldr,
+                      y, ldy, out, m, n, k, nullptr, 0, stream);
+}
+
+fg8_status grouped_gemm_bf16_int4(const uint16_t* x, int64_t ldx, const uint8_t* q, const void* scales,
+                                  int32_t scales_are_bf16, int32_t group, const int32_t* row_offsets,
+                                  fg8_activation activation, int32_t gated, void* y, int64_t ldy, fg8_out out, int64_t rows,
+                                  int64_t n, int64_t k, int32_t num_experts, hipStream_t stream) {
+  const char* fn = "grouped_gemm_bf16_int4";
+  if (fg8_status s = check_runs(fn, rows, num_experts)) return s;
+  return int4_product(fn, x, ldx, q, scales, scales_are_bf16, group, nullptr, 0, activation, gated, nullptr, 0, y, ldy, out,
+                      rows, n, k, row_offsets, num_experts, stream);
+}
+
+}  // extern "C"
+
 namespace {
 
 constexpr int64_t kMaxNormCols = 32768;

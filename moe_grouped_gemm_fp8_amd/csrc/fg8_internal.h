@@ -124,6 +124,22 @@ BfTile bf16_tile(const BfProblem& p, int num_cus);
 size_t bf16_workspace_bytes(const BfProblem& p, int num_cus);
 hipError_t launch_bf16(BfProblem p, const BfTile& t, hipStream_t stream);
 
+// ------------------------------------------------------ weights in 4 bits
+// p: a, d, sizes (N weight rows), runs and epilogue as the BF16 products', b
+// unused; `units` workgroups of `threads`, each 16 tm rows by 16 tn weight rows.
+struct Int4Tile {
+  int tm, tn, threads;
+  int64_t units;
+};
+Int4Tile int4_tile(const BfProblem& p, int num_cus);
+hipError_t launch_int4(const BfProblem& p, const Int4Tile& t, const uint8_t* codes, const void* scales,
+                       bool scales_bf16, int group, hipStream_t stream);
+int64_t int4_workgroups(int64_t batch, int64_t rows, int64_t cols);
+hipError_t launch_int4_quantize(const void* w, bool bf16, int64_t batch, int64_t rows, int64_t cols, int group,
+                                uint8_t* q, void* scales, bool scales_bf16, hipStream_t stream);
+hipError_t launch_int4_dequantize(const uint8_t* q, const void* scales, bool scales_bf16, int64_t batch,
+                                  int64_t rows, int64_t cols, int group, void* w, bool bf16, hipStream_t stream);
+
 // dz = dy * act'(z) in BF16 (row stride ldz, zeros from column n up to it) and
 // its column sums, by `chunks` row ranges in partial [chunks][n], then in
 // dbias [n]; either result may be left out (NULL).  rest: what that rounding of
