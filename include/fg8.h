@@ -561,6 +561,48 @@ fg8_status grouped_gemm_bf16_int4(const uint16_t* x, int64_t ldx, const uint8_t*
                                   int64_t n, int64_t k, int32_t num_experts, hipStream_t stream);
 
 /*
+ * linear_cross_entropy: the softmax cross entropy of a linear head's logits,
+ * which are never kept:
+ *   l[r][c] = x[r] . w[c],  lse[r] = log sum_c e^l[r][c],  loss[r] = lse[r] - l[r][targets[r]]
+ *   x bf16 [m][ldx]   w bf16 [vocab][k]
+ *   targets  int32 (targets_are_int64 = 0) or int64 (1) [m]; a row whose target
+ *            lies outside [0, vocab) has none: its loss is 0, its lse as ever
+ *   loss, lse float [m]
+ * Logits are FP32 sums and not rounded.  A row with a NaN or +inf logit has NaN
+ * for its lse and its loss; -inf adds nothing.
+ *   k % 8 == 0 (else FG8_EUNSUPPORTED), any vocab >= 1, m >= 0; neither vocab nor
+ *   k above 2^22.
+ *   workspace: fg8_linear_cross_entropy_workspace_bytes(m, vocab, k) bytes under
+ *   gemm_bf16_epilogue's rules.
+ */
+fg8_status linear_cross_entropy(const uint16_t* x, int64_t ldx, const uint16_t* w,
+                                const void* targets, int32_t targets_are_int64, float* loss,
+                                float* lse, int64_t m, int64_t vocab, int64_t k, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+size_t fg8_linear_cross_entropy_workspace_bytes(int64_t m, int64_t vocab, int64_t k);
+
+/*
+ * linear_cross_entropy_backward: its gradients from the rows' dloss:
+ *   dl[r][c] = (e^(l[r][c] - lse[r]) - [c = targets[r]]) dloss[r]   (0 for a row
+ *   without a target, whatever its dloss and lse hold),  dx = dl w,  dw = dl^T x
+ *   dloss, lse float [m]   dx bf16 [m][k], dw [vocab][k] float or bf16; either may
+ *   be NULL and is then not computed.
+ * The logits are computed again, as many classes at a time as make 512 MB of dl in
+ * BF16 (256 at least).  dl is rounded to BF16 for dx and a bf16 dw; a float dw takes
+ * it in two BF16 parts.  m >= 1.  workspace:
+ * fg8_linear_cross_entropy_backward_workspace_bytes(m, vocab, k, dw_out) bytes under
+ * gemm_bf16_epilogue's rules.
+ */
+fg8_status linear_cross_entropy_backward(const float* dloss, const uint16_t* x, int64_t ldx,
+                                         const uint16_t* w, const void* targets,
+                                         int32_t targets_are_int64, const float* lse, uint16_t* dx,
+                                         void* dw, fg8_out dw_out, int64_t m, int64_t vocab,
+                                         int64_t k, void* workspace, size_t workspace_bytes,
+                                         hipStream_t stream);
+size_t fg8_linear_cross_entropy_backward_workspace_bytes(int64_t m, int64_t vocab, int64_t k,
+                                                         fg8_out dw_out);
+
+/*
  * layer_norm: y = (x - mean) rstd weight + bias over the last axis, with
  * rstd = 1 / sqrt(variance + eps) and the variance taken around the mean.
  *   x [rows][ldx] bf16 (x_is_bf16 = 1) or float (0), any cols and ldx

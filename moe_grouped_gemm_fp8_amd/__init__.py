@@ -32,6 +32,8 @@ from ._lib import (  # noqa: F401
     int4_quantize,
     layer_norm,
     layer_norm_backward,
+    linear_cross_entropy,
+    linear_cross_entropy_backward,
     moe_capacity,
     moe_combine,
     moe_combine_backward,

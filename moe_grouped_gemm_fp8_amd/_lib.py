@@ -82,6 +82,13 @@ _SIGNATURES = {
     "grouped_gemm_bf16_int4": [_c_ptr, _c_i64, _c_ptr, _c_ptr, _c_i32, _c_i32, _c_ptr, ctypes.c_int,
                                _c_i32, _c_ptr, _c_i64, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i32,
                                _c_ptr],
+    "linear_cross_entropy": [_c_ptr, _c_i64, _c_ptr, _c_ptr, _c_i32, _c_ptr, _c_ptr, _c_i64, _c_i64,
+                             _c_i64, _c_ptr, ctypes.c_size_t, _c_ptr],
+    "linear_cross_entropy_backward": [_c_ptr, _c_ptr, _c_i64, _c_ptr, _c_ptr, _c_i32, _c_ptr, _c_ptr,
+                                      _c_ptr, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_ptr,
+                                      ctypes.c_size_t, _c_ptr],
+    "fg8_linear_cross_entropy_workspace_bytes": [_c_i64, _c_i64, _c_i64],
+    "fg8_linear_cross_entropy_backward_workspace_bytes": [_c_i64, _c_i64, _c_i64, ctypes.c_int],
     "layer_norm": [_c_ptr, _c_i64, _c_i32, _c_ptr, _c_ptr, _c_i32, ctypes.c_float, _c_i64, _c_i64,
                    _c_ptr, _c_ptr, _c_ptr, _c_ptr],
     "layer_norm_backward": [_c_ptr, _c_i64, _c_ptr, _c_i64, _c_i32, _c_ptr, _c_i32, _c_ptr, _c_ptr,
@@ -104,6 +111,8 @@ _RESTYPES = {"fg8_gemm_workspace_bytes": ctypes.c_size_t, "fg8_last_error": ctyp
              "fg8_gemm_bf16_backward_workspace_bytes": ctypes.c_size_t,
              "fg8_gemm_bf16_gated_workspace_bytes": ctypes.c_size_t,
              "fg8_gemm_bf16_gated_backward_workspace_bytes": ctypes.c_size_t,
+             "fg8_linear_cross_entropy_workspace_bytes": ctypes.c_size_t,
+             "fg8_linear_cross_entropy_backward_workspace_bytes": ctypes.c_size_t,
              "fg8_layer_norm_backward_workspace_bytes": ctypes.c_size_t}
 
 _lib = None
@@ -907,6 +916,68 @@ def grouped_gemm_bf16_int4(x, q, scales, row_offsets, activation="none", gated=F
                                         row_offsets.data_ptr(), act, int(gated), out.data_ptr(), ldy, code,
                                         rows, n, k, E, _stream_of(x)))
     return out
+
+
+# ------------------------------------------ cross entropy of a linear head
+def _head(x, w, targets):
+    _dev(w, torch.bfloat16, "w")
+    ldx = _rows(x, torch.bfloat16, "x")
+    if w.dim() != 2 or x.shape[1] != w.shape[1] or w.shape[0] == 0:
+        raise ValueError("x must be [m, k] and w [vocab, k]")
+    wide = targets.dtype == torch.int64
+    _dev(targets, torch.int64 if wide else torch.int32, "targets")
+    if targets.shape != (x.shape[0],):
+        raise ValueError("targets must be [m]")
+    return ldx, int(wide), x.shape[0], w.shape[0], w.shape[1]
+
+
+def linear_cross_entropy(x, w, targets, workspace=None):
+    """Softmax cross entropy of each row of x w^T at its target, without the
+    logits in memory: x bf16 [m, k] (rows may be strided), w bf16 [vocab, k],
+    targets int64 or int32 [m] -> (loss, lse) float32 [m], lse the log of the sum
+    of exponentials for the backward pass.  A target outside [0, vocab) means
+    none: loss 0."""
+    ldx, wide, m, vocab, k = _head(x, w, targets)
+    loss, lse = x.new_empty(m, dtype=torch.float32), x.new_empty(m, dtype=torch.float32)
+    L = lib()
+    stream = _stream_of(x)
+    if workspace is None:
+        workspace, ws, ws_bytes = _workspace_of(L.fg8_linear_cross_entropy_workspace_bytes(m, vocab, k), x, stream)
+    else:
+        ws, ws_bytes = _workspace_given(workspace)
+    _check(L.linear_cross_entropy(x.data_ptr(), ldx, w.data_ptr(), targets.data_ptr(), wide, loss.data_ptr(),
+                                  lse.data_ptr(), m, vocab, k, ws, ws_bytes, stream))
+    return loss, lse
+
+
+def linear_cross_entropy_backward(dloss, x, w, targets, lse, dw_dtype=torch.float32, needs=(True, True),
+                                  workspace=None):
+    """Gradients of linear_cross_entropy: dloss float32 [m] (1 / count for a mean),
+    lse as the forward pass returned it -> (dx bf16 [m, k], dw dw_dtype [vocab,
+    k]); `needs` leaves out (None) what is not wanted.  dx and a bfloat16 dw take
+    the logits' gradients rounded to bfloat16, a float32 dw to 2^-16 (a second
+    product)."""
+    ldx, wide, m, vocab, k = _head(x, w, targets)
+    for name, t in (("dloss", dloss), ("lse", lse)):
+        _dev(t, torch.float32, name)
+        if t.shape != (m,):
+            raise ValueError(f"{name} must be [m]")
+    dx = x.new_empty((m, k)) if needs[0] else None
+    dw = w.new_empty(w.shape, dtype=dw_dtype) if needs[1] else None
+    code = _out_code(dw_dtype)
+    if m == 0:     # sums over no rows
+        return dx, dw if dw is None else dw.zero_()
+    L = lib()
+    stream = _stream_of(x)
+    if workspace is None:
+        workspace, ws, ws_bytes = _workspace_of(
+            L.fg8_linear_cross_entropy_backward_workspace_bytes(m, vocab, k, code), x, stream)
+    else:
+        ws, ws_bytes = _workspace_given(workspace)
+    _check(L.linear_cross_entropy_backward(dloss.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), targets.data_ptr(), wide,
+                                           lse.data_ptr(), _ptr(dx), _ptr(dw), code, m, vocab, k, ws, ws_bytes,
+                                           stream))
+    return dx, dw
 
 
 # --------------------------------------------------------------- layer norm

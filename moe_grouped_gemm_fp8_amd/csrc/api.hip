@@ -794,7 +794,7 @@ namespace {
 
 fg8::BfProblem gated_bf16(int64_t m, int64_t n, int64_t k) {
   fg8::BfProblem p = dense_bf16(m, 2 * n, k, false, false);
-  p.gated = 1;
+  p.kind = fg8::kKindGated;
   return p;
 }
 
@@ -1038,7 +1038,7 @@ fg8_status int4_product(const char* fn, const uint16_t* x, int64_t ldx, const ui
   fg8::BfProblem p = dense_bf16(m, gated ? 2 * n : n, k, false, false);
   p.a = x; p.lda = ldx; p.d = y; p.ldd = ldy;
   p.out_bf16 = out == FG8_OUT_BF16;
-  p.bias = bias; p.bias_bf16 = bias_bf16; p.act = (int)activation; p.gated = gated;
+  p.bias = bias; p.bias_bf16 = bias_bf16; p.act = (int)activation; p.kind = gated ? fg8::kKindGated : fg8::kKindTile;
   p.residual = residual; p.ldr = ldr;
   if (num_experts) {
     FG8_CHECK_PTR(offsets);
@@ -1107,6 +1107,173 @@ fg8_status grouped_gemm_bf16_int4(const uint16_t* x, int64_t ldx, const uint8_t*
   if (fg8_status s = check_runs(fn, rows, num_experts)) return s;
   return int4_product(fn, x, ldx, q, scales, scales_are_bf16, group, nullptr, 0, activation, gated, nullptr, 0, y, ldy, out,
                       rows, n, k, row_offsets, num_experts, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------- cross entropy of a linear head
+namespace {
+
+// The forward pass's workspace: counters (left alone: another call on the same
+// workspace finds them at zero), target logits, and each column tile's pieces.
+struct LossSpace {
+  size_t picked, pieces, total;
+  int64_t tiles;
+};
+fg8::BfProblem loss_bf16(int64_t m, int64_t v, int64_t k, int kind) {
+  fg8::BfProblem p = dense_bf16(m, v, k, false, false);
+  p.kind = kind;
+  return p;
+}
+LossSpace loss_space(int64_t m, int64_t v, int64_t k) {
+  const fg8::BfTile t = fg8::bf16_tile(loss_bf16(m, v, k, fg8::kKindLse), fg8::device_cu_count());
+  LossSpace s{};
+  s.tiles = (v + t.bn - 1) / t.bn;
+  s.picked = fg8::kSplitKCounterBytes;
+  s.pieces = s.picked + (size_t)up(m * 4, 16);
+  s.total = s.pieces + (size_t)s.tiles * m * 8;
+  return s;
+}
+
+// The backward pass's: counters and its products' partial tiles, then dlogits of
+// one piece of the vocabulary (and what their rounding left), and dx's sums
+// where there is more than one piece.
+constexpr int64_t kLossPieceBytes = (int64_t)512 << 20;    // of dlogits at a time
+struct LossBackwardSpace {
+  size_t products, dz, rest, sums, total;
+  int64_t piece, ldz;       // classes of a piece, the last one may have fewer
+};
+LossBackwardSpace loss_backward_space(int64_t m, int64_t v, int64_t k, bool rest) {
+  const int cus = fg8::device_cu_count();
+  LossBackwardSpace s{};
+  const int64_t most = kLossPieceBytes / (2 * m) < 256 ? 256 : kLossPieceBytes / (2 * m);
+  const int64_t pieces = (v + most - 1) / most;
+  s.piece = pieces == 1 ? v : up((v + pieces - 1) / pieces, 256);
+  s.ldz = up(s.piece, 8);
+  s.products = fg8::kSplitKCounterBytes;
+  for (int64_t n : {s.piece, v % s.piece ? v % s.piece : s.piece})
+    for (int add = 0; add < 2; ++add) {
+      fg8::BfProblem p = dense_bf16(m, k, n, false, true), q = dense_bf16(n, k, m, true, true);
+      p.add = q.add = add;
+      for (const fg8::BfProblem& r : {p, q}) {
+        const size_t b = fg8::bf16_workspace_bytes(r, cus);
+        if (b > s.products) s.products = b;
+      }
+    }
+  const size_t dz = (size_t)up(m * s.ldz * 2, 16);
+  s.dz = s.products;
+  s.rest = s.dz + dz;
+  s.sums = s.rest + (rest ? dz : 0);
+  s.total = s.sums + (pieces > 1 ? (size_t)m * k * 4 : 0);
+  return s;
+}
+
+fg8_status check_loss(const char* fn, int64_t m, int64_t v, int64_t k, int32_t targets64) {
+  if (fg8_status s = check_m(fn, m, 0)) return s;
+  if (fg8_status s = check_nk(fn, v, false, k)) return s;
+  if (v > kMaxLd || k > kMaxLd)
+    return fail(FG8_EUNSUPPORTED, "%s: vocab=%lld and k=%lld must not exceed %lld", fn, (long long)v, (long long)k, (long long)kMaxLd);
+  if (targets64 != 0 && targets64 != 1) return fail(FG8_EINVAL, "%s: targets_are_int64=%d", fn, (int)targets64);
+  return FG8_OK;
+}
+
+bool loss_sizes(int64_t m, int64_t v, int64_t k) {
+  return m >= 1 && v >= 1 && k >= 1 && m <= kMaxRows && v <= kMaxLd && k <= kMaxLd;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fg8_linear_cross_entropy_workspace_bytes(int64_t m, int64_t vocab, int64_t k) {
+  return loss_sizes(m, vocab, k) ? loss_space(m, vocab, k).total : 0;
+}
+
+fg8_status linear_cross_entropy(const uint16_t* x, int64_t ldx, const uint16_t* w, const void* targets,
+                                int32_t targets_are_int64, float* loss, float* lse, int64_t m, int64_t vocab, int64_t k,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const char* fn = "linear_cross_entropy";
+  if (fg8_status s = check_loss(fn, m, vocab, k, targets_are_int64)) return s;
+  if (m == 0) return FG8_OK;
+  FG8_CHECK_PTR(x);
+  FG8_CHECK_PTR(w);
+  FG8_CHECK_PTR(targets);
+  FG8_CHECK_PTR(loss);
+  FG8_CHECK_PTR(lse);
+  FG8_CHECK_LD(ldx, k, 8);
+  const LossSpace here = loss_space(m, vocab, k);
+  fg8::BfProblem p = loss_bf16(m, vocab, k, fg8::kKindLse);
+  if (fg8_status s = set_workspace(p, fn, workspace, workspace_bytes, here.total)) return s;
+  p.a = x; p.lda = ldx; p.b = w; p.ldb = k;
+  p.loss.targets = targets; p.loss.targets64 = targets_are_int64; p.loss.classes = (int)vocab;
+  p.loss.picked = (float*)((char*)workspace + here.picked);
+  p.loss.pieces = (float2*)((char*)workspace + here.pieces);
+  if (fg8_status s = run_bf16(p, fn, stream)) return s;
+  const hipError_t e = fg8::launch_loss_finish(p.loss, here.tiles, m, loss, lse, stream);
+  if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  g_err[0] = 0;
+  return FG8_OK;
+}
+
+size_t fg8_linear_cross_entropy_backward_workspace_bytes(int64_t m, int64_t vocab, int64_t k, fg8_out dw_out) {
+  return loss_sizes(m, vocab, k) ? loss_backward_space(m, vocab, k, dw_out == FG8_OUT_F32).total : 0;
+}
+
+fg8_status linear_cross_entropy_backward(const float* dloss, const uint16_t* x, int64_t ldx, const uint16_t* w,
+                                         const void* targets, int32_t targets_are_int64, const float* lse, uint16_t* dx,
+                                         void* dw, fg8_out dw_out, int64_t m, int64_t vocab, int64_t k, void* workspace,
+                                         size_t workspace_bytes, hipStream_t stream) {
+  const char* fn = "linear_cross_entropy_backward";
+  if (fg8_status s = check_loss(fn, m, vocab, k, targets_are_int64)) return s;
+  if (fg8_status s = check_out(fn, dw_out)) return s;
+  if (m < 1) return fail(FG8_EINVAL, "%s: m=%lld", fn, (long long)m);
+  if (!dx && !dw) return fail(FG8_EINVAL, "%s: no output", fn);
+  FG8_CHECK_PTR(dloss);
+  FG8_CHECK_PTR(x);
+  FG8_CHECK_PTR(w);
+  FG8_CHECK_PTR(targets);
+  FG8_CHECK_PTR(lse);
+  if (dx) FG8_CHECK_PTR(dx);
+  if (dw) FG8_CHECK_PTR(dw);
+  FG8_CHECK_LD(ldx, k, 8);
+  const bool rest = dw && dw_out == FG8_OUT_F32;
+  const LossBackwardSpace here = loss_backward_space(m, vocab, k, dw_out == FG8_OUT_F32);
+  fg8::BfProblem p = loss_bf16(m, 0, k, fg8::kKindDlogits);
+  if (fg8_status s = set_workspace(p, fn, workspace, workspace_bytes, here.total)) return s;
+  uint16_t* dz = (uint16_t*)((char*)workspace + here.dz);
+  uint16_t* left = (uint16_t*)((char*)workspace + here.rest);
+  float* sums = (float*)((char*)workspace + here.sums);
+  const bool pieces = here.piece < vocab;
+  p.a = x; p.lda = ldx; p.ldb = k; p.d = dz; p.ldd = here.ldz;
+  p.loss.targets = targets; p.loss.targets64 = targets_are_int64; p.loss.classes = (int)vocab;
+  p.loss.lse = lse; p.loss.dloss = dloss; p.loss.rest = rest ? left : nullptr;
+  for (int64_t v0 = 0; v0 < vocab; v0 += here.piece) {
+    const int64_t n = vocab - v0 < here.piece ? vocab - v0 : here.piece;
+    p.N = (int)n; p.b = w + v0 * k; p.loss.first = (int)v0;
+    if (fg8_status s = run_bf16(p, fn, stream)) return s;
+    if (dx) {
+      fg8::BfProblem q = dense_bf16(m, k, n, false, true);
+      q.counters = p.counters; q.partial = p.partial;
+      q.a = dz; q.lda = here.ldz; q.b = p.b; q.ldb = k; q.ldd = k;
+      q.d = pieces ? (void*)sums : dx; q.out_bf16 = !pieces; q.add = v0 > 0;
+      if (fg8_status s = run_bf16(q, fn, stream)) return s;
+    }
+    // A float dw takes dlogits in two BF16 parts, as gemm_bf16_epilogue_backward's does.
+    for (int part = 0; part < (dw ? rest ? 2 : 1 : 0); ++part) {
+      fg8::BfProblem q = dense_bf16(n, k, m, true, true);
+      q.counters = p.counters; q.partial = p.partial;
+      q.a = part ? left : dz; q.lda = here.ldz; q.b = x; q.ldb = ldx; q.ldd = k;
+      q.out_bf16 = !rest; q.add = part;
+      q.d = (char*)dw + v0 * k * (rest ? 4 : 2);
+      if (fg8_status s = run_bf16(q, fn, stream)) return s;
+    }
+  }
+  if (dx && pieces) {
+    const hipError_t e = fg8::launch_round_bf16(sums, m * k, dx, stream);
+    if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  }
+  g_err[0] = 0;
+  return FG8_OK;
 }
 
 }  // extern "C"

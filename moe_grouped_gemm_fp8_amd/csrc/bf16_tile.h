@@ -529,4 +529,113 @@ struct GatedOut {
   }
 };
 
+// ----------------------------------------------------- loss of a linear head
+// The target of a row as a class, -1 for none.
+__device__ __forceinline__ int target_of(const BfLoss& s, int64_t row) {
+  const int64_t t = s.targets64 ? ((const int64_t*)s.targets)[row] : ((const int32_t*)s.targets)[row];
+  return t >= 0 && t < s.classes ? (int)t : -1;
+}
+// v of the four lanes that hold a row's columns, combined
+template <class F>
+__device__ __forceinline__ float over_row(float v, F f) {
+  typedef unsigned u2 __attribute__((ext_vector_type(2)));
+  u2 a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+constexpr float kLog2e = 1.4426950408889634f;
+// From here on down an exponential adds nothing, and where every logit of a piece
+// is -inf or past the last class the piece has a maximum to subtract.
+constexpr float kLowest = -3.4028235e38f;
+
+// A wave's 64 columns of a tile of logits, GROUPS times sixteen rows: kKindLse
+// leaves each row's maximum and sum in LDS (merge() below joins the waves'),
+// kKindDlogits stores dlogits.
+template <int KIND, int GROUPS>
+struct LossOut {
+  static constexpr int kTurn = 2048;    // LDS of a wave
+  const BfProblem& p;
+  uint8_t* turn;
+  int64_t m0;
+  int rows, n, lane;
+  bool whole;
+  static constexpr int kNone = -0x7fffffff - 1;
+  int target[GROUPS];                   // of this lane's row, counted from this product's first class
+  float lse[GROUPS], dloss[GROUPS];
+  __device__ LossOut(const BfProblem& q, const BfUnit& w, int bm, int bn, int wave_n, uint8_t* t, int l)
+      : p(q), turn(t), m0(w.m0), rows(w.rows), n(w.n0 + wave_n), lane(l) {
+    whole = w.rows >= bm && w.n0 + bn <= p.N;
+  }
+  // what the rows from r0 of the tile on need
+  __device__ void fetch(int r0) {
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      const int64_t row = m0 + min(r0 + 16 * g + (lane & 15), rows - 1);
+      const int t = target_of(p.loss, row);
+      target[g] = t < 0 ? kNone : t - p.loss.first;
+      if constexpr (KIND == kKindDlogits) {
+        lse[g] = p.loss.lse[row];
+        dloss[g] = p.loss.dloss[row];
+      }
+    }
+  }
+  // rows r .. r + 15 of the tile, the g-th sixteen of this wave
+  __device__ void rows16(int g, int r, v4f (&v)[4]) {
+    const int64_t m = m0 + r;
+    const int c0 = n + 4 * (lane >> 4);         // v[t][e] is column c0 + 16 t + e
+    if constexpr (KIND == kKindLse) {
+      float top = kLowest, sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = c0 + 16 * t + e;
+          if (c == target[g] && r + (lane & 15) < rows) p.loss.picked[m + (lane & 15)] = v[t][e];
+          if (!whole && c >= p.N) v[t][e] = -__builtin_inff();
+          top = fmaxf(top, v[t][e]);
+        }
+      top = over_row(top, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f((v[t][e] - top) * kLog2e);
+      sum = over_row(sum, [](float a, float b) { return a + b; });
+      if (lane < 16) reinterpret_cast<float2*>(turn)[16 * g + lane] = make_float2(top, sum);
+    } else {
+      v4f rest[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = c0 + 16 * t + e;
+          float d = __builtin_amdgcn_exp2f((v[t][e] - lse[g]) * kLog2e);
+          if (c == target[g]) d -= 1.f;
+          d = target[g] == kNone || (!whole && c >= p.N) ? 0.f : d * dloss[g];
+          v[t][e] = d;
+          rest[t][e] = bf16_rest(d);
+        }
+      const int N = (p.N + 7) & ~7;             // (zeros up to whole pieces)
+      store_bf16_rows(turn, v, (uint16_t*)p.d + m * p.ldd, p.ldd, rows - r, n, N, lane, whole);
+      if (p.loss.rest) store_bf16_rows(turn, rest, p.loss.rest + m * p.ldd, p.ldd, rows - r, n, N, lane, whole);
+    }
+  }
+  // After a barrier: the maxima and sums of WAVES waves side by side, whose pieces
+  // of LDS lie `apart`, joined and stored; row: this lane's of 16 GROUPS.
+  template <int WAVES>
+  __device__ static void merge(const BfProblem& p, const BfUnit& w, const uint8_t* turns, int apart, int row, int r0, int bn) {
+    if (r0 + row >= w.rows) return;
+    float2 v[WAVES];
+    float top = kLowest, sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < WAVES; ++q) {
+      v[q] = reinterpret_cast<const float2*>(turns + q * apart)[row];
+      top = fmaxf(top, v[q].x);
+    }
+#pragma unroll
+    for (int q = 0; q < WAVES; ++q) sum += v[q].y * __builtin_amdgcn_exp2f((v[q].x - top) * kLog2e);
+    p.loss.pieces[(int64_t)(w.n0 / bn) * p.M + w.m0 + r0 + row] = make_float2(top, sum);
+  }
+};
+
 }  // namespace fg8

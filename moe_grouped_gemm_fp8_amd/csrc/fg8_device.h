@@ -138,6 +138,12 @@ __device__ __forceinline__ float normal_cdf(float z, float* bell) {
   return z < 0.f ? n : 1.f - n;
 }
 
+// What rounding d to BF16 leaves (exact in FP32); 0 beside an infinity or NaN.
+__device__ __forceinline__ float bf16_rest(float d) {
+  const uint32_t hi = bf16x2(d, 0.f) << 16;
+  return (hi & 0x7f800000u) == 0x7f800000u ? 0.f : d - __uint_as_float(hi);
+}
+
 // ---------------------------------------------------------------- GEMM helpers
 // 16-byte chunk swizzle of LDS row r.  Measured with SQ_LDS_BANK_CONFLICT on
 // gfx950: (r >> 1) & 7 leaves the MFMA operand reads (one chunk of 16

@@ -86,6 +86,27 @@ int device_cu_count();
 enum BfMode : int { kBfDense = 0, kBfRowRuns = 1, kBfKRuns = 2 };
 enum BfAct : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
 
+// What a product's epilogue makes of its sums: the output tile, h of a gated
+// product, the statistics of a row's logits, or the logits' gradient.
+enum BfKind : int { kKindTile = 0, kKindGated = 1, kKindLse = 2, kKindDlogits = 3 };
+
+// The linear head's loss: rows' targets (class ids, int64 or int32; one outside
+// [0, classes) means none), and for
+//   kKindLse      each row's largest logit and sum of exponentials from it on,
+//                 [column tile][M], and its target's logit
+//   kKindDlogits  d, BF16 [M][ldd], the gradient of the logits of classes first ..
+//                 first + N - 1 (zeros up to a multiple of 8), and what its
+//                 rounding left (NULL: not wanted), from lse and dloss [M]
+struct BfLoss {
+  const void* targets;
+  int targets64, classes, first;
+  float2* pieces;
+  float* picked;
+  const float* lse;
+  const float* dloss;
+  uint16_t* rest;
+};
+
 struct BfProblem {
   const uint16_t* a;            // [M][K], or [K][M] if a_kmajor
   const uint16_t* b;            // [N][K], or [K][N] if b_kmajor
@@ -106,13 +127,14 @@ struct BfProblem {
   int64_t ldr;
   uint16_t* z;                  // the value before the activation, BF16
   int64_t ldz;
-  int add;                      // both operands k-major, FP32: D += the product
-  int gated;                    // B, both k-contiguous: N / 2 gate rows over N / 2 up rows; D and z as GatedOut
+  int add;                      // B k-major, FP32: D += the product
   int grid;                     // workgroups of a persistent launch (set by the launcher)
   // split k (dense)
   int splits;
   float* partial;
   int32_t* counters;
+  int kind;                     // BfKind; gated: B is N / 2 gate rows over N / 2 up rows, D has N / 2 columns
+  BfLoss loss;
 };
 struct BfTile {
   int cfg, bm, bn, splits;
@@ -153,6 +175,11 @@ hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const uint16_t*
 // act'(z_gate), then dh act(z_gate), then zeros up to ldz.  rest: as above.
 hipError_t launch_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* z, int act, int64_t m,
                                  int64_t n, bool rest, uint16_t* dz, int64_t ldz, hipStream_t stream);
+
+// loss and lse [m] from kKindLse's pieces [tiles][m] and target logits.
+hipError_t launch_loss_finish(const BfLoss& s, int64_t tiles, int64_t m, float* loss, float* lse, hipStream_t stream);
+// n floats rounded to BF16.
+hipError_t launch_round_bf16(const float* x, int64_t n, uint16_t* y, hipStream_t stream);
 
 // --------------------------------------------------------------- layer norm
 int64_t layer_norm_teams(int64_t rows, int64_t cols, bool bf16, int num_cus);

@@ -237,8 +237,9 @@ __device__ __forceinline__ bool last_of_splits(const BfProblem& p, const BfUnit&
   return *last;
 }
 // ------------------------------------------------------------------ kernel
-template <class C, bool AK, bool BK, int MODE, bool ADD = false, bool GATED = false>
+template <class C, bool AK, bool BK, int MODE, bool ADD = false, int KIND = kKindTile>
 __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
+  constexpr bool GATED = KIND == kKindGated;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::STAGES * C::STAGE_BYTES];
   __shared__ int last;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -348,6 +349,21 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void bf16_kernel(BfProblem p) {
         up[t] = acc[i][COLS + t];
       }
       out.rows16(wm0 + 16 * i, gate, up);
+    }
+  } else if constexpr (KIND != kKindTile) {
+    typedef LossOut<KIND, C::TM> Out;
+    static_assert(C::WN == 64 && C::WAVES * Out::kTurn <= C::STAGES * C::STAGE_BYTES && C::WM * 8 <= Out::kTurn);
+    Out out(p, w, C::BM, C::BN, wn0, smem + wave * Out::kTurn, lane);
+    out.fetch(wm0);
+    __syncthreads();      // every wave is done with the stages
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i) out.rows16(i, wm0 + 16 * i, acc[i]);
+    if constexpr (KIND == kKindLse) {
+      __syncthreads();
+      // (waves w and w + WAVES_M hold the same rows; the first WAVES_M join them)
+      if (wave < C::WAVES_M)
+        for (int r = lane; r < C::WM; r += 64)
+          Out::template merge<C::WAVES_N>(p, w, smem + wave * Out::kTurn, C::WAVES_M * Out::kTurn, r, wm0, C::BN);
     }
   } else if constexpr (C::WN == 64) {
     constexpr bool EPI = MODE == kBfDense && !AK && !BK;
@@ -613,11 +629,12 @@ __device__ __forceinline__ void phase_barrier() {
 // take 0.31: the two add up whatever the order of the tiles (experts mixed over
 // the XCDs, other numbers of tiles together on one, staggered starts and two
 // workgroups a CU measured within 2% or slower).
-template <bool AK, bool BK, int MODE, bool EPI, bool ADD = false, bool GATED = false>
+template <bool AK, bool BK, int MODE, bool EPI, bool ADD = false, int KIND = kKindTile>
 __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
+  constexpr bool GATED = KIND == kKindGated, LOSS = KIND == kKindLse || KIND == kKindDlogits;
   typedef HalfTile<AK, 64> HalfA;
   typedef std::conditional_t<GATED, GatedHalf, HalfTile<BK, 32>> HalfB;
-  typedef std::conditional_t<GATED, GatedOut<2>, TileOut<EPI, ADD>> Out;
+  typedef std::conditional_t<GATED, GatedOut<2>, std::conditional_t<LOSS, LossOut<KIND, 8>, TileOut<EPI, ADD>>> Out;
   constexpr uint32_t kHalf = HalfA::BYTES;         // LDS: per stage A0, A1, B0, B1
   constexpr uint32_t kTurns = 8 * kHalf, kTable = kTurns + 8 * Out::kTurn;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kTable + (MODE == kBfRowRuns ? sizeof(RunTable) : 0)];
@@ -764,6 +781,14 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(out.bias[i]));
     }
+    if constexpr (LOSS) {
+      out.fetch(grp * 128);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        asm volatile("" : "+v"(out.target[i]));
+        if constexpr (KIND == kKindDlogits) asm volatile("" : "+v"(out.lse[i]), "+v"(out.dloss[i]));
+      }
+    }
     // the next unit's first copies, under this one's epilogue
     BfUnit next{};
     u += G;
@@ -785,6 +810,9 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
       if constexpr (GATED) {
         v4f gate[2] = {acc[ha][i][0][0], acc[ha][i][0][1]}, up[2] = {acc[ha][i][1][0], acc[ha][i][1][1]};
         out.rows16(grp * 128 + 16 * g, gate, up);
+      } else if constexpr (LOSS) {
+        v4f v[4] = {acc[ha][i][0][0], acc[ha][i][0][1], acc[ha][i][1][0], acc[ha][i][1][1]};
+        out.rows16(g, grp * 128 + 16 * g, v);
       } else {
         v4f v[4] = {acc[ha][i][0][0], acc[ha][i][0][1], acc[ha][i][1][0], acc[ha][i][1][1]};
         out.rows16(grp * 128 + 16 * g, v, res);
@@ -794,6 +822,11 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
         res[1] = ahead[1];
       }
     }
+    if constexpr (KIND == kKindLse) {
+      __syncthreads();
+      // (waves 4 grp .. 4 grp + 3 hold the same 128 rows; the first two of them join them)
+      if (q < 2) Out::template merge<4>(p, w, smem + kTurns + 4 * grp * Out::kTurn, Out::kTurn, 64 * q + here, 128 * grp, 256);
+    }
     if (u >= total) return;
     w = next;
   }
@@ -802,17 +835,18 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
 // ------------------------------------------------------------------- host
 // Tile configurations.  kBig: bf16_big_kernel; kFew: bf16_few_kernel; the
 // others: bf16_kernel with two workgroups a CU.
-enum { kBig = 0, kDuo, kMid, kHigh, kLow, kFlat, kThin, kFew, kConfigs };
+enum { kBig = 0, kDuo, kMid, kHigh, kLow, kFlat, kThin, kFew, kSlab, kConfigs };
 using BfDuo = BfCfg<128, 256, 1, 4, 3, 2, 32>;
 using BfMid = BfCfg<128, 128, 2, 2, 2, 2>;
 using BfHigh = BfCfg<128, 64, 2, 2, 3, 2>;
 using BfLow = BfCfg<64, 64, 2, 2, 4, 2>;
 using BfFlat = BfCfg<32, 64, 2, 2, 5, 2>;
 using BfThin = BfCfg<16, 64, 1, 4, 6, 2>;
-constexpr int kBm[kConfigs] = {256, 128, 128, 128, 64, 32, 16, 16};
-constexpr int kBn[kConfigs] = {256, 256, 128, 64, 64, 64, 64, 16};
+using BfSlab = BfCfg<64, 128, 2, 2, 3, 2>;
+constexpr int kBm[kConfigs] = {256, 128, 128, 128, 64, 32, 16, 16, 64};
+constexpr int kBn[kConfigs] = {256, 256, 128, 64, 64, 64, 64, 16, 128};
 constexpr int kThreads[kConfigs] = {512, BfDuo::THREADS, BfMid::THREADS, BfHigh::THREADS,
-                                    BfLow::THREADS, BfFlat::THREADS, BfThin::THREADS, 512};
+                                    BfLow::THREADS, BfFlat::THREADS, BfThin::THREADS, 512, BfSlab::THREADS};
 
 namespace {
 
@@ -838,13 +872,24 @@ template <int MODE>
 hipError_t launch_gated(BfProblem p, const BfTile& t, hipStream_t stream) {
   const unsigned units = grid_of(p, t.bm, t.bn);
   if (t.cfg == kFew) return start(bf16_few_kernel<MODE, true>, p, units, 512, stream);
-  if (t.cfg == kFlat) return start(bf16_kernel<BfFlat, false, false, MODE, false, true>, p, units, BfFlat::THREADS, stream);
-  if (t.cfg == kLow) return start(bf16_kernel<BfLow, false, false, MODE, false, true>, p, units, BfLow::THREADS, stream);
-  if (t.cfg == kHigh) return start(bf16_kernel<BfHigh, false, false, MODE, false, true>, p, units, BfHigh::THREADS, stream);
-  if (t.cfg == kMid) return start(bf16_kernel<BfMid, false, false, MODE, false, true>, p, units, BfMid::THREADS, stream);
+  if (t.cfg == kFlat) return start(bf16_kernel<BfFlat, false, false, MODE, false, kKindGated>, p, units, BfFlat::THREADS, stream);
+  if (t.cfg == kLow) return start(bf16_kernel<BfLow, false, false, MODE, false, kKindGated>, p, units, BfLow::THREADS, stream);
+  if (t.cfg == kHigh) return start(bf16_kernel<BfHigh, false, false, MODE, false, kKindGated>, p, units, BfHigh::THREADS, stream);
+  if (t.cfg == kMid) return start(bf16_kernel<BfMid, false, false, MODE, false, kKindGated>, p, units, BfMid::THREADS, stream);
   const unsigned cus = (unsigned)device_cu_count();
   p.grid = (int)(units < cus ? units : cus);
-  return start(bf16_big_kernel<false, false, MODE, false, false, true>, p, p.grid, 512, stream);
+  return start(bf16_big_kernel<false, false, MODE, false, false, kKindGated>, p, p.grid, 512, stream);
+}
+
+// A linear head's logits.
+template <int KIND>
+hipError_t launch_loss(BfProblem p, const BfTile& t, hipStream_t stream) {
+  const unsigned units = grid_of(p, t.bm, t.bn);
+  if (t.cfg == kSlab) return start(bf16_kernel<BfSlab, false, false, kBfDense, false, KIND>, p, units, BfSlab::THREADS, stream);
+  if (t.cfg == kMid) return start(bf16_kernel<BfMid, false, false, kBfDense, false, KIND>, p, units, BfMid::THREADS, stream);
+  const unsigned cus = (unsigned)device_cu_count();
+  p.grid = (int)(units < cus ? units : cus);
+  return start(bf16_big_kernel<false, false, kBfDense, false, false, KIND>, p, p.grid, 512, stream);
 }
 
 template <bool AK, bool BK, int MODE>
@@ -868,12 +913,12 @@ hipError_t launch_tile(BfProblem p, const BfTile& t, hipStream_t stream) {
   const unsigned cus = (unsigned)device_cu_count();
   p.grid = (int)(units < cus ? units : cus);
   if constexpr (MODE == kBfKRuns) {
-    if (p.add) return start(bf16_big_kernel<AK, BK, MODE, false, true>, p, p.grid, 512, stream);
+    if (p.add) return start(bf16_big_kernel<AK, BK, MODE, false, kKindGated>, p, p.grid, 512, stream);
   }
-  if constexpr (MODE == kBfDense && AK && BK) {
+  if constexpr (MODE == kBfDense && BK) {
     if (p.add)
       return t.cfg == kMid ? start(bf16_kernel<BfMid, AK, BK, MODE, true>, p, units, BfMid::THREADS, stream)
-                           : start(bf16_big_kernel<AK, BK, MODE, false, true>, p, p.grid, 512, stream);
+                           : start(bf16_big_kernel<AK, BK, MODE, false, kKindGated>, p, p.grid, 512, stream);
   }
   if (t.cfg == kMid) return start(bf16_kernel<BfMid, AK, BK, MODE>, p, units, BfMid::THREADS, stream);
   if constexpr (MODE == kBfDense && !AK && !BK) {
@@ -901,9 +946,14 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
   // within its backward pass, dW of 4096 x 4096 x 2048 169 for 182 within its.
   // At 560 to 640: 1280 x 7168 x 2048 42 for 56, 4096 x 2560 x 7168 129 for 182,
   // dW of 4000 x 5000 x 2048 207 for 239.
-  const bool dense = p.mode == kBfDense;
+  const bool dense = p.mode == kBfDense, gated = p.kind == kKindGated;
+  const bool loss = p.kind == kKindLse || p.kind == kKindDlogits;
   const bool second_round = units(kMid) > 2 * cus;
-  if (p.a_kmajor) {
+  if (loss) {
+    t.cfg = rows <= 64 ? kSlab : second_round ? kBig : kMid;
+  } else if (p.add && !p.a_kmajor) {      // (the tiles that add)
+    t.cfg = second_round ? kBig : kMid;
+  } else if (p.a_kmajor) {
     // Weight gradients of runs: the big tile from two tiles and 64 of its steps
     // a CU on (8 runs of 4096 rows, 4096 x 2048: 461-482 for 520-529 and
     // 562-578; 8 of 1024 144-152 for 149-155 and 158-165; 16 of 512 175-200 for
@@ -922,9 +972,9 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
     // 1024 rows (256, 296) 89 for 82, of 1024 rows, 4096 x 2048 (512, 592) 136
     // for 145.  Runs of whole tiles: 41 for 34, 56 for 65, 104 for 137.
     t.cfg = kBig;
-  } else if (rows <= 8 && !p.b_kmajor && p.K <= 4096 && units(kFew) <= (p.gated ? 4 : 2) * cus) {
+  } else if (rows <= 8 && !p.b_kmajor && p.K <= 4096 && units(kFew) <= (gated ? 4 : 2) * cus) {
     t.cfg = kFew;      // 1 x 1024 x 2048 5.5 for 6.6; 1 x 2112 x 7168 12.8 for 11.2
-  } else if (rows <= (dense ? 16 : 8) && !p.gated) {   // (its waves own too few columns for both sums)
+  } else if (rows <= (dense ? 16 : 8) && !gated) {   // (its waves own too few columns for both sums)
     t.cfg = kThin;     // 16 x 2112 x 7168 11.3 for 12.2; 32 runs of 16 rows on average 366 for 345
   } else if (rows <= 32) {
     t.cfg = kFlat;     // 32 x 2112 x 7168 12.3 for 13.7
@@ -935,11 +985,11 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
     t.cfg = rows <= 256 ? kLow : kHigh;
   }
   t.bm = kBm[t.cfg];
-  t.bn = kBn[t.cfg] * (p.gated && t.cfg == kFew ? 2 : 1);   // (16 gate and 16 up rows)
+  t.bn = kBn[t.cfg] * (gated && t.cfg == kFew ? 2 : 1);   // (16 gate and 16 up rows)
   t.threads = kThreads[t.cfg];
   t.persistent = t.cfg == kBig;
   t.splits = 1;
-  if (dense && t.cfg != kBig && t.cfg != kFew) {
+  if (dense && t.cfg != kBig && t.cfg != kFew && !loss) {
     // One workgroup a CU; two where several row tiles read the same weights
     // (64 x 2112 x 7168 14.1 in 6 splits, 16.2 in 12; 128 x 2112 x 7168 18.9
     // in 6, 19.8 in 3), and five steps a split at least.
@@ -963,7 +1013,9 @@ size_t bf16_workspace_bytes(const BfProblem& p, int cus) {
 
 hipError_t launch_bf16(BfProblem p, const BfTile& t, hipStream_t stream) {
   p.splits = t.splits;
-  if (p.gated) return p.mode == kBfRowRuns ? launch_gated<kBfRowRuns>(p, t, stream) : launch_gated<kBfDense>(p, t, stream);
+  if (p.kind == kKindLse) return launch_loss<kKindLse>(p, t, stream);
+  if (p.kind == kKindDlogits) return launch_loss<kKindDlogits>(p, t, stream);
+  if (p.kind == kKindGated) return p.mode == kBfRowRuns ? launch_gated<kBfRowRuns>(p, t, stream) : launch_gated<kBfDense>(p, t, stream);
   if (p.mode == kBfRowRuns)
     return p.b_kmajor ? launch_tile<false, true, kBfRowRuns>(p, t, stream)
                       : launch_tile<false, false, kBfRowRuns>(p, t, stream);

@@ -120,7 +120,7 @@ __global__ __launch_bounds__(512, 2) void int4_kernel(Int4Problem q) {
   // weight row that tile t starts at (gated: the first half of the tiles are
   // gate rows, the others the up rows of the same columns)
   auto row_of = [&](int t) {
-    if (!p.gated) return w.n0 + 16 * t;
+    if (p.kind != kKindGated) return w.n0 + 16 * t;
     return t < TN / 2 ? w.n0 / 2 + 16 * t : half + w.n0 / 2 + 16 * (t - TN / 2);
   };
   __amdgpu_buffer_rsrc_t wr[TN];
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(512, 2) void int4_kernel(Int4Problem q) {
     for (int u = 1; u < waves; ++u) v += sums[u][at][lane];
     return v;
   };
-  if (p.gated) {
+  if (p.kind == kKindGated) {
     if constexpr (TN > 1) {
       for (int u = wave; u < TM * (TN / 2); u += waves) {
         const int m = u / (TN / 2), t = u % (TN / 2);
@@ -265,7 +265,7 @@ Int4Tile int4_tile(const BfProblem& p, int cus) {
   const int64_t rows = p.mode == kBfRowRuns ? (p.M + p.groups - 1) / p.groups : p.M;
   t.tm = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   t.tn = 2;
-  if (!p.gated && t.tm == 1 && p.mode == kBfDense) {
+  if (p.kind != kKindGated && t.tm == 1 && p.mode == kBfDense) {
     if ((int64_t)p.N < 16 * 2 * cus) t.tn = 1;
     else if ((int64_t)p.N >= 16 * 4 * cus) t.tn = 4;
   }

@@ -1,0 +1,68 @@
+// What the softmax cross entropy of a linear head needs beside its products: the
+// rows' statistics joined over the vocabulary, and the rounding of dx's sums.
+//
+//   lse = M + log sum over tiles of s_t e^(m_t - M),  M = max over tiles of m_t
+//   loss = lse - (the target's logit), 0 for a row without a target
+#include <algorithm>
+
+#include "bf16_tile.h"
+
+namespace fg8 {
+
+namespace {
+
+// Sixteen waves to 64 rows, a lane a row: a wave reads every sixteenth tile's
+// pieces, and the waves join in LDS in a fixed order.
+__global__ __launch_bounds__(1024) void loss_finish_kernel(BfLoss s, int tiles, int64_t m, float* __restrict__ loss,
+                                                           float* __restrict__ lse) {
+  __shared__ float2 part[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int64_t r0 = (int64_t)blockIdx.x * 64; r0 < m; r0 += (int64_t)gridDim.x * 64) {
+    const int64_t row = r0 + lane;
+    float top = kLowest, sum = 0.f;
+    auto add = [&](float2 v) {
+      const float t = fmaxf(top, v.x);
+      sum = sum * __builtin_amdgcn_exp2f((top - t) * kLog2e) + v.y * __builtin_amdgcn_exp2f((v.x - t) * kLog2e);
+      top = t;
+    };
+    if (row < m) {
+#pragma unroll 4
+      for (int t = wave; t < tiles; t += 16) add(s.pieces[t * m + row]);
+    }
+    part[wave][lane] = make_float2(top, sum);
+    __syncthreads();
+    if (wave == 0 && row < m) {
+      for (int w = 1; w < 16; ++w) add(part[w][lane]);
+      const float l = logf(sum);
+      lse[row] = top + l;
+      // (the maximum and the target's logit first: where the target dominates
+      // they cancel exactly)
+      loss[row] = target_of(s, row) < 0 ? 0.f : (top - s.picked[row]) + l;
+    }
+    __syncthreads();
+  }
+}
+
+// (n is a multiple of 8)
+__global__ __launch_bounds__(256) void round_kernel(const float* __restrict__ x, int64_t n, uint16_t* __restrict__ y) {
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
+    const float4 a = *reinterpret_cast<const float4*>(x + i), b = *reinterpret_cast<const float4*>(x + i + 4);
+    *reinterpret_cast<uint4*>(y + i) = make_uint4(bf16x2(a.x, a.y), bf16x2(a.z, a.w), bf16x2(b.x, b.y), bf16x2(b.z, b.w));
+  }
+}
+
+constexpr int64_t kMostBlocks = 1 << 16;
+
+}  // namespace
+
+hipError_t launch_loss_finish(const BfLoss& s, int64_t tiles, int64_t m, float* loss, float* lse, hipStream_t stream) {
+  hipLaunchKernelGGL(loss_finish_kernel, dim3((unsigned)std::min((m + 63) / 64, kMostBlocks)), dim3(1024), 0, stream, s, (int)tiles, m, loss, lse);
+  return hipGetLastError();
+}
+
+hipError_t launch_round_bf16(const float* x, int64_t n, uint16_t* y, hipStream_t stream) {
+  hipLaunchKernelGGL(round_kernel, dim3((unsigned)std::min((n + 2047) / 2048, kMostBlocks)), dim3(256), 0, stream, x, n, y);
+  return hipGetLastError();
+}
+
+}  // namespace fg8

@@ -499,12 +499,6 @@ __device__ __forceinline__ float act_gradient(int act, float z, float dy) {
   return dy;
 }
 
-// What rounding d to BF16 leaves (exact in FP32); 0 beside an infinity or NaN.
-__device__ __forceinline__ float bf16_rest(float d) {
-  const uint32_t hi = bf16x2(d, 0.f) << 16;
-  return (hi & 0x7f800000u) == 0x7f800000u ? 0.f : d - __uint_as_float(hi);
-}
-
 constexpr int kActCols = 512;   // columns of a workgroup: eight a lane
 
 // Bound by HBM: dy and z read, dz written once (4096 x 7168 0.036 ms, 4.9 TB/s).

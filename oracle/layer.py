@@ -1,7 +1,7 @@
 """Plain float64 forms of what an MoE layer computes around its FP8 products:
 expert products over ragged row runs, the dense product with an epilogue, the
-gated feed-forward products, layer norm and the combine step, each with its
-gradients.  Loops and textbook
+gated feed-forward products, the cross entropy of a linear head, layer norm and
+the combine step, each with its gradients.  Loops and textbook
 formulas; no code shared with the HIP path.
 """
 import math
@@ -90,6 +90,31 @@ def gated_dz(name, dh, z):
     dh, z = _f64(dh, z)
     n = z.shape[1] // 2
     return np.concatenate([dh * z[:, n:] * slope(name, z[:, :n]), dh * activation(name, z[:, :n])], 1)
+
+
+# ------------------------------------------ cross entropy of a linear head
+def cross_entropy(logits, targets):
+    """(loss, lse) of each row; 0 for a row whose target is no class."""
+    logits = np.asarray(logits, np.float64)
+    top = logits.max(1)
+    lse = top + np.log(np.exp(logits - top[:, None]).sum(1))
+    loss = np.zeros(len(lse))
+    for r, t in enumerate(targets):
+        if 0 <= t < logits.shape[1]:
+            loss[r] = lse[r] - logits[r, t]
+    return loss, lse
+
+
+def cross_entropy_backward(dloss, logits, targets, lse):
+    """The logits' gradient."""
+    dloss, logits, lse = _f64(dloss, logits, lse)
+    d = np.zeros_like(logits)
+    for r, t in enumerate(targets):
+        if 0 <= t < logits.shape[1]:
+            d[r] = np.exp(logits[r] - lse[r])
+            d[r, t] -= 1
+            d[r] *= dloss[r]
+    return d
 
 
 # --------------------------------------------------------------- layer norm
