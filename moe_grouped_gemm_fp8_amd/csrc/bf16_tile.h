@@ -11,8 +11,25 @@ namespace fg8 {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
+constexpr int kLdsBytes = 160 * 1024;          // of a CU
 constexpr int kBK = 64;                       // k depth of one step
 constexpr uint32_t kNowhere = 0x80000000u;    // an offset past every buffer resource
+
+// A copy of 16 bytes a lane into LDS at `lds` + 16 * lane.  The instruction
+// writes no VGPR; the wait state between the write of m0 and its use is ours
+// to keep inside an asm block.
+__device__ __forceinline__ void copy16(v4i rsrc, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(off), "s"(rsrc), "s"(lds)
+               : "memory", "m0");
+}
+
+__device__ __forceinline__ v4i resource(const void* base, int64_t bytes) {
+  const uint64_t a = uniform((uint64_t)base);
+  const int n = uniform((int)(bytes < 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : bytes));
+  return v4i{(int)(uint32_t)a, (int)((uint32_t)(a >> 32) & 0xffffu), n, kBufferDword3};
+}
 
 // ------------------------------------------------------------ work units
 struct BfUnit {

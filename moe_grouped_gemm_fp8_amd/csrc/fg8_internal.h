@@ -148,9 +148,9 @@ hipError_t launch_bf16(BfProblem p, const BfTile& t, hipStream_t stream);
 
 // ------------------------------------------------------ weights in 4 bits
 // p: a, d, sizes (N weight rows), runs and epilogue as the BF16 products', b
-// unused; `units` workgroups of `threads`, each 16 tm rows by 16 tn weight rows.
+// unused; `units` workgroups of `threads`.
 struct Int4Tile {
-  int tm, tn, threads;
+  int cfg, threads;
   int64_t units;
 };
 Int4Tile int4_tile(const BfProblem& p, int num_cus);

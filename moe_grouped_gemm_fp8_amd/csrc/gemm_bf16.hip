@@ -48,7 +48,6 @@ namespace fg8 {
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
-constexpr int kLdsBytes = 160 * 1024;          // of a CU
 
 template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, int OCC_, int DEPTH_ = kBK>
 struct BfCfg {
@@ -63,22 +62,6 @@ struct BfCfg {
   // (the stages, and bf16_kernel's flag beside them)
   static_assert(OCC * (STAGES * STAGE_BYTES + 16) <= kLdsBytes, "OCC workgroups share the LDS of a CU");
 };
-
-// A copy of 16 bytes a lane into LDS at `lds` + 16 * lane.  The instruction
-// writes no VGPR; the wait state between the write of m0 and its use is ours
-// to keep inside an asm block.
-__device__ __forceinline__ void copy16(v4i rsrc, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               :
-               : "v"(off), "s"(rsrc), "s"(lds)
-               : "memory", "m0");
-}
-
-__device__ __forceinline__ v4i resource(const void* base, int64_t bytes) {
-  const uint64_t a = uniform((uint64_t)base);
-  const int n = uniform((int)(bytes < 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : bytes));
-  return v4i{(int)(uint32_t)a, (int)((uint32_t)(a >> 32) & 0xffffu), n, kBufferDword3};
-}
 
 // One operand's tile: BX rows (m or n) by 64 k.  KMAJOR: memory is [k][x].
 template <bool KMAJOR, int BX, int WAVES, int DEPTH = kBK>

@@ -16,64 +16,62 @@ namespace fg8 {
 namespace {
 
 // ------------------------------------------------------- few-row products
-// A workgroup owns 16 TM rows and 16 TN weight rows; its waves take chunks of
-// 128 k in turn and load both operands straight into registers, the next chunk
-// ahead of the one being multiplied; their sums meet in LDS at the end.
+// A workgroup is WK x WN waves.  A wave owns 16 TM rows by 16 TN weight rows (its
+// place among the WN) and every WK-th chunk of 256 k, a 128-byte line of codes a
+// row; the WK waves' sums meet in LDS at the end.  Codes, scales and x of a chunk
+// are copied from global memory straight into LDS, S - 1 chunks ahead: what is in
+// flight takes no registers, and nothing waits for it but one counter.  Codes and
+// scales are the wave's own; x is shared by the WN waves of a chunk (a barrier a
+// chunk, none where WN is 1).
 //
-// A lane loads 16 bytes of codes, 32 k of one weight row; four swaps between the
+// A lane reads 16 bytes of codes, 32 k of one weight row; four swaps between the
 // four groups of sixteen lanes turn that into the layout of four MFMAs of 32 k
 // each (lane i + 16 g: row i, k = 8 g .. 8 g + 7), so a group of 32 k or more is
 // whole MFMAs.  A code goes into the upper four mantissa bits of a BF16 whose
-// exponent is 16's: 16 + code, one shift and one bit operation for two weights.
-// Pairs come out as k, k + 4 of a lane's eight; x's pairs are put in that order.
+// exponent is 16's: 16 + code, one product and one bit operation for two weights.
 // The 24 that every weight is too large is taken off with an MFMA against a
 // constant -24, once for all the tiles that share x: the group's sum then starts
 // from -24 sum(x).  Every value and product is exact; what the detour adds is
-// FP32 rounding of partial sums at the size of 24 |x| for 8 |x|.
+// FP32 rounding of partial sums at the size of 24 |x| for 8 |x|.  x goes in as the
+// first operand, so a lane holds rows of one weight column and needs one scale.
 struct Int4Problem {
   BfProblem p;             // a: x; N: weight rows; d, epilogue, runs
   const uint8_t* codes;
   const void* scales;
 };
 
-template <bool BF16>
-__device__ __forceinline__ v4i load_scales(const void* s, int64_t at, int left, bool four) {
-  // four: rows of scales are whole fours of columns
-  v4i v = {0, 0, 0, 0};
-  if constexpr (BF16) {
-    const uint16_t* q = (const uint16_t*)s + at;
-    if (four) {
-      if (left > 0) {
-        const uint2 u = *reinterpret_cast<const uint2*>(q);
-        v[0] = (int)u.x;
-        v[1] = (int)u.y;
-      }
-    } else {
-      uint32_t e[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = i < left ? q[i] : 0;
-      v[0] = (int)(e[0] | e[1] << 16);
-      v[1] = (int)(e[2] | e[3] << 16);
-    }
+// The copies of bf16_tile.h with the non-temporal hint (weights are read once),
+// and of four bytes a lane.
+__device__ __forceinline__ void copy16_nt(v4i rsrc, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds"
+               :
+               : "v"(off), "s"(rsrc), "s"(lds)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void copy4(v4i rsrc, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(off), "s"(rsrc), "s"(lds)
+               : "memory", "m0");
+}
+
+// A lane holds column i's scale of group g of four, or of group g / 2 of two; this
+// hands every lane all of them.
+template <int NG>
+__device__ __forceinline__ void spread_scales(uint32_t v, float* s) {
+  typedef unsigned u2 __attribute__((ext_vector_type(2)));
+  const u2 a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  if constexpr (NG == 2) {
+    s[0] = __uint_as_float(a[0]);
+    s[1] = __uint_as_float(a[1]);
   } else {
-    const int* q = (const int*)s + at;
-    if (four) {
-      if (left > 0) v = *reinterpret_cast<const v4i*>(q);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) v[i] = q[i];
+    for (int h = 0; h < 2; ++h) {
+      const u2 b = __builtin_amdgcn_permlane16_swap(a[h], a[h], false, false);
+      s[2 * h] = __uint_as_float(b[0]);
+      s[2 * h + 1] = __uint_as_float(b[1]);
     }
   }
-  return v;
-}
-template <bool BF16>
-__device__ __forceinline__ v4f scale_values(v4i v) {
-  if constexpr (BF16)
-    return v4f{__uint_as_float((uint32_t)v[0] << 16), __uint_as_float((uint32_t)v[0] & 0xffff0000u),
-               __uint_as_float((uint32_t)v[1] << 16), __uint_as_float((uint32_t)v[1] & 0xffff0000u)};
-  else
-    return __builtin_bit_cast(v4f, v);
 }
 
 // Word 4 g + j of sixteen, held by lane group g as its word j, to word 4 j + g.
@@ -86,83 +84,143 @@ __device__ __forceinline__ void transpose_words(v4i& w) {
   w = v4i{(int)lo[0], (int)lo[1], (int)hi[0], (int)hi[1]};
 }
 
-// Eight codes as BF16 16 + code: elements 0, 4, 1, 5, 2, 6, 3, 7.
-__device__ __forceinline__ v8bf codes_plus_16(uint32_t w) {
-  constexpr uint32_t kCode = 0x00780078u, k16 = 0x41804180u;
-  const v4i v = {(int)((w << 3 & kCode) | k16), (int)((w >> 1 & kCode) | k16), (int)((w >> 5 & kCode) | k16),
-                 (int)((w >> 9 & kCode) | k16)};
-  return __builtin_bit_cast(v8bf, v);
-}
-// x's elements in that order
-__device__ __forceinline__ v8bf paired(v4i x) {
-  const v4i v = {(int)__builtin_amdgcn_perm(x[2], x[0], 0x05040100u), (int)__builtin_amdgcn_perm(x[2], x[0], 0x07060302u),
-                 (int)__builtin_amdgcn_perm(x[3], x[1], 0x05040100u), (int)__builtin_amdgcn_perm(x[3], x[1], 0x07060302u)};
-  return __builtin_bit_cast(v8bf, v);
-}
+// Eight codes as BF16 16 + code, two a byte: a byte times 2^15 + 2^3 has its low
+// half in bits 3 .. 6 and its high half in bits 19 .. 22.  The constants come from
+// registers: as literals they keep the two bit operations apart.
+struct CodeBits {
+  uint32_t mask = 0x00780078u, sixteen = 0x41804180u, twice = 0x8008u;
+  __device__ CodeBits() { asm("" : "+s"(mask), "+v"(sixteen), "+v"(twice)); }
+  __device__ v8bf plus_16(uint32_t w) const {
+    v4i v;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) v[p] = (int)((__umul24(w >> (8 * p) & 255u, twice) & mask) | sixteen);
+    return __builtin_bit_cast(v8bf, v);
+  }
+};
 
-template <int TM, int TN, int GROUP, bool SBF16>
-__global__ __launch_bounds__(512, 2) void int4_kernel(Int4Problem q) {
-  constexpr int NG = 128 / GROUP, GJ = GROUP / 32;      // groups of a chunk, MFMAs of a group
-  __shared__ v4f sums[8][TM * TN][64];
+// XR: rows of x that are copied (the least that hold the tile's rows).
+constexpr int kChunk = 256;
+template <int TM_, int XR_, int TN_, int WK_, int WN_, int S_>
+struct I4Cfg {
+  static constexpr int TM = TM_, XR = XR_, TN = TN_, WK = WK_, WN = WN_, S = S_;
+  static constexpr int WAVES = WK * WN, THREADS = 64 * WAVES, BM = 16 * TM, BN = 16 * TN * WN;
+  static constexpr int CODES = WAVES * TN * 2048, X = WK * XR * 512;
+  static constexpr int XCOPIES = XR / 2 / WN;          // of 1 KB, a wave's of a chunk
+  static constexpr int scale_copies(int group) { return kChunk / group > 4 ? 2 : 1; }
+  static constexpr int stage(int group) { return CODES + WAVES * TN * 256 * scale_copies(group) + X; }
+  static_assert(XR / 2 % WN == 0 && XR >= 2 && (XR == 16 * TM || (TM == 1 && XR < 16)), "every wave copies the same number");
+};
+
+template <class C, int GROUP, bool SBF16>
+__global__ __launch_bounds__(C::THREADS) void int4_kernel(Int4Problem q) {
+  constexpr int TM = C::TM, TN = C::TN, WK = C::WK, WN = C::WN, S = C::S;
+  constexpr int NG = 128 / GROUP, GJ = GROUP / 32;      // groups of 128 k, MFMAs of a group
+  constexpr int GC = 2 * NG, SC = C::scale_copies(GROUP);     // groups of a chunk, copies of their scales
+  constexpr int STAGE = C::stage(GROUP), SCALES = C::WAVES * TN * 256 * SC;
+  constexpr int COPIES = TN * (2 + SC) + C::XCOPIES;   // all of a wave's of a chunk
+  static_assert((S - 2) * COPIES < 64, "the counter of loads in flight");
+  static_assert(C::WAVES * TM * TN * 1024 <= S * STAGE && S * STAGE <= kLdsBytes, "sums in the stages, stages in the LDS");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
   const BfProblem& p = q.p;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int waves = blockDim.x >> 6, i = lane & 15, g = lane >> 4;
+  const int kg = wave / WN, wn = wave % WN, i = lane & 15, g = lane >> 4;
   BfUnit w;
-  if (!(p.mode == kBfRowRuns ? find_unit<16 * TM, 16 * TN, kBfRowRuns>(p, lane, w)
-                             : find_unit<16 * TM, 16 * TN, kBfDense>(p, lane, w)))
+  if (!(p.mode == kBfRowRuns ? find_unit<C::BM, C::BN, kBfRowRuns>(p, lane, w) : find_unit<C::BM, C::BN, kBfDense>(p, lane, w)))
     return;
+  const bool gated = p.kind == kKindGated;
   const int N = p.N, K = p.K, half = N / 2;
-  const int64_t expert = max(w.g, 0);
-  const int64_t row_bytes = K / 2, per_group = N;
-  const uint8_t* codes = q.codes + expert * N * row_bytes;
-  const int64_t scales0 = expert * per_group * (K / GROUP);
+  const int64_t expert = max(w.g, 0), row_bytes = K / 2;
 
-  // weight row that tile t starts at (gated: the first half of the tiles are
-  // gate rows, the others the up rows of the same columns)
+  // Weight row that tile t of this wave starts at (gated: the first half of the
+  // tiles are gate rows, the others the up rows of the same columns).
   auto row_of = [&](int t) {
-    if (p.kind != kKindGated) return w.n0 + 16 * t;
-    return t < TN / 2 ? w.n0 / 2 + 16 * t : half + w.n0 / 2 + 16 * (t - TN / 2);
+    if (!gated) return w.n0 + 16 * (wn * TN + t);
+    const int j = w.n0 / 2 + 16 * (wn * (TN / 2) + (t < TN / 2 ? t : t - TN / 2));
+    return t < TN / 2 ? j : half + j;
   };
-  __amdgpu_buffer_rsrc_t wr[TN];
-  int col[TN], left[TN];             // this lane's four columns of scales, and how many there are from them on
+  // Sources of the copies.  A row of codes is eight pieces of 16 bytes, a row of x 32;
+  // a copy of 1 KB is whole rows, piece l of it lane l's.  In LDS the pieces of a row
+  // are XORed with a function of it, which keeps the reads free of bank conflicts.
+  // Rows that do not exist, and k past the end, are no address.
+  const char* cfrom[TN];               // at this wave's chunk of the step to copy next
+  uint32_t coff[TN][2];
+  int cpart[2], col[TN];              // first k of a lane's piece in the chunk; its column of scales
+#pragma unroll
+  for (int h = 0; h < 2; ++h) cpart[h] = ((lane & 7) ^ swz(8 * h + (lane >> 3))) * 32;
 #pragma unroll
   for (int t = 0; t < TN; ++t) {
     const int r = uniform(row_of(t));
-    const int64_t bytes = r < N ? (N - r) * row_bytes : 0;
-    wr[t] = buffer_rsrc(uniform((const void*)(codes + (r < N ? r : 0) * row_bytes)),
-                        (uint32_t)(bytes > 0x7fffffff ? 0x7fffffff : bytes));
-    col[t] = r + 4 * g;
-    left[t] = N - col[t];
+    cfrom[t] = (const char*)q.codes + (expert * N + (r < N ? r : 0)) * row_bytes + kg * (kChunk / 2);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = 8 * h + (lane >> 3);
+      coff[t][h] = row < N - r ? (uint32_t)(row * (int)row_bytes + cpart[h] / 2) : kNowhere;
+    }
+    col[t] = r + i;
   }
-  const bool four = N % 4 == 0;
-  const uint32_t wo = (uint32_t)(i * (int)row_bytes + 16 * g);
-  const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(uniform((const void*)(p.a + w.m0 * p.lda)), 0x7fffffff);
-  uint32_t xo[TM];
+  const char* xfrom = (const char*)(p.a + w.m0 * p.lda) + kg * (kChunk * 2);
+  uint32_t xoff[C::XCOPIES];
+  int xpart[C::XCOPIES];
 #pragma unroll
-  for (int m = 0; m < TM; ++m)
-    xo[m] = 16 * m + i < w.rows ? (uint32_t)((16 * m + i) * (int)p.lda + 8 * g) * 2 : kNowhere;
+  for (int u = 0; u < C::XCOPIES; ++u) {
+    const int r = (wn * C::XCOPIES + u) * 2 + (lane >> 5), piece = (lane & 31) ^ (r & 15);
+    xoff[u] = r < w.rows ? (uint32_t)(r * (int)p.lda + piece * 8) * 2 : kNowhere;
+    xpart[u] = piece * 8;
+  }
+  // Scales: elements from the expert's first on, copied as the dwords that hold them
+  // (two BF16 ones each).  The very last of an odd number of BF16 ones is in no whole
+  // dword and is kept aside.  A lane's copy u holds column i's of group 4 u + g of the
+  // chunk, or of group g / 2 where a chunk has two.
+  constexpr int SIZE = SBF16 ? 2 : 4;
+  const int64_t per_expert = (int64_t)N * (K / GROUP), all = per_expert * (p.mode == kBfRowRuns ? p.groups : 1);
+  const int group0 = GC == 2 ? g >> 1 : g, last_group = K / GROUP - 1;
+  const bool odd_end = SBF16 && (all & 1) && (expert + 1) * per_expert == all;
+  uint32_t slast = 0;
+  if (odd_end) slast = (uint32_t)((const uint16_t*)q.scales)[all - 1] << 16;
+  int64_t sfrom = expert * per_expert + (int64_t)kg * GC * N;      // of the step to copy next
+  const int odd = SBF16 ? (int)(sfrom & 1) : 0;                    // (a chunk has an even number of groups)
+  int cnext = kg, next_slot = 0, rem_next = w.ks - kg * kChunk;
 
-  struct Batch {
-    v4i w[TN], x[TM][4], s[TN][NG];
+  const int chunks = (w.ks + kChunk - 1) / kChunk, steps = (chunks + WK - 1) / WK;
+  const uint32_t lds0 = lds_addr(smem);
+  auto all_of = [](const char* from) { return resource(from, 0x7fffffff); };
+  auto issue_as = [&](auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;      // all of the chunk's k exist
+    const uint32_t st = uniform(lds0 + (uint32_t)(next_slot * STAGE));
+    const int rem = rem_next;          // k from this chunk on
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+      const v4i rs = all_of(cfrom[t]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        copy16_nt(rs, WHOLE || cpart[h] < rem ? coff[t][h] : kNowhere, uniform(st + (uint32_t)((wave * TN + t) * 2 + h) * 1024));
+      cfrom[t] += WK * (kChunk / 2);
+    }
+    const v4i srs = all_of((const char*)q.scales + (sfrom - odd) * SIZE);
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+      for (int u = 0; u < SC; ++u) {
+        const int grp = 4 * u + group0;
+        uint32_t o = (uint32_t)((odd + grp * N + col[t]) * SIZE) & ~3u;
+        if (odd_end && cnext * GC + grp == last_group && col[t] == N - 1) o = kNowhere;
+        copy4(srs, (WHOLE || grp * GROUP < rem) && col[t] < N ? o : kNowhere,
+              uniform(st + C::CODES + (uint32_t)((wave * TN + t) * SC + u) * 256));
+      }
+    sfrom += (int64_t)(WK * GC) * N;
+    const v4i xrs = all_of(xfrom);
+#pragma unroll
+    for (int u = 0; u < C::XCOPIES; ++u)
+      copy16(xrs, WHOLE || xpart[u] < rem ? xoff[u] : kNowhere,
+             uniform(st + C::CODES + SCALES + (uint32_t)(kg * C::XR * 512 + (wn * C::XCOPIES + u) * 1024)));
+    xfrom += WK * (kChunk * 2);
+    rem_next -= WK * kChunk;
+    cnext += WK;
+    next_slot = next_slot + 1 == S ? 0 : next_slot + 1;
   };
-  auto fetch = [&](Batch& f, int c) {
-    const int rem = uniform(w.ks - c * 128);      // k from this chunk on, a multiple of 32 (0 or less: no chunk)
-    const uint32_t at = 32 * g < rem ? wo : kNowhere;
-#pragma unroll
-    for (int t = 0; t < TN; ++t)
-      f.w[t] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(wr[t], at, uniform(c * 64), kStream));
-#pragma unroll
-    for (int m = 0; m < TM; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        f.x[m][j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(xr, 32 * j < rem ? xo[m] : kNowhere,
-                                                                                  uniform(c * 256 + 64 * j), 0));
-#pragma unroll
-    for (int t = 0; t < TN; ++t)
-#pragma unroll
-      for (int e = 0; e < NG; ++e)
-        f.s[t][e] = load_scales<SBF16>(q.scales, scales0 + (int64_t)(c * NG + e) * per_group + col[t],
-                                       e * GROUP < rem ? left[t] : 0, four);
+  auto issue = [&] {
+    if (rem_next >= kChunk) issue_as(std::true_type{});
+    else issue_as(std::false_type{});
   };
 
   v4f acc[TM][TN];
@@ -171,107 +229,207 @@ __global__ __launch_bounds__(512, 2) void int4_kernel(Int4Problem q) {
 #pragma unroll
     for (int t = 0; t < TN; ++t) acc[m][t] = v4f{0.f, 0.f, 0.f, 0.f};
   const v8bf minus24 = __builtin_bit_cast(v8bf, v4i{(int)0xC1C0C1C0u, (int)0xC1C0C1C0u, (int)0xC1C0C1C0u, (int)0xC1C0C1C0u});
-  auto multiply = [&](Batch& f) {
+  const CodeBits bits;
+  int slot = 0, cnow = kg;
+  auto multiply = [&] {
+    const uint8_t* st = smem + slot * STAGE;
+    const uint8_t* xs = st + C::CODES + SCALES + kg * C::XR * 512;
+    uint32_t sraw[TN][SC];
 #pragma unroll
-    for (int t = 0; t < TN; ++t) transpose_words(f.w[t]);
+    for (int t = 0; t < TN; ++t)
 #pragma unroll
-    for (int e = 0; e < NG; ++e) {
-      v8bf x[TM][GJ];
-      v4f start[TM], part[TM][TN];
+      for (int u = 0; u < SC; ++u)
+        sraw[t][u] = *reinterpret_cast<const uint32_t*>(st + C::CODES + ((wave * TN + t) * SC + u) * 256 + lane * 4);
+    // all the codes and x out of LDS before any of them is used
+    v4i codes[2][TN], raw[2][TM][4];
+    auto read = [&](int h) {
 #pragma unroll
-      for (int m = 0; m < TM; ++m) {
-        start[m] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < TN; ++t)
+        codes[h][t] = *reinterpret_cast<const v4i*>(st + (wave * TN + t) * 2048 + i * 128 + (((4 * h + g) ^ swz(i)) << 4));
 #pragma unroll
-        for (int j = 0; j < GJ; ++j) {
-          x[m][j] = paired(f.x[m][e * GJ + j]);
-          start[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus24, x[m][j], start[m], 0, 0, 0);
+      for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = (16 * m + i) & (C::XR - 1);
+          raw[h][m][j] = *reinterpret_cast<const v4i*>(xs + r * 512 + (((16 * h + 4 * j + g) ^ (r & 15)) << 4));
         }
+    };
+    read(0);
+    read(1);
+    __builtin_amdgcn_sched_barrier(0);
+    float s[TN][GC];
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+#pragma unroll
+      for (int u = 0; u < SC; ++u) {
+        uint32_t v = sraw[t][u];
+        const int grp = 4 * u + group0;
+        if constexpr (SBF16) {
+          v = (odd + grp * N + col[t]) & 1 ? v & 0xffff0000u : v << 16;
+          if (odd_end && cnow * GC + grp == last_group && col[t] == N - 1) v = slast;
+        }
+        spread_scales<GC == 2 ? 2 : 4>(v, s[t] + 4 * u);
       }
 #pragma unroll
-      for (int j = 0; j < GJ; ++j)
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int t = 0; t < TN; ++t) {
-          const v8bf v = codes_plus_16((uint32_t)f.w[t][e * GJ + j]);
+      for (int t = 0; t < TN; ++t) transpose_words(codes[h][t]);
+#pragma unroll
+      for (int e = 0; e < NG; ++e) {
+        v8bf x[TM][GJ];
+        v4f start[TM], part[TM][TN];
+#pragma unroll
+        for (int m = 0; m < TM; ++m) {
+          start[m] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < GJ; ++j) {
+            x[m][j] = __builtin_bit_cast(v8bf, raw[h][m][e * GJ + j]);
+            start[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m][j], minus24, start[m], 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < GJ; ++j)
+#pragma unroll
+          for (int t = 0; t < TN; ++t) {
+            const v8bf v = bits.plus_16((uint32_t)codes[h][t][e * GJ + j]);
+#pragma unroll
+            for (int m = 0; m < TM; ++m)
+              part[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m][j], v, j ? part[m][t] : start[m], 0, 0, 0);
+          }
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
 #pragma unroll
           for (int m = 0; m < TM; ++m)
-            part[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, x[m][j], j ? part[m][t] : start[m], 0, 0, 0);
-        }
 #pragma unroll
-      for (int t = 0; t < TN; ++t) {
-        const v4f s = scale_values<SBF16>(f.s[t][e]);
-#pragma unroll
-        for (int m = 0; m < TM; ++m)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[m][t][v] = fmaf(s[v], part[m][t][v], acc[m][t][v]);
+            for (int v = 0; v < 4; ++v) acc[m][t][v] = fmaf(s[t][h * NG + e], part[m][t][v], acc[m][t][v]);
       }
     }
+    slot = slot + 1 == S ? 0 : slot + 1;
+    cnow += WK;
   };
-  const int chunks = (w.ks + 127) / 128;
-  if (wave < chunks) {
-    Batch f0, f1;
-    fetch(f0, wave);
-    for (int c = wave; c < chunks; c += 2 * waves) {
-      fetch(f1, c + waves);
-      multiply(f0);
-      if (c + waves >= chunks) break;
-      fetch(f0, c + 2 * waves);
-      multiply(f1);
+  if (steps > 0) {
+#pragma unroll
+    for (int u = 0; u < S - 1; ++u) issue();
+    for (int step = 0; step < steps; ++step) {
+      wait_vmcnt<(S - 2) * COPIES>();         // this step's copies (past the last step they are of zeros)
+      if constexpr (WN > 1) __syncthreads();
+      else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      issue();                                // over the last step's, which everybody has read
+      multiply();
     }
   }
+  wait_vmcnt<0>();
+  __syncthreads();
 
+  // The sums over the WK waves.  Lane i + 16 g has column i of rows 4 g .. 4 g + 3;
+  // here it takes columns 4 g .. 4 g + 3 of row i.
+  v4f* sums = reinterpret_cast<v4f*>(smem);     // [wave][tile][lane]
 #pragma unroll
   for (int m = 0; m < TM; ++m)
 #pragma unroll
-    for (int t = 0; t < TN; ++t) sums[wave][m * TN + t][lane] = acc[m][t];
+    for (int t = 0; t < TN; ++t) sums[(wave * TM * TN + m * TN + t) * 64 + lane] = acc[m][t];
   __syncthreads();
-  auto sum_of = [&](int at) {
-    v4f v = sums[0][at][lane];
-    for (int u = 1; u < waves; ++u) v += sums[u][at][lane];
+  auto sum_of = [&](int n, int m, int t) {      // of the n-th of the WN waves
+    const int from = (4 * g + 16 * (i >> 2)) * 4 + (i & 3);
+    v4f v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < WK; ++u) {
+      const float* f = reinterpret_cast<const float*>(sums + ((u * WN + n) * TM * TN + m * TN + t) * 64) + from;
+      v += v4f{f[0], f[4], f[8], f[12]};
+    }
     return v;
   };
-  if (p.kind == kKindGated) {
+  if (gated) {
     if constexpr (TN > 1) {
-      for (int u = wave; u < TM * (TN / 2); u += waves) {
-        const int m = u / (TN / 2), t = u % (TN / 2);
-        v4f gate[1] = {sum_of(m * TN + t)}, up[1] = {sum_of(m * TN + TN / 2 + t)};
-        GatedOut<1>(p, w, 16 * TM, 16 * TN, 32 * t, nullptr, lane).rows16(16 * m, gate, up);
+      for (int u = wave; u < TM * WN * (TN / 2); u += C::WAVES) {
+        const int m = u / (WN * (TN / 2)), pair = u % (WN * (TN / 2)), n = pair / (TN / 2), t = pair % (TN / 2);
+        v4f gate[1] = {sum_of(n, m, t)}, up[1] = {sum_of(n, m, TN / 2 + t)};
+        GatedOut<1>(p, w, C::BM, C::BN, 32 * pair, nullptr, lane).rows16(16 * m, gate, up);
       }
     }
   } else {
     const BfOut out(p, w.g);
-    for (int u = wave; u < TM * TN; u += waves) {
-      const int r = 16 * (u / TN) + i;
-      const v4f v = sum_of(u);
-      if (r < w.rows) out.four(w.m0 + r, w.n0 + 16 * (u % TN) + 4 * g, v);
+    for (int u = wave; u < TM * WN * TN; u += C::WAVES) {
+      const int m = u / (WN * TN), t = u % (WN * TN), r = 16 * m + i;
+      const v4f v = sum_of(t / TN, m, t % TN);
+      if (r < w.rows) out.four(w.m0 + r, w.n0 + 16 * t + 4 * g, v);
     }
   }
 }
 
-template <int TM, int TN>
-hipError_t start(const Int4Problem& q, int group, bool sbf16, unsigned grid, int threads, hipStream_t stream) {
+// TM, XR, TN, WK, WN, S
+enum { kI4One = 0, kI4OneWide, kI4OneShort, kI4Four, kI4FourWide, kI4Row, kI4RowWide, kI4Runs, kI4Many };
+using I4One = I4Cfg<1, 2, 1, 8, 1, 3>;
+using I4OneWide = I4Cfg<1, 2, 2, 4, 1, 3>;
+using I4OneShort = I4Cfg<1, 2, 2, 2, 1, 3>;
+using I4Four = I4Cfg<1, 4, 1, 8, 1, 3>;
+using I4FourWide = I4Cfg<1, 4, 2, 4, 1, 3>;
+using I4Row = I4Cfg<1, 16, 1, 4, 2, 2>;
+using I4RowWide = I4Cfg<1, 16, 2, 2, 2, 2>;
+using I4Runs = I4Cfg<1, 16, 2, 1, 4, 2>;
+using I4Many = I4Cfg<2, 32, 2, 1, 4, 2>;
+
+template <class C>
+hipError_t start(const Int4Problem& q, int group, bool sbf16, unsigned grid, hipStream_t stream) {
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, stream, q);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(C::THREADS), 0, stream, q);
     return hipGetLastError();
   };
-  if (group == 32) return sbf16 ? go(int4_kernel<TM, TN, 32, true>) : go(int4_kernel<TM, TN, 32, false>);
-  if (group == 64) return sbf16 ? go(int4_kernel<TM, TN, 64, true>) : go(int4_kernel<TM, TN, 64, false>);
-  return sbf16 ? go(int4_kernel<TM, TN, 128, true>) : go(int4_kernel<TM, TN, 128, false>);
+  if (group == 32) return sbf16 ? go(int4_kernel<C, 32, true>) : go(int4_kernel<C, 32, false>);
+  if (group == 64) return sbf16 ? go(int4_kernel<C, 64, true>) : go(int4_kernel<C, 64, false>);
+  return sbf16 ? go(int4_kernel<C, 128, true>) : go(int4_kernel<C, 128, false>);
+}
+
+template <class F>
+auto with_config(int cfg, F f) {
+  switch (cfg) {
+    case kI4One: return f(I4One{});
+    case kI4OneWide: return f(I4OneWide{});
+    case kI4OneShort: return f(I4OneShort{});
+    case kI4Four: return f(I4Four{});
+    case kI4FourWide: return f(I4FourWide{});
+    case kI4Row: return f(I4Row{});
+    case kI4RowWide: return f(I4RowWide{});
+    case kI4Runs: return f(I4Runs{});
+    default: return f(I4Many{});
+  }
 }
 
 }  // namespace
 
+// (times in us, the choice first; 256 CUs)
 Int4Tile int4_tile(const BfProblem& p, int cus) {
   Int4Tile t{};
-  const int64_t rows = p.mode == kBfRowRuns ? (p.M + p.groups - 1) / p.groups : p.M;
-  t.tm = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  t.tn = 2;
-  if (p.kind != kKindGated && t.tm == 1 && p.mode == kBfDense) {
-    if ((int64_t)p.N < 16 * 2 * cus) t.tn = 1;
-    else if ((int64_t)p.N >= 16 * 4 * cus) t.tn = 4;
+  const bool runs = p.mode == kBfRowRuns, pairs = p.kind == kKindGated;     // (gate and up: two tiles a wave at least)
+  const int64_t rows = runs ? (p.M + p.groups - 1) / p.groups : p.M;
+  // 64 columns a workgroup fill the device
+  const bool wide = (rows + 15) / 16 * ((int64_t)p.N + 63) / 64 >= cus;
+  if (runs) {
+    // One row tile a run while most runs fit it: 512 rows over 32 experts of 4096 x
+    // 7168 (gated) 124 for 131, 128 rows 89 for 112, 1280 rows 245 for 202.
+    t.cfg = rows <= 24 ? kI4Runs : kI4Many;
+  } else if (rows <= 4) {
+    // One tile a wave and eight waves on k where k is long and columns are few:
+    // 1 x 7168 x 16384 16.7 for 18.7, 1 x 2112 x 7168 6.8 for 9.3, 1 x 16384 x 16384
+    // 30.1 for 27.3, 1 x 7168 x 2048 6.4 for 5.8.  Two waves for a short one: 1 x
+    // 24576 x 1536 8.6 for 11.0.  x takes half the LDS for two rows: 1 x 7168 x
+    // 16384 19.7 with four.
+    const bool two = rows <= 2;
+    if (!pairs && p.K > 4096 && !wide) t.cfg = two ? kI4One : kI4Four;
+    else t.cfg = !two ? kI4FourWide : p.K <= 2048 && wide ? kI4OneShort : kI4OneWide;
+  } else if (rows <= 64) {
+    // 16 x 16384 x 8192 20.5 for 25.4, 32 x 8192 x 8192 19.0 for 23.4, 24 x 4096 x
+    // 4096 17.3 for 11.6
+    t.cfg = pairs || wide ? kI4RowWide : kI4Row;
+  } else {
+    t.cfg = kI4Many;
   }
-  t.threads = p.K >= 16 * 128 ? 512 : 256;
-  const int64_t bm = 16 * t.tm, bn = 16 * t.tn;
-  t.units = ((p.M + bm - 1) / bm + (p.mode == kBfRowRuns ? p.groups + 1 : 0)) * ((p.N + bn - 1) / bn);
+  with_config(t.cfg, [&](auto c) {
+    typedef decltype(c) C;
+    t.threads = C::THREADS;
+    t.units = (((int64_t)p.M + C::BM - 1) / C::BM + (runs ? p.groups + 1 : 0)) * (((int64_t)p.N + C::BN - 1) / C::BN);
+    return 0;
+  });
   return t;
 }
 
@@ -279,11 +437,7 @@ hipError_t launch_int4(const BfProblem& p, const Int4Tile& t, const uint8_t* cod
                        int group, hipStream_t stream) {
   const Int4Problem q{p, codes, scales};
   const unsigned grid = (unsigned)((t.units + 7) / 8 * 8);
-  if (t.tm == 1 && t.tn == 1) return start<1, 1>(q, group, scales_bf16, grid, t.threads, stream);
-  if (t.tm == 1 && t.tn == 2) return start<1, 2>(q, group, scales_bf16, grid, t.threads, stream);
-  if (t.tm == 1) return start<1, 4>(q, group, scales_bf16, grid, t.threads, stream);
-  if (t.tm == 2) return start<2, 2>(q, group, scales_bf16, grid, t.threads, stream);
-  return start<4, 2>(q, group, scales_bf16, grid, t.threads, stream);
+  return with_config(t.cfg, [&](auto c) { return start<decltype(c)>(q, group, scales_bf16, grid, stream); });
 }
 
 // ------------------------------------------------- quantize and dequantize
