@@ -1137,24 +1137,44 @@ LossSpace loss_space(int64_t m, int64_t v, int64_t k) {
 
 // The backward pass's: counters and its products' partial tiles, then dlogits of
 // one piece of the vocabulary (and what their rounding left), and dx's sums
-// where there is more than one piece.
+// where there is more than one piece or part.
 constexpr int64_t kLossPieceBytes = (int64_t)512 << 20;    // of dlogits at a time
 struct LossBackwardSpace {
   size_t products, dz, rest, sums, total;
   int64_t piece, ldz;       // classes of a piece, the last one may have fewer
+  int parts;                // of dx's sums within a piece (0: the product's own choice)
 };
+// dx [m][k] sums over a piece's classes, many for its few tiles: parts of them, each
+// with sums of its own, fill the last round of the CUs.  4095 x 2048 over 50,176
+// classes, 128 tiles of 256 x 256: TBD us in two parts, 878 in tiles of 128 x 128.
+int loss_dx_parts(int64_t m, int64_t k, int64_t classes, int cus) {
+  const int64_t tiles = (m + 255) / 256 * ((k + 255) / 256);
+  if (m < 384 || 8 * tiles < cus) return 0;
+  int best = 0;
+  double least = 0;
+  for (int parts = 1; parts <= 8 && classes / parts >= 1024; ++parts) {
+    // rounds of the CUs at 1.5 us for 64 classes, and sums at 4.9 TB/s, written and read
+    const double us = (double)((tiles * parts + cus - 1) / cus) * classes / parts * (1.5 / 64) + parts * (m * k * 8 / 4.9e6);
+    if (!best || us < least) best = parts, least = us;
+  }
+  return best;
+}
 LossBackwardSpace loss_backward_space(int64_t m, int64_t v, int64_t k, bool rest) {
   const int cus = fg8::device_cu_count();
   LossBackwardSpace s{};
-  const int64_t most = kLossPieceBytes / (2 * m) < 256 ? 256 : kLossPieceBytes / (2 * m);
-  const int64_t pieces = (v + most - 1) / most;
-  s.piece = pieces == 1 ? v : up((v + pieces - 1) / pieces, 256);
+  // Pieces of one size, rounded up to 8192 classes: 32 tiles' columns, so that only
+  // the last piece leaves rounds of the CUs unfilled.
+  const int64_t fit = kLossPieceBytes / (2 * m), unit = fit >= 8192 ? 8192 : 256;
+  const int64_t most = fit < 256 ? 256 : fit / unit * unit;
+  s.piece = v <= fit || v <= 256 ? v : up((v + (v + most - 1) / most - 1) / ((v + most - 1) / most), unit);
   s.ldz = up(s.piece, 8);
+  s.parts = loss_dx_parts(m, k, s.piece, cus);
   s.products = fg8::kSplitKCounterBytes;
   for (int64_t n : {s.piece, v % s.piece ? v % s.piece : s.piece})
     for (int add = 0; add < 2; ++add) {
       fg8::BfProblem p = dense_bf16(m, k, n, false, true), q = dense_bf16(n, k, m, true, true);
       p.add = q.add = add;
+      p.parts = s.parts;
       for (const fg8::BfProblem& r : {p, q}) {
         const size_t b = fg8::bf16_workspace_bytes(r, cus);
         if (b > s.products) s.products = b;
@@ -1164,7 +1184,7 @@ LossBackwardSpace loss_backward_space(int64_t m, int64_t v, int64_t k, bool rest
   s.dz = s.products;
   s.rest = s.dz + dz;
   s.sums = s.rest + (rest ? dz : 0);
-  s.total = s.sums + (pieces > 1 ? (size_t)m * k * 4 : 0);
+  s.total = s.sums + (s.piece < v || s.parts > 1 ? (size_t)m * k * 4 * (s.parts ? s.parts : 1) : 0);
   return s;
 }
 
@@ -1243,7 +1263,7 @@ fg8_status linear_cross_entropy_backward(const float* dloss, const uint16_t* x, 
   uint16_t* dz = (uint16_t*)((char*)workspace + here.dz);
   uint16_t* left = (uint16_t*)((char*)workspace + here.rest);
   float* sums = (float*)((char*)workspace + here.sums);
-  const bool pieces = here.piece < vocab;
+  const bool summed = here.piece < vocab || here.parts > 1;
   p.a = x; p.lda = ldx; p.ldb = k; p.d = dz; p.ldd = here.ldz;
   p.loss.targets = targets; p.loss.targets64 = targets_are_int64; p.loss.classes = (int)vocab;
   p.loss.lse = lse; p.loss.dloss = dloss; p.loss.rest = rest ? left : nullptr;
@@ -1255,7 +1275,8 @@ fg8_status linear_cross_entropy_backward(const float* dloss, const uint16_t* x, 
       fg8::BfProblem q = dense_bf16(m, k, n, false, true);
       q.counters = p.counters; q.partial = p.partial;
       q.a = dz; q.lda = here.ldz; q.b = p.b; q.ldb = k; q.ldd = k;
-      q.d = pieces ? (void*)sums : dx; q.out_bf16 = !pieces; q.add = v0 > 0;
+      q.d = summed ? (void*)sums : dx; q.out_bf16 = !summed; q.add = v0 > 0;
+      q.parts = here.parts; q.d_stride = here.parts > 1 ? m * k : 0;
       if (fg8_status s = run_bf16(q, fn, stream)) return s;
     }
     // A float dw takes dlogits in two BF16 parts, as gemm_bf16_epilogue_backward's does.
@@ -1268,8 +1289,8 @@ fg8_status linear_cross_entropy_backward(const float* dloss, const uint16_t* x, 
       if (fg8_status s = run_bf16(q, fn, stream)) return s;
     }
   }
-  if (dx && pieces) {
-    const hipError_t e = fg8::launch_round_bf16(sums, m * k, dx, stream);
+  if (dx && summed) {
+    const hipError_t e = fg8::launch_sum_bf16(sums, here.parts ? here.parts : 1, m * k, dx, stream);
     if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
   }
   g_err[0] = 0;

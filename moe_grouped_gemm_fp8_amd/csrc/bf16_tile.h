@@ -430,7 +430,7 @@ struct TileOut {
   v4f bias[EPI ? 4 : 1];
   __device__ TileOut(const BfProblem& q, const BfUnit& w, int bm, int bn, int wave_n, uint8_t* t, int l)
       : p(q), turn(t), m0(w.m0), rows(w.rows), n(w.n0 + wave_n), lane(l) {
-    d = (char*)p.d + (int64_t)(p.mode == kBfKRuns ? w.g : 0) * p.d_stride * (p.out_bf16 ? 2 : 4);
+    d = (char*)p.d + w.g * p.d_stride * (p.out_bf16 ? 2 : 4);     // (row runs: d_stride is 0)
     whole = w.rows >= bm && w.n0 + bn <= p.N;
     full = whole && p.ldd % (p.out_bf16 ? 8 : 4) == 0;
     if constexpr (EPI) {

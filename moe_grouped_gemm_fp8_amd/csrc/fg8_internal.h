@@ -129,6 +129,7 @@ struct BfProblem {
   int64_t ldz;
   int add;                      // B k-major, FP32: D += the product
   int grid;                     // workgroups of a persistent launch (set by the launcher)
+  int parts;                    // dense, B k-major, FP32: k in so many parts, the sums of each at d + part * d_stride
   // split k (dense)
   int splits;
   float* partial;
@@ -178,8 +179,8 @@ hipError_t launch_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_
 
 // loss and lse [m] from kKindLse's pieces [tiles][m] and target logits.
 hipError_t launch_loss_finish(const BfLoss& s, int64_t tiles, int64_t m, float* loss, float* lse, hipStream_t stream);
-// n floats rounded to BF16.
-hipError_t launch_round_bf16(const float* x, int64_t n, uint16_t* y, hipStream_t stream);
+// y [n] = the sum of x [parts][n], rounded to BF16.
+hipError_t launch_sum_bf16(const float* x, int parts, int64_t n, uint16_t* y, hipStream_t stream);
 
 // --------------------------------------------------------------- layer norm
 int64_t layer_norm_teams(int64_t rows, int64_t cols, bool bf16, int num_cus);

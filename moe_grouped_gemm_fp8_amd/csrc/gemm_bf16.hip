@@ -632,7 +632,9 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
     __syncthreads();
     mt = uniform(runs.sum[p.groups + 1]);
   }
-  const int total = mt * nt * (MODE == kBfKRuns ? p.groups : 1), G = p.grid;
+  // dx of a head in parts of its classes: each part's sums are an output of their own
+  constexpr bool PARTS = MODE == kBfDense && !AK && BK;
+  const int total = mt * nt * (MODE == kBfKRuns ? p.groups : PARTS ? p.splits : 1), G = p.grid;
 
   auto find = [&](int u, BfUnit& w) {
     int id = xcd_round(u, total, G), m, n;
@@ -644,7 +646,7 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
       w.m0 = m0;
       w.ks = w.g < 0 ? 0 : p.K;
     } else {
-      const int part = MODE == kBfKRuns ? id / (mt * nt) : 0;
+      const int part = MODE == kBfKRuns || PARTS ? id / (mt * nt) : 0;
       raster(id - part * (mt * nt), mt, nt, m, n);
       w.m0 = (int64_t)m * 256;
       w.rows = p.M - (int)w.m0;
@@ -654,6 +656,12 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
         const int a = clamp_off(p.offsets[part], p.K), b = clamp_off(p.offsets[part + 1], p.K);
         w.k0 = uniform(a);
         w.ks = uniform(max(b - a, 0));
+      }
+      if constexpr (PARTS) {
+        const int steps = (p.K + kBK - 1) / kBK;
+        const int s0 = (int)((int64_t)part * steps / p.splits), s1 = (int)((int64_t)(part + 1) * steps / p.splits);
+        w.k0 = s0 * kBK;
+        w.ks = min(p.K, s1 * kBK) - s0 * kBK;
       }
     }
     w.n0 = n * 256;
@@ -934,6 +942,8 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
   const bool second_round = units(kMid) > 2 * cus;
   if (loss) {
     t.cfg = rows <= 64 ? kSlab : second_round ? kBig : kMid;
+  } else if (p.parts) {
+    t.cfg = kBig;
   } else if (p.add && !p.a_kmajor) {      // (the tiles that add)
     t.cfg = second_round ? kBig : kMid;
   } else if (p.a_kmajor) {
@@ -971,7 +981,7 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
   t.bn = kBn[t.cfg] * (gated && t.cfg == kFew ? 2 : 1);   // (16 gate and 16 up rows)
   t.threads = kThreads[t.cfg];
   t.persistent = t.cfg == kBig;
-  t.splits = 1;
+  t.splits = p.parts ? p.parts : 1;
   if (dense && t.cfg != kBig && t.cfg != kFew && !loss) {
     // One workgroup a CU; two where several row tiles read the same weights
     // (64 x 2112 x 7168 14.1 in 6 splits, 16.2 in 12; 128 x 2112 x 7168 18.9
@@ -989,7 +999,7 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
 
 size_t bf16_workspace_bytes(const BfProblem& p, int cus) {
   const BfTile t = bf16_tile(p, cus);
-  if (t.splits <= 1) return 0;
+  if (t.splits <= 1 || p.parts) return 0;
   const size_t tiles = (size_t)((p.M + t.bm - 1) / t.bm) * ((p.N + t.bn - 1) / t.bn);
   return kSplitKCounterBytes + tiles * t.splits * t.bm * t.bn * 4;
 }

@@ -470,11 +470,13 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const T* __restrict_
   scales += (int64_t)blockIdx.z * rows * (cols / GROUP);
   constexpr int PER = kQuantRows / 4;
   float f[PER][8];
+  const int here = (int)min(rows - r0 - wave * PER, (int64_t)PER);     // this wave's rows
+  w += (r0 + wave * PER) * cols + c;
+  q += ((r0 + wave * PER) * cols + c) / 2;
 #pragma unroll
   for (int u = 0; u < PER; ++u) {
-    const int64_t r = r0 + wave * PER + u;
-    if (r < rows && c < cols) {
-      load_eight(w + r * cols + c, f[u]);
+    if (u < here && c < cols) {
+      load_eight(w + u * cols, f[u]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[u][e] = 0.f;
@@ -496,19 +498,20 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const T* __restrict_
     // w / s rounded correctly from the correctly rounded reciprocal (Markstein:
     // t = w r, then t + r (w - t s)), where nothing leaves the range of normal
     // numbers; one addition then rounds it to the code, 8 on top
-    const float r = __fdiv_rn(1.f, s);
     uint32_t code = 0;
-    const bool plain = s > 0x1p-100f && s < 0x1p100f;
+    auto put = [&](int e, float t) { code |= (__float_as_uint(t + (12582912.f + 8.f)) & 15u) << (4 * e); };
+    if (__all(s > 0x1p-100f && s < 0x1p100f)) {
+      const float r = __fdiv_rn(1.f, s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float t = f[u][e] * r;
-      t = fmaf(fmaf(-t, s, f[u][e]), r, t);
-      if (!plain) t = __fdiv_rn(f[u][e], s);
-      const uint32_t v = __float_as_uint(t + (12582912.f + 8.f)) & 15u;
-      code |= v << (4 * e);
+      for (int e = 0; e < 8; ++e) {
+        const float t = f[u][e] * r;
+        put(e, fmaf(fmaf(-t, s, f[u][e]), r, t));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) put(e, __fdiv_rn(f[u][e], s));
     }
-    const int64_t row = r0 + wave * PER + u;
-    if (row < rows && c < cols) store_nt(q + row * (cols / 2) + c / 2, code);
+    if (u < here && c < cols) store_nt(q + u * (cols / 2), code);
   }
   __syncthreads();
   for (int at = threadIdx.x; at < G * kQuantRows; at += 256) {

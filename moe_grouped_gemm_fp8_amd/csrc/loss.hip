@@ -1,5 +1,5 @@
 // What the softmax cross entropy of a linear head needs beside its products: the
-// rows' statistics joined over the vocabulary, and the rounding of dx's sums.
+// rows' statistics joined over the vocabulary, and dx's sums added and rounded.
 //
 //   lse = M + log sum over tiles of s_t e^(m_t - M),  M = max over tiles of m_t
 //   loss = lse - (the target's logit), 0 for a row without a target
@@ -26,8 +26,13 @@ __global__ __launch_bounds__(1024) void loss_finish_kernel(BfLoss s, int tiles, 
       top = t;
     };
     if (row < m) {
-#pragma unroll 4
-      for (int t = wave; t < tiles; t += 16) add(s.pieces[t * m + row]);
+      for (int t0 = wave; t0 < tiles; t0 += 16 * 8) {      // (eight loads before the first is used)
+        float2 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = t0 + 16 * u < tiles ? s.pieces[(int64_t)(t0 + 16 * u) * m + row] : make_float2(kLowest, 0.f);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) add(v[u]);
+      }
     }
     part[wave][lane] = make_float2(top, sum);
     __syncthreads();
@@ -44,10 +49,14 @@ __global__ __launch_bounds__(1024) void loss_finish_kernel(BfLoss s, int tiles, 
 }
 
 // (n is a multiple of 8)
-__global__ __launch_bounds__(256) void round_kernel(const float* __restrict__ x, int64_t n, uint16_t* __restrict__ y) {
+__global__ __launch_bounds__(256) void sum_kernel(const float* __restrict__ x, int parts, int64_t n, uint16_t* __restrict__ y) {
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
-    const float4 a = *reinterpret_cast<const float4*>(x + i), b = *reinterpret_cast<const float4*>(x + i + 4);
-    *reinterpret_cast<uint4*>(y + i) = make_uint4(bf16x2(a.x, a.y), bf16x2(a.z, a.w), bf16x2(b.x, b.y), bf16x2(b.z, b.w));
+    v4f a = {0.f, 0.f, 0.f, 0.f}, b = a;
+    for (int p = 0; p < parts; ++p) {
+      a += *reinterpret_cast<const v4f*>(x + p * n + i);
+      b += *reinterpret_cast<const v4f*>(x + p * n + i + 4);
+    }
+    *reinterpret_cast<uint4*>(y + i) = make_uint4(bf16x2(a[0], a[1]), bf16x2(a[2], a[3]), bf16x2(b[0], b[1]), bf16x2(b[2], b[3]));
   }
 }
 
@@ -60,8 +69,8 @@ hipError_t launch_loss_finish(const BfLoss& s, int64_t tiles, int64_t m, float* 
   return hipGetLastError();
 }
 
-hipError_t launch_round_bf16(const float* x, int64_t n, uint16_t* y, hipStream_t stream) {
-  hipLaunchKernelGGL(round_kernel, dim3((unsigned)std::min((n + 2047) / 2048, kMostBlocks)), dim3(256), 0, stream, x, n, y);
+hipError_t launch_sum_bf16(const float* x, int parts, int64_t n, uint16_t* y, hipStream_t stream) {
+  hipLaunchKernelGGL(sum_kernel, dim3((unsigned)std::min((n + 2047) / 2048, kMostBlocks)), dim3(256), 0, stream, x, parts, n, y);
   return hipGetLastError();
 }
 
