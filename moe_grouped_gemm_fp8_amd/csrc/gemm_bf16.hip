@@ -826,18 +826,19 @@ __global__ __launch_bounds__(512, 2) void bf16_big_kernel(BfProblem p) {
 // ------------------------------------------------------------------- host
 // Tile configurations.  kBig: bf16_big_kernel; kFew: bf16_few_kernel; the
 // others: bf16_kernel with two workgroups a CU.
-enum { kBig = 0, kDuo, kMid, kHigh, kLow, kFlat, kThin, kFew, kSlab, kConfigs };
+enum { kBig = 0, kDuo, kMid, kHigh, kLow, kFlat, kThin, kFew, kSlab, kDeep, kConfigs };
 using BfDuo = BfCfg<128, 256, 1, 4, 3, 2, 32>;
 using BfMid = BfCfg<128, 128, 2, 2, 2, 2>;
 using BfHigh = BfCfg<128, 64, 2, 2, 3, 2>;
 using BfLow = BfCfg<64, 64, 2, 2, 4, 2>;
 using BfFlat = BfCfg<32, 64, 2, 2, 5, 2>;
 using BfThin = BfCfg<16, 64, 1, 4, 6, 2>;
-using BfSlab = BfCfg<64, 128, 2, 2, 3, 2>;
-constexpr int kBm[kConfigs] = {256, 128, 128, 128, 64, 32, 16, 16, 64};
-constexpr int kBn[kConfigs] = {256, 256, 128, 64, 64, 64, 64, 16, 128};
+using BfSlab = BfCfg<64, 128, 2, 2, 3, 2>;    // (this and the next for a head's logits only)
+using BfDeep = BfCfg<128, 128, 2, 2, 3, 1>;
+constexpr int kBm[kConfigs] = {256, 128, 128, 128, 64, 32, 16, 16, 64, 128};
+constexpr int kBn[kConfigs] = {256, 256, 128, 64, 64, 64, 64, 16, 128, 128};
 constexpr int kThreads[kConfigs] = {512, BfDuo::THREADS, BfMid::THREADS, BfHigh::THREADS,
-                                    BfLow::THREADS, BfFlat::THREADS, BfThin::THREADS, 512, BfSlab::THREADS};
+                                    BfLow::THREADS, BfFlat::THREADS, BfThin::THREADS, 512, BfSlab::THREADS, BfDeep::THREADS};
 
 namespace {
 
@@ -877,6 +878,7 @@ template <int KIND>
 hipError_t launch_loss(BfProblem p, const BfTile& t, hipStream_t stream) {
   const unsigned units = grid_of(p, t.bm, t.bn);
   if (t.cfg == kSlab) return start(bf16_kernel<BfSlab, false, false, kBfDense, false, KIND>, p, units, BfSlab::THREADS, stream);
+  if (t.cfg == kDeep) return start(bf16_kernel<BfDeep, false, false, kBfDense, false, KIND>, p, units, BfDeep::THREADS, stream);
   if (t.cfg == kMid) return start(bf16_kernel<BfMid, false, false, kBfDense, false, KIND>, p, units, BfMid::THREADS, stream);
   const unsigned cus = (unsigned)device_cu_count();
   p.grid = (int)(units < cus ? units : cus);
@@ -941,7 +943,11 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
   const bool loss = p.kind == kKindLse || p.kind == kKindDlogits;
   const bool second_round = units(kMid) > 2 * cus;
   if (loss) {
-    t.cfg = rows <= 64 ? kSlab : second_round ? kBig : kMid;
+    // Few rows: the weights' one way through, 64-row tiles for less work (64 x 128000
+    // x 7168 341).  128 x 128 tiles with a third stage while one a CU holds them all:
+    // 128 x 32000 x 4096 74 for 87, 200 x 16000 x 7168 90 for 122, beyond, two a CU:
+    // 256 x 32000 x 4096 99 for 109.
+    t.cfg = rows <= 64 ? kSlab : second_round ? kBig : units(kMid) <= cus ? kDeep : kMid;
   } else if (p.parts) {
     t.cfg = kBig;
   } else if (p.add && !p.a_kmajor) {      // (the tiles that add)
