@@ -189,6 +189,23 @@ def test_runs(dev, case, gated):
     _check(y, layer.gated("silu", z), 1.13 * ez[:, :n] * (u + ez[:, n:]) + a * ez[:, n:] + 2.0 ** -19 * a * u, "h")
 
 
+@pytest.mark.parametrize("n,k,group", [(37, 64, 64), (21, 96, 32), (5, 384, 128), (40, 160, 32)])
+def test_runs_bf16_scales(dev, n, k, group):
+    """Experts whose scales start at odd elements, and a last one in no whole dword:
+    exact, with poison behind the scales."""
+    counts = [2, 0, 17, 1, 3]
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    g = _gen(10, n, k)
+    codes, scales = _weights(g, 5, n, k, group, True)
+    x = _x(g, int(off[-1]), k, True)
+    want, _ = layer.grouped(_np(x), np.stack([int4.values(c, s) for c, s in zip(codes, scales)]), off)
+    room = torch.full((scales.numel() + 64,), float("nan"), dtype=BF16, device=dev)
+    room[:scales.numel()] = scales.to(BF16).to(dev).flatten()
+    y = _fg8().grouped_gemm_bf16_int4(x.to(dev), torch.from_numpy(int4.pack(codes)).to(dev), room[:scales.numel()].view(scales.shape),
+                                      torch.from_numpy(off).to(dev), out_dtype=F32)
+    assert np.array_equal(_np(y), want)
+
+
 @pytest.mark.parametrize("m,n,k,group", [(1, 16, 128, 128), (1, 1031, 256, 32), (20, 45, 96, 32), (64, 128, 2304, 64)])
 def test_gated_dense(dev, m, n, k, group):
     g = _gen(7, m, n)
