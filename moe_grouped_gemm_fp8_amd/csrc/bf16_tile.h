@@ -470,7 +470,9 @@ struct TileOut {
 };
 
 // Sixteen rows x 32 columns as BF16 (1 KB of LDS) -> four lanes a row, 64 bytes.
-// ld8: to and ld are whole 16-byte pieces.
+// ld8: to and ld are whole 16-byte pieces.  Half lines, which meet their other
+// halves in the L2: ordinary stores (29,319 ragged rows, k = 360, with z of 2 x 1520
+// columns 120 us for 165 with the non-temporal hint).
 __device__ __forceinline__ void store_bf16_half_rows(uint8_t* turn, v4f a, v4f b, uint16_t* to, int64_t ld, bool ld8,
                                                      int rows, int n, int N, int lane, bool whole) {
   const int i = lane & 15, g = lane >> 4;
@@ -482,7 +484,7 @@ __device__ __forceinline__ void store_bf16_half_rows(uint8_t* turn, v4f a, v4f b
   }
   const int r = lane >> 2, c = lane & 3;
   const uint4 u = *reinterpret_cast<const uint4*>(turn + r * 64 + ((c ^ (r >> 2)) << 4));
-  if (whole || r < rows) store_eight(to + r * ld, ld8 ? 8 : 1, n + 8 * c, N, whole && ld8, u);
+  if (whole || r < rows) store_eight(to + r * ld, ld8 ? 8 : 1, n + 8 * c, N, false, u);
 }
 
 // One unit's output of a gated product: a wave holds the gate and the up sums of
