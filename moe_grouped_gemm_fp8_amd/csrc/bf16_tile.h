@@ -569,8 +569,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.4028235e38f;
 
 // A wave's 64 columns of a tile of logits, GROUPS times sixteen rows: kKindLse
-// leaves each row's maximum and sum in LDS (merge() below joins the waves'),
-// kKindDlogits stores dlogits.
+// leaves each row's maximum and sum in LDS (merge() below joins the waves'; one pair
+// a row and tile goes to memory, 33 MB for the 4 GB of logits of 8192 x 128000),
+// kKindDlogits stores dlogits.  The logits are the FP32 sums, never rounded.
 template <int KIND, int GROUPS>
 struct LossOut {
   static constexpr int kTurn = 2048;    // LDS of a wave

@@ -41,6 +41,9 @@
 //   stores: the weight gradient of short runs, whose FP32 tiles take as long as
 //     their sums and do not overlap them (kernel below).
 //   weights: few rows, where the time is that of reading them once.
+// A gated product runs at the rate of the plain one of 2 n columns (8192 x 4096 x
+// 7168: 312 us for 311, with z 323 for 311), and so do a head's logits with
+// their statistics (8192 x 128000 x 7168: 10.3 ms, 1450 TFLOP/s).
 #include "bf16_tile.h"
 
 namespace fg8 {
