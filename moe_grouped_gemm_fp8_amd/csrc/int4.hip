@@ -23,10 +23,11 @@ namespace {
 // A workgroup is WK x WN waves.  A wave owns 16 TM rows by 16 TN weight rows (its
 // place among the WN) and every WK-th chunk of 256 k, a 128-byte line of codes a
 // row; the WK waves' sums meet in LDS at the end.  Codes, scales and x of a chunk
-// are copied from global memory straight into LDS, S - 1 chunks ahead: what is in
-// flight takes no registers, and nothing waits for it but one counter.  Codes and
-// scales are the wave's own; x is shared by the WN waves of a chunk (a barrier a
-// chunk, none where WN is 1).
+// are copied from global memory straight into LDS, a chunk ahead: what is in flight
+// takes no registers, and nothing waits for it but one counter.  (A second chunk
+// ahead takes the LDS of another workgroup: 4 x 24576 x 2048 16.4 us for 12.0.)
+// Codes and scales are the wave's own; x is shared by the WN waves of a chunk (a
+// barrier a chunk, none where WN is 1).
 //
 // A lane reads 16 bytes of codes, 32 k of one weight row; four swaps between the
 // four groups of sixteen lanes turn that into the layout of four MFMAs of 32 k
@@ -103,10 +104,10 @@ struct CodeBits {
 };
 
 // XR: rows of x that are copied (the least that hold the tile's rows).
-constexpr int kChunk = 256;
-template <int TM_, int XR_, int TN_, int WK_, int WN_, int S_>
+constexpr int kChunk = 256, kStages = 2;
+template <int TM_, int XR_, int TN_, int WK_, int WN_>
 struct I4Cfg {
-  static constexpr int TM = TM_, XR = XR_, TN = TN_, WK = WK_, WN = WN_, S = S_;
+  static constexpr int TM = TM_, XR = XR_, TN = TN_, WK = WK_, WN = WN_;
   static constexpr int WAVES = WK * WN, THREADS = 64 * WAVES, BM = 16 * TM, BN = 16 * TN * WN;
   static constexpr int CODES = WAVES * TN * 2048, X = WK * XR * 512;
   static constexpr int XCOPIES = XR / 2 / WN;          // of 1 KB, a wave's of a chunk
@@ -117,14 +118,12 @@ struct I4Cfg {
 
 template <class C, int GROUP, bool SBF16>
 __global__ __launch_bounds__(C::THREADS) void int4_kernel(Int4Problem q) {
-  constexpr int TM = C::TM, TN = C::TN, WK = C::WK, WN = C::WN, S = C::S;
+  constexpr int TM = C::TM, TN = C::TN, WK = C::WK, WN = C::WN;
   constexpr int NG = 128 / GROUP, GJ = GROUP / 32;      // groups of 128 k, MFMAs of a group
   constexpr int GC = 2 * NG, SC = C::scale_copies(GROUP);     // groups of a chunk, copies of their scales
   constexpr int STAGE = C::stage(GROUP), SCALES = C::WAVES * TN * 256 * SC;
-  constexpr int COPIES = TN * (2 + SC) + C::XCOPIES;   // all of a wave's of a chunk
-  static_assert((S - 2) * COPIES < 64, "the counter of loads in flight");
-  static_assert(C::WAVES * TM * TN * 1024 <= S * STAGE && S * STAGE <= kLdsBytes, "sums in the stages, stages in the LDS");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
+  static_assert(C::WAVES * TM * TN * 1024 <= kStages * STAGE && kStages * STAGE <= kLdsBytes, "sums in the stages, stages in the LDS");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kStages * STAGE];
   const BfProblem& p = q.p;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kg = wave / WN, wn = wave % WN, i = lane & 15, g = lane >> 4;
@@ -220,7 +219,7 @@ __global__ __launch_bounds__(C::THREADS) void int4_kernel(Int4Problem q) {
     xfrom += WK * (kChunk * 2);
     rem_next -= WK * kChunk;
     cnext += WK;
-    next_slot = next_slot + 1 == S ? 0 : next_slot + 1;
+    next_slot ^= 1;
   };
   auto issue = [&] {
     if (rem_next >= kChunk) issue_as(std::true_type{});
@@ -308,14 +307,13 @@ __global__ __launch_bounds__(C::THREADS) void int4_kernel(Int4Problem q) {
             for (int v = 0; v < 4; ++v) acc[m][t][v] = fmaf(s[t][h * NG + e], part[m][t][v], acc[m][t][v]);
       }
     }
-    slot = slot + 1 == S ? 0 : slot + 1;
+    slot ^= 1;
     cnow += WK;
   };
   if (steps > 0) {
-#pragma unroll
-    for (int u = 0; u < S - 1; ++u) issue();
+    issue();
     for (int step = 0; step < steps; ++step) {
-      wait_vmcnt<(S - 2) * COPIES>();         // this step's copies (past the last step they are of zeros)
+      wait_vmcnt<0>();                        // this step's copies
       if constexpr (WN > 1) __syncthreads();
       else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       issue();                                // over the last step's, which everybody has read
@@ -361,17 +359,16 @@ __global__ __launch_bounds__(C::THREADS) void int4_kernel(Int4Problem q) {
   }
 }
 
-// TM, XR, TN, WK, WN, S
-enum { kI4One = 0, kI4OneWide, kI4OneShort, kI4Four, kI4FourWide, kI4Row, kI4RowWide, kI4Runs, kI4Many };
-using I4One = I4Cfg<1, 2, 1, 8, 1, 3>;
-using I4OneWide = I4Cfg<1, 2, 2, 4, 1, 3>;
-using I4OneShort = I4Cfg<1, 2, 2, 2, 1, 3>;
-using I4Four = I4Cfg<1, 4, 1, 8, 1, 3>;
-using I4FourWide = I4Cfg<1, 4, 2, 4, 1, 3>;
-using I4Row = I4Cfg<1, 16, 1, 4, 2, 2>;
-using I4RowWide = I4Cfg<1, 16, 2, 2, 2, 2>;
-using I4Runs = I4Cfg<1, 16, 2, 1, 4, 2>;
-using I4Many = I4Cfg<2, 32, 2, 1, 4, 2>;
+// TM, XR, TN, WK, WN
+enum { kI4One = 0, kI4OneWide, kI4Four, kI4FourWide, kI4Row, kI4RowWide, kI4Runs, kI4Many };
+using I4One = I4Cfg<1, 2, 1, 8, 1>;
+using I4OneWide = I4Cfg<1, 2, 2, 4, 1>;
+using I4Four = I4Cfg<1, 4, 1, 8, 1>;
+using I4FourWide = I4Cfg<1, 4, 2, 4, 1>;
+using I4Row = I4Cfg<1, 16, 1, 4, 2>;
+using I4RowWide = I4Cfg<1, 16, 2, 2, 2>;
+using I4Runs = I4Cfg<1, 16, 2, 1, 4>;
+using I4Many = I4Cfg<2, 32, 2, 1, 4>;
 
 template <class C>
 hipError_t start(const Int4Problem& q, int group, bool sbf16, unsigned grid, hipStream_t stream) {
@@ -389,7 +386,6 @@ auto with_config(int cfg, F f) {
   switch (cfg) {
     case kI4One: return f(I4One{});
     case kI4OneWide: return f(I4OneWide{});
-    case kI4OneShort: return f(I4OneShort{});
     case kI4Four: return f(I4Four{});
     case kI4FourWide: return f(I4FourWide{});
     case kI4Row: return f(I4Row{});
@@ -410,20 +406,19 @@ Int4Tile int4_tile(const BfProblem& p, int cus) {
   const bool wide = (rows + 15) / 16 * ((int64_t)p.N + 63) / 64 >= cus;
   if (runs) {
     // One row tile a run while most runs fit it: 512 rows over 32 experts of 4096 x
-    // 7168 (gated) 124 for 131, 128 rows 89 for 112, 1280 rows 245 for 202.
+    // 7168 (gated) 124 for 129, 128 rows 87 for 104, 1280 rows 234 for 189.
     t.cfg = rows <= 24 ? kI4Runs : kI4Many;
   } else if (rows <= 4) {
-    // One tile a wave and eight waves on k where k is long and columns are few:
-    // 1 x 7168 x 16384 16.7 for 18.7, 1 x 2112 x 7168 6.8 for 9.3, 1 x 16384 x 16384
-    // 30.1 for 27.3, 1 x 7168 x 2048 6.4 for 5.8.  Two waves for a short one: 1 x
-    // 24576 x 1536 8.6 for 11.0.  x takes half the LDS for two rows: 1 x 7168 x
-    // 16384 19.7 with four.
-    const bool two = rows <= 2;
-    if (!pairs && p.K > 4096 && !wide) t.cfg = two ? kI4One : kI4Four;
-    else t.cfg = !two ? kI4FourWide : p.K <= 2048 && wide ? kI4OneShort : kI4OneWide;
+    // One tile a wave and eight waves on k where columns are few, two tiles and four
+    // waves where they are many or k is short: 1 x 7168 x 16384 15.3 for 19.2, 1 x
+    // 2112 x 7168 7.0 for 9.2, 1 x 4096 x 2048 4.6 for 5.1; 1 x 16384 x 16384 28.5 for
+    // 26.3, 1 x 7168 x 2048 6.2 for 5.8, 1 x 24576 x 1536 14.4 for 8.7.  Copying two
+    // rows of x, not four, leaves room for another workgroup.
+    const bool narrow = !pairs && !wide && (p.K > 4096 || p.N <= 16 * cus);
+    t.cfg = rows <= 2 ? (narrow ? kI4One : kI4OneWide) : (narrow ? kI4Four : kI4FourWide);
   } else if (rows <= 64) {
-    // 16 x 16384 x 8192 20.5 for 25.4, 32 x 8192 x 8192 19.0 for 23.4, 24 x 4096 x
-    // 4096 17.3 for 11.6
+    // 16 x 16384 x 8192 22.4 for 25.4, 32 x 8192 x 8192 19.1 for 23.4, 48 x 16384 x
+    // 4096 24 for 41; 24 x 4096 x 7168 17.5 for 11.7, 13 x 7168 x 16384 35 for 25
     t.cfg = pairs || wide ? kI4RowWide : kI4Row;
   } else {
     t.cfg = kI4Many;
@@ -447,11 +442,12 @@ hipError_t launch_int4(const BfProblem& p, const Int4Tile& t, const uint8_t* cod
 // ------------------------------------------------- quantize and dequantize
 namespace {
 
-// Bound by HBM: 32 x 4096 x 7168 BF16 weights 438 us (5.4 TB/s) and back 465 (5.1).
-// A workgroup owns 32 rows x 512 k: a wave reads 512 k of a row, eight a lane,
-// eight rows in all.  Scales lie [group][row] in memory and cross in LDS, so that
-// they are written and read as runs of 32 rows.
-constexpr int kQuantRows = 32, kQuantCols = 512;
+// Bound by HBM: 32 x 4096 x 7168 BF16 weights 430 us (5.5 TB/s) and back 460 (5.2);
+// 2112 x 7168 11 and 8 us.
+// A workgroup owns 16 rows x 512 k: a wave reads 512 k of a row, eight a lane, four
+// rows in all (eight rows a wave: 13 us for 11).  Scales lie [group][row] in memory
+// and cross in LDS, so that they are written and read as runs of 16 rows.
+constexpr int kQuantRows = 16, kQuantCols = 512;
 
 template <class T>
 __device__ __forceinline__ void load_eight(const T* p, float (&f)[8]) {

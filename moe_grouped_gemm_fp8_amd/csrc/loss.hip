@@ -19,10 +19,20 @@ __global__ __launch_bounds__(1024) void loss_finish_kernel(BfLoss s, int tiles, 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int64_t r0 = (int64_t)blockIdx.x * 64; r0 < m; r0 += (int64_t)gridDim.x * 64) {
     const int64_t row = r0 + lane;
+    int target = -1;
+    float picked = 0.f;                  // (read before the pieces are waited for)
+    if (wave == 0 && row < m) {
+      target = target_of(s, row);
+      if (target >= 0) picked = s.picked[row];
+    }
     float top = kLowest, sum = 0.f;
-    auto add = [&](float2 v) {
-      const float t = fmaxf(top, v.x);
-      sum = sum * __builtin_amdgcn_exp2f((top - t) * kLog2e) + v.y * __builtin_amdgcn_exp2f((v.x - t) * kLog2e);
+    auto add = [&](const float2 (&v)[8]) {
+      float t = top;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) t = fmaxf(t, v[u].x);
+      sum *= __builtin_amdgcn_exp2f((top - t) * kLog2e);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) sum += v[u].y * __builtin_amdgcn_exp2f((v[u].x - t) * kLog2e);
       top = t;
     };
     if (row < m) {
@@ -30,19 +40,26 @@ __global__ __launch_bounds__(1024) void loss_finish_kernel(BfLoss s, int tiles, 
         float2 v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[u] = t0 + 16 * u < tiles ? s.pieces[(int64_t)(t0 + 16 * u) * m + row] : make_float2(kLowest, 0.f);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) add(v[u]);
+        add(v);
       }
     }
     part[wave][lane] = make_float2(top, sum);
     __syncthreads();
     if (wave == 0 && row < m) {
-      for (int w = 1; w < 16; ++w) add(part[w][lane]);
+      top = kLowest;
+      sum = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float2 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = part[8 * h + u][lane];
+        add(v);
+      }
       const float l = logf(sum);
       lse[row] = top + l;
       // (the maximum and the target's logit first: where the target dominates
       // they cancel exactly)
-      loss[row] = target_of(s, row) < 0 ? 0.f : (top - s.picked[row]) + l;
+      loss[row] = target < 0 ? 0.f : (top - picked) + l;
     }
     __syncthreads();
   }

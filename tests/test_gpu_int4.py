@@ -113,7 +113,8 @@ def _check(got, want, err, what):
 # m, n, k, group: single tokens, odd widths, every tile, partial chunks of k, several row blocks
 DENSE = [(1, 1, 32, 32), (1, 16, 128, 128), (1, 33, 96, 32), (1, 100, 4224, 128), (2, 130, 192, 64), (5, 37, 2080, 32),
          (16, 64, 1024, 64), (17, 48, 160, 32), (31, 259, 384, 128), (33, 70, 2112, 64), (64, 36, 512, 128), (65, 52, 288, 32),
-         (150, 20, 256, 128), (3, 8200, 128, 128), (4, 16400, 96, 32)]
+         (150, 20, 256, 128), (3, 8200, 128, 128), (4, 16400, 96, 32), (2, 4200, 288, 32), (3, 50, 160, 32), (4, 130, 4224, 128),
+         (64, 4200, 288, 32)]
 
 
 @pytest.mark.parametrize("exact", [True, False])
