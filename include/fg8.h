@@ -590,8 +590,10 @@ size_t fg8_linear_cross_entropy_workspace_bytes(int64_t m, int64_t vocab, int64_
  *   dloss, lse float [m]   dx bf16 [m][k], dw [vocab][k] float or bf16; either may
  *   be NULL and is then not computed.
  * The logits are computed again, as many classes at a time as make 512 MB of dl in
- * BF16 (256 at least).  dl is rounded to BF16 for dx and a bf16 dw; a float dw takes
- * it in two BF16 parts.  m >= 1.  workspace:
+ * BF16 (256 at least).  dl is rounded to BF16 for dx and a bf16 dw (2^-8 of each
+ * value at most, a target's -dloss (1 - p) alike in all rows of one dloss: a power of
+ * two keeps it where p is small); a float dw takes it in two BF16 parts.  m >= 1.
+ * workspace:
  * fg8_linear_cross_entropy_backward_workspace_bytes(m, vocab, k, dw_out) bytes under
  * gemm_bf16_epilogue's rules.
  */

@@ -901,20 +901,16 @@ hipError_t launch_tile(BfProblem p, const BfTile& t, hipStream_t stream) {
     if (t.cfg == kHigh) return start(bf16_kernel<BfHigh, AK, BK, MODE>, p, units, BfHigh::THREADS, stream);
   }
   if constexpr (MODE == kBfKRuns) {
-    if (p.add) {
-      if (t.cfg == kDuo) return start(bf16_kernel<BfDuo, AK, BK, MODE, true>, p, units, BfDuo::THREADS, stream);
-      if (t.cfg == kMid) return start(bf16_kernel<BfMid, AK, BK, MODE, true>, p, units, BfMid::THREADS, stream);
-    } else if (t.cfg == kDuo) return start(bf16_kernel<BfDuo, AK, BK, MODE>, p, units, BfDuo::THREADS, stream);
+    if (t.cfg == kDuo)
+      return p.add ? start(bf16_kernel<BfDuo, AK, BK, MODE, true>, p, units, BfDuo::THREADS, stream)
+                   : start(bf16_kernel<BfDuo, AK, BK, MODE>, p, units, BfDuo::THREADS, stream);
   }
   const unsigned cus = (unsigned)device_cu_count();
   p.grid = (int)(units < cus ? units : cus);
-  if constexpr (MODE == kBfKRuns) {
-    if (p.add) return start(bf16_big_kernel<AK, BK, MODE, false, kKindGated>, p, p.grid, 512, stream);
-  }
-  if constexpr (MODE == kBfDense && BK) {
+  if constexpr (BK && MODE != kBfRowRuns) {
     if (p.add)
       return t.cfg == kMid ? start(bf16_kernel<BfMid, AK, BK, MODE, true>, p, units, BfMid::THREADS, stream)
-                           : start(bf16_big_kernel<AK, BK, MODE, false, kKindGated>, p, p.grid, 512, stream);
+                           : start(bf16_big_kernel<AK, BK, MODE, false, true>, p, p.grid, 512, stream);
   }
   if (t.cfg == kMid) return start(bf16_kernel<BfMid, AK, BK, MODE>, p, units, BfMid::THREADS, stream);
   if constexpr (MODE == kBfDense && !AK && !BK) {

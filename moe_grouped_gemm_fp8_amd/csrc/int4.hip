@@ -442,8 +442,8 @@ hipError_t launch_int4(const BfProblem& p, const Int4Tile& t, const uint8_t* cod
 // ------------------------------------------------- quantize and dequantize
 namespace {
 
-// Bound by HBM: 32 x 4096 x 7168 BF16 weights 430 us (5.5 TB/s) and back 460 (5.2);
-// 2112 x 7168 11 and 8 us.
+// Bound by HBM: 32 x 4096 x 7168 BF16 weights 400 us (5.9 TB/s) and back 455 (5.3);
+// 2112 x 7168 10 and 8 us.
 // A workgroup owns 16 rows x 512 k: a wave reads 512 k of a row, eight a lane, four
 // rows in all (eight rows a wave: 13 us for 11).  Scales lie [group][row] in memory
 // and cross in LDS, so that they are written and read as runs of 16 rows.

@@ -249,3 +249,27 @@ def test_captured(dev):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
         assert all(torch.equal(a, b) for a, b in zip(both(), want))
+
+
+@pytest.mark.parametrize("experts,rows,n,k,tile", [(64, 1300, 1024, 1024, (128, 256)), (4, 8420, 2048, 2048, (256, 256))])
+def test_float_weight_gradient_of_many_tiles(dev, experts, rows, n, k, tile):
+    """A float32 dw of row runs where both of its products take the larger tiles,
+    against float32 products of the same dz on the GPU (TF32 is off): its dz is
+    2^-15 off, its sums and theirs 4 (rows + 1) 2^-24 of the absolute sums."""
+    fg8 = _fg8()
+    choice = fg8.bf16_tile_choice("grouped_gemm_bf16_wgrad", rows, 2 * n, k, groups=experts)
+    assert (choice["bm"], choice["bn"]) == tile
+    g = torch.Generator(device=dev).manual_seed(experts)
+    x, dh, z = (torch.randn(rows, c, device=dev, generator=g).to(BF16) for c in (k, n, 2 * n))
+    w = torch.zeros(experts, 2 * n, k, dtype=BF16, device=dev)
+    cuts = torch.sort(torch.randperm(rows, generator=torch.Generator().manual_seed(1))[:experts - 1]).values
+    off = torch.cat([torch.tensor([0]), cuts, torch.tensor([rows])]).to(torch.int32)
+    _, dw = fg8.grouped_gemm_bf16_gated_backward(dh, x, w, z, off.to(dev), needs=(False, True))
+    zg, zu = z[:, :n].double(), z[:, n:].double()
+    p = torch.sigmoid(zg)
+    dz = torch.cat([dh.double() * zu * (p + zg * p * (1 - p)), dh.double() * zg * p], 1).float()
+    size = torch.cat([dh.float().abs() * zu.float().abs() * 1.13, dh.float().abs() * (zg * p).float().abs()], 1)
+    for e in (0, 1, experts // 2, experts - 1):
+        r = slice(int(off[e]), int(off[e + 1]))
+        want, most = dz[r].T @ x[r].float(), size[r].T @ x[r].float().abs()
+        assert ((dw[e] - want).abs() <= (2.0 ** -15 + 2.0 ** -17 + 4 * (r.stop - r.start + 1) * 2.0 ** -24) * most + 1e-30).all(), e

@@ -102,3 +102,30 @@ def test_head_past_2_31(dev):
     dl[at, t - (v - 200)] -= 1
     want, size = dl.T @ x.float(), dl.abs().T @ x.float().abs()
     assert ((dw[-200:].float() - want).abs() <= (2.0 ** -8 + e + 2.0 ** -16) * size + 2.0 ** -8 * want.abs() + 1e-12).all()
+
+
+def test_most_classes(dev):
+    """As many classes as a head may have, few rows: pieces of the vocabulary whose
+    dx is added up by the tiles of few rows."""
+    import moe_grouped_gemm_fp8_amd as fg8
+    print("loss backward, 100 rows, 2^22 classes of 16", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    m, v, k = 100, 1 << 22, 16
+    assert 2 * m * v > 512 << 20
+    x, w = _normal(g, m, k), _normal(g, v, k)
+    t = torch.randint(0, v, (m,), device=dev, generator=g)
+    loss, lse = fg8.linear_cross_entropy(x, w, t)
+    logits = x.float() @ w.float().T
+    want = torch.logsumexp(logits.double(), 1)
+    e = 4 * (k + 1) * 2.0 ** -24 * float((x.float().abs() @ w.float().abs().amax(0)).max())
+    assert ((lse - want).abs() <= e + 2.0 ** -17 + 2.0 ** -22 * want.abs()).all()
+    dx, dw = fg8.linear_cross_entropy_backward(torch.ones(m, device=dev), x, w, t, lse, dw_dtype=BF16)
+    dl = torch.exp(logits - lse[:, None])
+    dl[torch.arange(m, device=dev), t] -= 1
+    size = dl.abs() @ w.float().abs()
+    # (float32 sums of 2^22 terms on both sides, in blocks: 2^-24 of the absolute sums
+    # for each of some thousand additions in a row at most)
+    assert ((dx.float() - dl @ w.float()).abs() <= (2.0 ** -8 + e + 2.0 ** -12) * size + 2.0 ** -8 * (dl @ w.float()).abs()).all()
+    some = torch.cat([t[:20], torch.tensor([0, 2097151, 2097152, v - 1], device=dev)])
+    want, size = dl[:, some].T @ x.float(), dl[:, some].abs().T @ x.float().abs()
+    assert ((dw[some].float() - want).abs() <= (2.0 ** -8 + e + 2.0 ** -16) * size + 2.0 ** -8 * want.abs() + 1e-12).all()
