@@ -1114,8 +1114,8 @@ fg8_status grouped_gemm_bf16_int4(const uint16_t* x, int64_t ldx, const uint8_t*
 // ---------------------------------------------- cross entropy of a linear head
 namespace {
 
-// The forward pass's workspace: counters (left alone: another call on the same
-// workspace finds them at zero), target logits, and each column tile's pieces.
+// The forward pass's workspace: counters and partial tiles as every product's, target
+// logits, and each column tile's pieces.
 struct LossSpace {
   size_t picked, pieces, total;
   int64_t tiles;
@@ -1126,10 +1126,16 @@ fg8::BfProblem loss_bf16(int64_t m, int64_t v, int64_t k, int kind) {
   return p;
 }
 LossSpace loss_space(int64_t m, int64_t v, int64_t k) {
-  const fg8::BfTile t = fg8::bf16_tile(loss_bf16(m, v, k, fg8::kKindLse), fg8::device_cu_count());
+  const fg8::BfProblem p = loss_bf16(m, v, k, fg8::kKindLse);
+  const int cus = fg8::device_cu_count();
+  const fg8::BfTile t = fg8::bf16_tile(p, cus);
   LossSpace s{};
   s.tiles = (v + t.bn - 1) / t.bn;
+  // (the counters keep their place whatever the shape: another call on the same
+  // workspace finds them at zero)
   s.picked = fg8::kSplitKCounterBytes;
+  const size_t product = fg8::bf16_workspace_bytes(p, cus);
+  if (product > s.picked) s.picked = product;
   s.pieces = s.picked + (size_t)up(m * 4, 16);
   s.total = s.pieces + (size_t)s.tiles * m * 8;
   return s;
@@ -1175,7 +1181,7 @@ LossBackwardSpace loss_backward_space(int64_t m, int64_t v, int64_t k, bool rest
       fg8::BfProblem p = dense_bf16(m, k, n, false, true), q = dense_bf16(n, k, m, true, true);
       p.add = q.add = add;
       p.parts = s.parts;
-      for (const fg8::BfProblem& r : {p, q}) {
+      for (const fg8::BfProblem& r : {p, q, loss_bf16(m, n, k, fg8::kKindDlogits)}) {
         const size_t b = fg8::bf16_workspace_bytes(r, cus);
         if (b > s.products) s.products = b;
       }

@@ -987,13 +987,15 @@ BfTile bf16_tile(const BfProblem& p, int cus) {
   t.threads = kThreads[t.cfg];
   t.persistent = t.cfg == kBig;
   t.splits = p.parts ? p.parts : 1;
-  if (dense && t.cfg != kBig && t.cfg != kFew && !loss) {
+  if (dense && t.cfg != kBig && t.cfg != kFew) {
     // One workgroup a CU; two where several row tiles read the same weights
     // (64 x 2112 x 7168 14.1 in 6 splits, 16.2 in 12; 128 x 2112 x 7168 18.9
-    // in 6, 19.8 in 3), and five steps a split at least.
+    // in 6, 19.8 in 3), and five steps a split at least.  A head's loss: 40 x 5000
+    // x 7168 28 for 64 unsplit, 200 x 8000 x 4096 40 for 51 (in tiles of kDeep, of
+    // which a CU holds one; 46 at two a CU).
     const int64_t u = units(t.cfg), steps = (p.K + kBK - 1) / kBK;
     if (4 * u < 3 * cus && u <= kSplitKMaxTiles) {
-      int64_t s = (rows > t.bm ? 2 * cus : cus) / u;
+      int64_t s = (rows > t.bm && t.cfg != kDeep ? 2 * cus : cus) / u;
       if (s > steps / 5) s = steps / 5;
       if (s > kBfMaxSplits) s = kBfMaxSplits;
       if (s > 1) t.splits = (int)s;

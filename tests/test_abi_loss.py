@@ -23,6 +23,9 @@ def test_forward(L):
     need = L.fg8_linear_cross_entropy_workspace_bytes(40, 1000, 64)
     # counters, target logits, a maximum and a sum for each row and 128 classes
     assert need == 4096 + 160 + 8 * 40 * 8
+    # with a long k partial tiles of 64 x 128 besides
+    longer = L.fg8_linear_cross_entropy_workspace_bytes(40, 1000, 4096)
+    assert longer > need and (longer - need) % (64 * 128 * 4) == 0
     assert L.fg8_linear_cross_entropy_workspace_bytes(0, 1000, 64) == 0
 
     def call(x=ok, ldx=64, w=ok, t=ok, wide=1, loss=ok, lse=ok, m=40, v=1000, k=64, ws=ok, size=need):

@@ -49,9 +49,9 @@ def _inputs(case, m, v, k):
     return x, w, t
 
 
-# m, vocab, k: one row, one class, odd vocabularies, every tile
+# m, vocab, k: one row, one class, odd vocabularies, every tile, products in several k ranges
 CASES = [(1, 1, 8), (1, 1000, 64), (2, 77, 200), (13, 129, 72), (64, 300, 136), (65, 513, 64), (130, 1001, 328), (257, 40, 512), (500, 4099, 72),
-         (1100, 8200, 64)]
+         (1100, 8200, 64), (53, 300, 2048), (3, 1158, 4104), (130, 520, 4096), (200, 2000, 2120)]
 
 
 def _close(got, want, err, what):
