@@ -618,7 +618,11 @@ hipError_t launch_act_backward(const uint16_t* dy, int64_t lddy, const uint16_t*
 
 hipError_t launch_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* z, int act, int64_t m,
                                  int64_t n, bool rest, uint16_t* dz, int64_t ldz, hipStream_t stream) {
-  const int chunks = act_backward_chunks(m, n);
+  // About 2048 workgroups, a row a wave at least: the whole backward pass of 300 x 520,
+  // k = 256, 24 us (33 at four rows a wave), of 64 x 2048, k = 2048, 25 (31).
+  const int64_t blocks = (n + kActCols - 1) / kActCols;
+  int64_t chunks = (2048 + blocks - 1) / blocks;
+  if (chunks > (m + 3) / 4) chunks = (m + 3) / 4;
   const int64_t per = (m + chunks - 1) / chunks;
   hipLaunchKernelGGL(rest ? gated_backward_kernel<true> : gated_backward_kernel<false>,
                      dim3((unsigned)((n + kActCols - 1) / kActCols), (unsigned)chunks), dim3(256), 0, stream, dh,
