@@ -955,8 +955,8 @@ def linear_cross_entropy_backward(dloss, x, w, targets, lse, dw_dtype=torch.floa
     """Gradients of linear_cross_entropy: dloss float32 [m] (1 / count for a mean),
     lse as the forward pass returned it -> (dx bf16 [m, k], dw dw_dtype [vocab,
     k]); `needs` leaves out (None) what is not wanted.  dx and a bfloat16 dw take
-    the logits' gradients rounded to bfloat16, a float32 dw to 2^-16 (a second
-    product)."""
+    the logits' gradients rounded to bfloat16, a float32 dw to 2^-16 (in two
+    parts)."""
     ldx, wide, m, vocab, k = _head(x, w, targets)
     for name, t in (("dloss", dloss), ("lse", lse)):
         _dev(t, torch.float32, name)

@@ -1146,9 +1146,10 @@ LossSpace loss_space(int64_t m, int64_t v, int64_t k) {
 // where there is more than one piece or part.
 constexpr int64_t kLossPieceBytes = (int64_t)512 << 20;    // of dlogits at a time
 struct LossBackwardSpace {
-  size_t products, dz, rest, sums, total;
+  size_t products, dz, rest, sums, twice, total;
   int64_t piece, ldz;       // classes of a piece, the last one may have fewer
   int parts;                // of dx's sums within a piece (0: the product's own choice)
+  bool stacked;             // a float dw's two parts of dlogits as one product's rows
 };
 // dx [m][k] sums over a piece's classes, many for its few tiles: parts of them, each
 // with sums of its own, fill the last round of the CUs.  4095 x 2048 over 50,176
@@ -1175,10 +1176,16 @@ LossBackwardSpace loss_backward_space(int64_t m, int64_t v, int64_t k, bool rest
   s.piece = v <= fit || v <= 256 ? v : up((v + (v + most - 1) / most - 1) / ((v + most - 1) / most), unit);
   s.ldz = up(s.piece, 8);
   s.parts = loss_dx_parts(m, k, s.piece, cus);
+  // A float dw takes dlogits in two BF16 parts, of which the second lies under the
+  // first: with x under x one product of 2 m rows adds them, and dw is written once
+  // rather than written, read and written.  x's copies move 6 k bytes a row, what is
+  // saved 8 k a class (128 x 128 x 4096 37 us for 64 in two products, 61 x 32003 x
+  // 2048 121 for 264, 8192 x 8192 x 4096 1680 for 1710).
+  s.stacked = rest && m <= s.piece;
   s.products = fg8::kSplitKCounterBytes;
   for (int64_t n : {s.piece, v % s.piece ? v % s.piece : s.piece})
     for (int add = 0; add < 2; ++add) {
-      fg8::BfProblem p = dense_bf16(m, k, n, false, true), q = dense_bf16(n, k, m, true, true);
+      fg8::BfProblem p = dense_bf16(m, k, n, false, true), q = dense_bf16(n, k, s.stacked ? 2 * m : m, true, true);
       p.add = q.add = add;
       p.parts = s.parts;
       for (const fg8::BfProblem& r : {p, q, loss_bf16(m, n, k, fg8::kKindDlogits)}) {
@@ -1186,11 +1193,12 @@ LossBackwardSpace loss_backward_space(int64_t m, int64_t v, int64_t k, bool rest
         if (b > s.products) s.products = b;
       }
     }
-  const size_t dz = (size_t)up(m * s.ldz * 2, 16);
+  const size_t dz = (size_t)m * s.ldz * 2;      // (a multiple of 16)
   s.dz = s.products;
   s.rest = s.dz + dz;
   s.sums = s.rest + (rest ? dz : 0);
-  s.total = s.sums + (s.piece < v || s.parts > 1 ? (size_t)m * k * 4 * (s.parts ? s.parts : 1) : 0);
+  s.twice = s.sums + (s.piece < v || s.parts > 1 ? (size_t)m * k * 4 * (s.parts ? s.parts : 1) : 0);
+  s.total = s.twice + (s.stacked ? (size_t)m * k * 4 : 0);
   return s;
 }
 
@@ -1273,6 +1281,12 @@ fg8_status linear_cross_entropy_backward(const float* dloss, const uint16_t* x, 
   p.a = x; p.lda = ldx; p.ldb = k; p.d = dz; p.ldd = here.ldz;
   p.loss.targets = targets; p.loss.targets64 = targets_are_int64; p.loss.classes = (int)vocab;
   p.loss.lse = lse; p.loss.dloss = dloss; p.loss.rest = rest ? left : nullptr;
+  const bool stacked = rest && here.stacked;
+  uint16_t* twice = (uint16_t*)((char*)workspace + here.twice);
+  if (stacked) {
+    const hipError_t e = fg8::launch_twice(x, ldx, m, k, twice, stream);
+    if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  }
   for (int64_t v0 = 0; v0 < vocab; v0 += here.piece) {
     const int64_t n = vocab - v0 < here.piece ? vocab - v0 : here.piece;
     p.N = (int)n; p.b = w + v0 * k; p.loss.first = (int)v0;
@@ -1286,10 +1300,11 @@ fg8_status linear_cross_entropy_backward(const float* dloss, const uint16_t* x, 
       if (fg8_status s = run_bf16(q, fn, stream)) return s;
     }
     // A float dw takes dlogits in two BF16 parts, as gemm_bf16_epilogue_backward's does.
-    for (int part = 0; part < (dw ? rest ? 2 : 1 : 0); ++part) {
-      fg8::BfProblem q = dense_bf16(n, k, m, true, true);
+    for (int part = 0; part < (dw ? rest && !stacked ? 2 : 1 : 0); ++part) {
+      fg8::BfProblem q = dense_bf16(n, k, stacked ? 2 * m : m, true, true);
       q.counters = p.counters; q.partial = p.partial;
-      q.a = part ? left : dz; q.lda = here.ldz; q.b = x; q.ldb = ldx; q.ldd = k;
+      q.a = part ? left : dz; q.lda = here.ldz; q.ldd = k;
+      q.b = stacked ? twice : x; q.ldb = stacked ? k : ldx;
       q.out_bf16 = !rest; q.add = part;
       q.d = (char*)dw + v0 * k * (rest ? 4 : 2);
       if (fg8_status s = run_bf16(q, fn, stream)) return s;

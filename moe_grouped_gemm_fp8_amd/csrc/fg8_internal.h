@@ -181,6 +181,7 @@ hipError_t launch_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_
 hipError_t launch_loss_finish(const BfLoss& s, int64_t tiles, int64_t m, float* loss, float* lse, hipStream_t stream);
 // y [n] = the sum of x [parts][n], rounded to BF16.
 hipError_t launch_sum_bf16(const float* x, int parts, int64_t n, uint16_t* y, hipStream_t stream);
+hipError_t launch_twice(const uint16_t* x, int64_t ldx, int64_t m, int64_t k, uint16_t* y, hipStream_t stream);
 
 // --------------------------------------------------------------- layer norm
 int64_t layer_norm_teams(int64_t rows, int64_t cols, bool bf16, int num_cus);

@@ -1,5 +1,5 @@
 // What the softmax cross entropy of a linear head needs beside its products: the
-// rows' statistics joined over the vocabulary, and dx's sums added and rounded.
+// rows' statistics joined over the vocabulary, dx's sums added and rounded, and x twice.
 //
 //   lse = M + log sum over tiles of s_t e^(m_t - M),  M = max over tiles of m_t
 //   loss = lse - (the target's logit), 0 for a row without a target
@@ -77,6 +77,19 @@ __global__ __launch_bounds__(256) void sum_kernel(const float* __restrict__ x, i
   }
 }
 
+// x [m][ldx] twice, one under the other (k a multiple of 8), for the two parts of
+// dlogits that a float weight gradient takes.  A launch's latency at few rows.
+__global__ __launch_bounds__(256) void twice_kernel(const uint16_t* __restrict__ x, int64_t ldx, int64_t m, int64_t k,
+                                                    uint16_t* __restrict__ y) {
+  const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
+  if (c >= k) return;
+  for (int64_t r = blockIdx.x; r < m; r += gridDim.x) {
+    const uint4 v = *reinterpret_cast<const uint4*>(x + r * ldx + c);
+    *reinterpret_cast<uint4*>(y + r * k + c) = v;
+    *reinterpret_cast<uint4*>(y + (m + r) * k + c) = v;
+  }
+}
+
 constexpr int64_t kMostBlocks = 1 << 16;
 
 }  // namespace
@@ -88,6 +101,12 @@ hipError_t launch_loss_finish(const BfLoss& s, int64_t tiles, int64_t m, float* 
 
 hipError_t launch_sum_bf16(const float* x, int parts, int64_t n, uint16_t* y, hipStream_t stream) {
   hipLaunchKernelGGL(sum_kernel, dim3((unsigned)std::min((n + 2047) / 2048, kMostBlocks)), dim3(256), 0, stream, x, parts, n, y);
+  return hipGetLastError();
+}
+
+hipError_t launch_twice(const uint16_t* x, int64_t ldx, int64_t m, int64_t k, uint16_t* y, hipStream_t stream) {
+  const dim3 grid((unsigned)std::min(m, kMostBlocks), (unsigned)((k + 2047) / 2048));
+  hipLaunchKernelGGL(twice_kernel, grid, dim3(256), 0, stream, x, ldx, m, k, y);
   return hipGetLastError();
 }
 

@@ -41,7 +41,9 @@ def test_forward(L):
 def test_backward(L):
     size = L.fg8_linear_cross_entropy_backward_workspace_bytes
     need = size(40, 1000, 64, 1)
-    assert size(40, 1000, 64, 0) == need + 40 * 1000 * 2          # what dlogits' rounding left
+    # what dlogits' rounding left, and x twice where there are no more rows than classes
+    assert size(40, 1000, 64, 0) == need + 40 * 1000 * 2 + 2 * 40 * 64 * 2
+    assert size(80, 72, 64, 0) == size(80, 72, 64, 1) + 80 * 72 * 2
     # one piece of the vocabulary while its dlogits are 512 MB at most, then pieces of
     # one size in units of 8192 classes, and dx's sums
     one, two = size(8192, 32768, 64, 1), size(8192, 32769, 64, 1)

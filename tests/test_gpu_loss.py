@@ -141,6 +141,19 @@ def test_pieces_of_the_vocabulary(dev):
     assert ((dwf[classes] - want).abs() <= (2.0 ** -13 + 2 * (m + 1) * 2.0 ** -24) * size).all()
 
 
+@pytest.mark.parametrize("m,v,k", [(33, 70, 72), (70, 33, 2056)])
+def test_float_weight_gradient_of_strided_rows(dev, m, v, k):
+    """Rows a stride apart, no more of them than classes and more: as laid close."""
+    x, w, t = _inputs(60, m, v, k)
+    wide = torch.full((m, k + 24), float("nan"), dtype=BF16)
+    wide[:, 8:8 + k] = x
+    fg8 = _fg8()
+    w, t, dloss = w.to(dev), t.to(dev), torch.rand(m, generator=_gen(60)).to(dev)
+    _, lse = fg8.linear_cross_entropy(x.to(dev), w, t)
+    for a, b in zip(*(fg8.linear_cross_entropy_backward(dloss, r, w, t, lse) for r in (x.to(dev), wide.to(dev)[:, 8:8 + k]))):
+        assert torch.equal(a, b) and a.isfinite().all()
+
+
 def test_against_differences(dev):
     """The mean loss along a direction, by central differences: a relative error
     of the step's square (2^-8) and the gradients' BF16 rounding: 0.02 of the
