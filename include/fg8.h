@@ -515,6 +515,7 @@ size_t fg8_gemm_bf16_gated_backward_workspace_bytes(int64_t m, int64_t n, int64_
  * `group` (32, 64 or 128) consecutive columns:
  *   s = fl32(amax / 7) (1 where that is 0), rounded to the scales' type;
  *   code = rne(fl32(w / s)) + 8, in 1 .. 15;   the code stands for (code - 8) s
+ *   (the quotient is limited to -7 .. 7, which it passes only where s is subnormal)
  *   q       uint8 [rows][cols / 2], column 2 j in the low four bits of byte j
  *   scales  [cols / group][rows] float (scales_are_bf16 = 0) or bf16 (1)
  * A group with a NaN or an infinity gets a NaN for its scale, and stands for NaN.

@@ -2,7 +2,7 @@
 // few rows of BF16, dense or over ragged row runs.
 //
 //   s = fl32(amax / 7) of GROUP consecutive k of a row (1 where that is 0),
-//   rounded to the scales' type;  code = rne(fl32(w / s)) + 8;  value (code - 8) s
+//   rounded to the scales' type;  code = rne(fl32(w / s) within -7 .. 7) + 8;  value (code - 8) s
 //   codes [n][k / 2], element 2 j in the low half of byte j; scales [k / GROUP][n]
 //
 //   D[m][n] = sum over groups of s[group][n] * sum over its k of (code - 8) x[m][k]
@@ -498,7 +498,10 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const T* __restrict_
     if (lane % LANES == 0) kept[lane / LANES][wave * PER + u] = s;
     // w / s rounded correctly from the correctly rounded reciprocal (Markstein:
     // t = w r, then t + r (w - t s)), where nothing leaves the range of normal
-    // numbers; one addition then rounds it to the code, 8 on top
+    // numbers; one addition then rounds it to the code, 8 on top.  A scale that is a
+    // normal number is 2^-8 below amax / 7 at most, and no quotient rounds past 7; one
+    // of few bits may be far below it (amax of 10 smallest steps: a scale of 1), so
+    // there the quotient is limited (a NaN, beside a NaN for the scale, to -7).
     uint32_t code = 0;
     auto put = [&](int e, float t) { code |= (__float_as_uint(t + (12582912.f + 8.f)) & 15u) << (4 * e); };
     if (__all(s > 0x1p-100f && s < 0x1p100f)) {
@@ -510,7 +513,7 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const T* __restrict_
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) put(e, __fdiv_rn(f[u][e], s));
+      for (int e = 0; e < 8; ++e) put(e, fminf(fmaxf(__fdiv_rn(f[u][e], s), -7.f), 7.f));
     }
     if (u < here && c < cols) store_nt(q + u * (cols / 2), code);
   }

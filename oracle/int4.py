@@ -15,7 +15,8 @@ def bf16(v):
 def quantize(w, group, scales_bf16=False):
     """(codes uint8 [rows, cols], scales float32 [cols / group, rows]) of finite
     float32 w [rows, cols]: s = fl32(amax / 7), 1 where that is 0; code =
-    rne(fl32(w / s)) + 8."""
+    rne(fl32(w / s)) + 8, the quotient limited to -7 .. 7 (a subnormal s may be far
+    below amax / 7)."""
     w = np.asarray(w, np.float32)
     rows, cols = w.shape
     codes = np.empty((rows, cols), np.uint8)
@@ -26,7 +27,7 @@ def quantize(w, group, scales_bf16=False):
         if scales_bf16:
             s = bf16(s)
         s = np.where(s == 0, np.float32(1), s)
-        codes[:, j * group:(j + 1) * group] = np.rint((part / s[:, None]).astype(np.float32)).astype(np.int32) + 8
+        codes[:, j * group:(j + 1) * group] = np.rint(np.clip((part / s[:, None]).astype(np.float32), -7, 7)).astype(np.int32) + 8
         scales[j] = s
     return codes, scales
 

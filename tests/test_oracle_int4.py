@@ -35,3 +35,16 @@ def test_error_is_half_a_step():
             off = np.abs(int4.values(codes, scales) - w)
             # (a BF16 scale may be 2^-8 below amax / 7, and the largest weight 7 times that further off)
             assert (off <= np.repeat(scales.T, group, 1) * (0.5 + 7 * 2.0 ** -8 * bf) * (1 + 1e-6)).all()
+
+
+def test_subnormal_scales():
+    """amax of 8, 10, 17 and 24 of the smallest steps: scales of 1, 1, 2 and 3 of
+    them, quotients past 7 limited to it."""
+    for step, bf in ((2.0 ** -149, False), (2.0 ** -133, True)):
+        w = np.zeros((4, 32), np.float32)
+        for r, top in enumerate((8, 10, 17, 24)):
+            w[r, :4] = np.array([top, -top, 4, -1], np.float64) * step
+        codes, scales = int4.quantize(w, 32, bf)
+        assert (scales[0] / np.float32(step)).tolist() == [1, 1, 2, 3]
+        assert codes[:, :4].tolist() == [[15, 1, 12, 7], [15, 1, 12, 7], [15, 1, 10, 8], [15, 1, 9, 8]]
+        assert (codes[:, 4:] == 8).all()
