@@ -596,7 +596,7 @@ size_t fg8_linear_cross_entropy_workspace_bytes(int64_t m, int64_t vocab, int64_
  * two keeps it where p is small); a float dw takes it in two BF16 parts.  m >= 1.
  * workspace:
  * fg8_linear_cross_entropy_backward_workspace_bytes(m, vocab, k, dw_out) bytes under
- * gemm_bf16_epilogue's rules.
+ * gemm_bf16_epilogue's rules; without dw, FG8_OUT_BF16's are enough.
  */
 fg8_status linear_cross_entropy_backward(const float* dloss, const uint16_t* x, int64_t ldx,
                                          const uint16_t* w, const void* targets,

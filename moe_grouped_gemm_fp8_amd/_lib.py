@@ -970,8 +970,9 @@ def linear_cross_entropy_backward(dloss, x, w, targets, lse, dw_dtype=torch.floa
     L = lib()
     stream = _stream_of(x)
     if workspace is None:
+        # (the second part of the logits' gradients is a float dw's alone)
         workspace, ws, ws_bytes = _workspace_of(
-            L.fg8_linear_cross_entropy_backward_workspace_bytes(m, vocab, k, code), x, stream)
+            L.fg8_linear_cross_entropy_backward_workspace_bytes(m, vocab, k, code if needs[1] else OUT_BF16), x, stream)
     else:
         ws, ws_bytes = _workspace_given(workspace)
     _check(L.linear_cross_entropy_backward(dloss.data_ptr(), x.data_ptr(), ldx, w.data_ptr(), targets.data_ptr(), wide,

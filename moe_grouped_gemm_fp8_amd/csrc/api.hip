@@ -1271,7 +1271,7 @@ fg8_status linear_cross_entropy_backward(const float* dloss, const uint16_t* x, 
   if (dw) FG8_CHECK_PTR(dw);
   FG8_CHECK_LD(ldx, k, 8);
   const bool rest = dw && dw_out == FG8_OUT_F32;
-  const LossBackwardSpace here = loss_backward_space(m, vocab, k, dw_out == FG8_OUT_F32);
+  const LossBackwardSpace here = loss_backward_space(m, vocab, k, rest);
   fg8::BfProblem p = loss_bf16(m, 0, k, fg8::kKindDlogits);
   if (fg8_status s = set_workspace(p, fn, workspace, workspace_bytes, here.total)) return s;
   uint16_t* dz = (uint16_t*)((char*)workspace + here.dz);
