@@ -540,10 +540,12 @@ fg8_status int4_dequantize(const uint8_t* q, const void* scales, int32_t scales_
  *              rows, then n up rows); no bias, no residual
  *   x bf16 [m][ldx]   q, scales as above (rows n or 2 n, cols k)
  *   bias, residual, activation, y as gemm_bf16_epilogue; m >= 0, any n
- * Sums run over (16 + code) x less 24 x: an x of 2^112 or more, or an infinite one,
- * makes its row NaN.  Any m is right, in pieces of 16 or 32 rows that read the
- * weights each; it is made for one to some dozens (beyond some hundreds,
- * int4_dequantize and a BF16 product are faster).
+ * Sums run over (16 + code) x less 24 x.  While every |x| is below 2^112 no sum of a
+ * group leaves FP32's range; larger ones may, and their row is then NaN, as an infinite
+ * x makes it.
+ * Any m is right, in pieces of 16 or 32 rows that read the weights each; it is made
+ * for one to some dozens (beyond some hundreds, int4_dequantize and a BF16 product
+ * are faster).
  */
 fg8_status gemm_bf16_int4(const uint16_t* x, int64_t ldx, const uint8_t* q, const void* scales,
                           int32_t scales_are_bf16, int32_t group, const void* bias,
