@@ -48,8 +48,9 @@
  *     block whose block_expert value lies outside [0, E) is skipped (its
  *     output rows are left as they were), and valid_rows values are clamped
  *     to [0, cap] (gemm_mxfp8: [0, m]).
- *   - Calls may run concurrently on different streams; a split-K workspace
- *     must not be shared by calls that can overlap.
+ *   - Calls may run concurrently on different streams; a workspace must not be
+ *     shared by calls that can overlap (those of two threads on one stream can:
+ *     their kernels may be queued in turn).
  *   - Every GEMM takes 128 <= k <= 2^24 - 128 with k % 128 == 0 (else
  *     FG8_EUNSUPPORTED): the copies into LDS address a tile of up to 256
  *     rows with 32-bit offsets.

@@ -279,9 +279,10 @@ def _new_workspace(nbytes, t):
 
 
 def _workspace_of(nbytes, t, stream):
-    """A workspace per (t's device, stream) with its counters at zero, as
-    (tensor, pointer, bytes); the kernels leave them so, and it is reused as
-    is.  One above WS_KEEP_BYTES goes back with the call.  A call recorded in a
+    """A workspace per (t's device, stream, calling thread) with its counters at
+    zero, as (tensor, pointer, bytes); the kernels leave them so, and it is reused
+    as is.  (Threads that share a stream may enqueue their calls' kernels in turn,
+    and a call of several keeps data here between them.)  One above WS_KEEP_BYTES goes back with the call.  A call recorded in a
     graph gets one of its own, with its arrival counters cleared by the graph,
     and leaves nothing here: a cached one may be replaced while the graph
     lives, and one that a graph allocated belongs to the graph, whose clearing
@@ -291,9 +292,14 @@ def _workspace_of(nbytes, t, stream):
     if nbytes > WS_KEEP_BYTES or torch.cuda.is_current_stream_capturing():
         ws = _new_workspace(nbytes, t)
     else:
-        key = (t.device, stream)
+        key = (t.device, stream, threading.get_ident())
         ws = _ws_cache.get(key)
         if ws is None or ws.numel() < nbytes:
+            if ws is None:               # (what threads kept that have ended)
+                alive = {th.ident for th in threading.enumerate()}
+                for other in list(_ws_cache):
+                    if other[2] not in alive and other[2] != key[2]:
+                        _ws_cache.pop(other, None)
             ws = None
             _ws_cache.pop(key, None)     # (its memory serves the larger one)
             ws = _ws_cache[key] = _new_workspace(nbytes, t)
