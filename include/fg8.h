@@ -693,6 +693,15 @@ fg8_status fg8_tile_choice(int32_t mode, int64_t m, int64_t n, int64_t k, int32_
 fg8_status fg8_bf16_tile_choice(int32_t product, int64_t m, int64_t n, int64_t k, int32_t groups,
                                 int32_t num_cus, int32_t* out);
 
+/* The same for the products with an epilogue of their own: product 0
+ * gemm_bf16_gated, 1 grouped_gemm_bf16_gated (n the columns of h, tile columns
+ * counted over gate and up rows), 2 linear_cross_entropy (n the vocabulary), 3 the
+ * logits of its backward pass, 4 that pass's dx (a piece of the vocabulary's, the
+ * splits the ranges of its classes); groups 1 but for product 1.  FG8_EINVAL as
+ * above, and for sizes that the calls refuse. */
+fg8_status fg8_bf16_fused_tile_choice(int32_t product, int64_t m, int64_t n, int64_t k, int32_t groups,
+                                      int32_t num_cus, int32_t* out);
+
 /* Text of the calling thread's last non-OK status ("" if none). */
 const char* fg8_last_error(void);
 

@@ -1166,14 +1166,17 @@ int loss_dx_parts(int64_t m, int64_t k, int64_t classes, int cus) {
   }
   return best > 1 ? best : 0;
 }
+// Classes of a piece.  Pieces of one size, rounded up to 8192 classes: 32 tiles'
+// columns, so that only the last piece leaves rounds of the CUs unfilled.
+int64_t loss_piece(int64_t m, int64_t v) {
+  const int64_t fit = kLossPieceBytes / (2 * m), unit = fit >= 8192 ? 8192 : 256;
+  const int64_t most = fit < 256 ? 256 : fit / unit * unit;
+  return v <= fit || v <= 256 ? v : up((v + (v + most - 1) / most - 1) / ((v + most - 1) / most), unit);
+}
 LossBackwardSpace loss_backward_space(int64_t m, int64_t v, int64_t k, bool rest) {
   const int cus = fg8::device_cu_count();
   LossBackwardSpace s{};
-  // Pieces of one size, rounded up to 8192 classes: 32 tiles' columns, so that only
-  // the last piece leaves rounds of the CUs unfilled.
-  const int64_t fit = kLossPieceBytes / (2 * m), unit = fit >= 8192 ? 8192 : 256;
-  const int64_t most = fit < 256 ? 256 : fit / unit * unit;
-  s.piece = v <= fit || v <= 256 ? v : up((v + (v + most - 1) / most - 1) / ((v + most - 1) / most), unit);
+  s.piece = loss_piece(m, v);
   s.ldz = up(s.piece, 8);
   s.parts = loss_dx_parts(m, k, s.piece, cus);
   // A float dw takes dlogits in two BF16 parts, of which the second lies under the
@@ -1315,6 +1318,29 @@ fg8_status linear_cross_entropy_backward(const float* dloss, const uint16_t* x, 
     if (e != hipSuccess) return fail(FG8_EHIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
   }
   g_err[0] = 0;
+  return FG8_OK;
+}
+
+fg8_status fg8_bf16_fused_tile_choice(int32_t product, int64_t m, int64_t n, int64_t k, int32_t groups,
+                                      int32_t num_cus, int32_t* out) {
+  const char* fn = "fg8_bf16_fused_tile_choice";
+  if (!out) return fail(FG8_EINVAL, "%s: out is NULL", fn);
+  if (product < 0 || product > 4 || m < 1 || n < 1 || k < 1 || m > kMaxRows || n > (product < 2 ? kMaxLd / 2 : kMaxLd) ||
+      k > kMaxLd || groups < 1 || groups > (product == 1 ? 1024 : 1) || num_cus < 1)
+    return fail(FG8_EINVAL, "%s: bad arguments (product=%d m=%lld n=%lld k=%lld groups=%d num_cus=%d)", fn,
+                (int)product, (long long)m, (long long)n, (long long)k, (int)groups, (int)num_cus);
+  const int64_t piece = loss_piece(m, n);
+  fg8::BfProblem p = product < 2    ? gated_bf16(m, n, k)
+                     : product == 2 ? loss_bf16(m, n, k, fg8::kKindLse)
+                     : product == 3 ? loss_bf16(m, piece, k, fg8::kKindDlogits)
+                                    : dense_bf16(m, k, piece, false, true);
+  if (product == 1) {
+    p.mode = fg8::kBfRowRuns;
+    p.groups = groups;
+  }
+  if (product == 4) p.parts = loss_dx_parts(m, k, piece, num_cus);
+  const fg8::BfTile t = fg8::bf16_tile(p, num_cus);
+  out[0] = t.bm; out[1] = t.bn; out[2] = t.splits; out[3] = t.persistent;
   return FG8_OK;
 }
 
