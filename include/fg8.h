@@ -545,8 +545,8 @@ fg8_status int4_dequantize(const uint8_t* q, const void* scales, int32_t scales_
  * group leaves FP32's range; larger ones may, and their row is then NaN, as an infinite
  * x makes it.
  * Any m is right, in pieces of 16 or 32 rows that read the weights each; it is made
- * for one to some dozens (beyond some hundreds, int4_dequantize and a BF16 product
- * are faster).
+ * for one to some dozens (beyond 500 to 900, int4_dequantize and a BF16 product are
+ * faster).
  */
 fg8_status gemm_bf16_int4(const uint16_t* x, int64_t ldx, const uint8_t* q, const void* scales,
                           int32_t scales_are_bf16, int32_t group, const void* bias,

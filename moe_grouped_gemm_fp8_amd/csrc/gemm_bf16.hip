@@ -43,7 +43,8 @@
 //   weights: few rows, where the time is that of reading them once.
 // A gated product runs at the rate of the plain one of 2 n columns (8192 x 4096 x
 // 7168: 312 us for 311, with z 323 for 311), and so do a head's logits with
-// their statistics (8192 x 128000 x 7168: 10.3 ms, 1450 TFLOP/s).
+// their statistics (8192 x 128000 x 7168: 10.3 to 10.9 ms, 1380 to
+// 1460 TFLOP/s).
 #include "bf16_tile.h"
 
 namespace fg8 {

@@ -8,8 +8,9 @@
 //   D[m][n] = sum over groups of s[group][n] * sum over its k of (code - 8) x[m][k]
 //
 // The product reads half a byte a weight and little else: HBM bounds it (1 x 16384 x
-// 16384 27 us, 5.1 TB/s of codes and scales), the launch and one round trip where
-// the weights are few (1 x 2112 x 7168 7 us), and with more rows the copies of x that
+// 16384 27 us, 5.1 TB/s of codes and scales), the launch and one round trip a
+// step where the weights are few (1 x 2112 x 7168, four steps, 7 us; 1 x 24576 x 1536,
+// two, 8.5 for 3.9 us of bytes), and with more rows the copies of x that
 // every workgroup makes (13 x 7168 x 16384 26 us, 2.9 TB/s: 24.9 without the
 // arithmetic, 16 without the copies; 512 rows over 32 experts, gated, 2 x 2048 x 7168
 // 116-124, 3.9 TB/s).
