@@ -291,11 +291,11 @@ def _workspace_of(nbytes, t, stream):
     """A workspace per (t's device, stream, calling thread) with its counters at
     zero, as (tensor, pointer, bytes); the kernels leave them so, and it is reused
     as is.  (Threads that share a stream may enqueue their calls' kernels in turn,
-    and a call of several keeps data here between them.)  One above WS_KEEP_BYTES goes back with the call.  A call recorded in a
-    graph gets one of its own, with its arrival counters cleared by the graph,
-    and leaves nothing here: a cached one may be replaced while the graph
-    lives, and one that a graph allocated belongs to the graph, whose clearing
-    has only been recorded."""
+    and a call of several keeps data here between them.)  One above WS_KEEP_BYTES
+    goes back with the call.  A call recorded in a graph gets one of its own, with
+    its arrival counters cleared by the graph, and leaves nothing here: a cached one
+    may be replaced while the graph lives, and one that a graph allocated belongs to
+    the graph, whose clearing has only been recorded."""
     if nbytes == 0:
         return None, None, 0
     if nbytes > WS_KEEP_BYTES or torch.cuda.is_current_stream_capturing():
